@@ -19,39 +19,35 @@
 #include <string>
 
 #include "gsr.h"
+#include "gsr_host.h"
 #include "gsr_params.h"
 
+using gsr::aligned16;
 using gsr::BK;
 using gsr::BM;
+using gsr::cdiv;
+using gsr::check_ksharded;
+using gsr::check_plan;
+using gsr::cuda_fail;
+using gsr::DeviceScope;
+using gsr::encode_fn;
+using gsr::EncodeTiledFn;
+using gsr::fail;
 using gsr::kMaxShards;
-
-struct gemm_shard_plan {
-  int device;
-  int sm_count;
-  int64_t max_M, max_N, max_K;
-  int max_R;
-  int opt_split;       // 0 = heuristic
-  int opt_block_n;     // 0 = heuristic
-  int opt_max_ctas;    // 0 = one per SM
-  int opt_raster_m;    // 0 = heuristic
-  int opt_raster_n;    // 0 = raster by m-tile groups
-  int opt_l2_hints;    // 0 = heuristic
-  int opt_cta_group;   // 0 = heuristic
-  int opt_schedule;    // 0 = heuristic, 1 = uniform, 2 = stream-K over the last one or two
-                       // waves, 3/4 = stream-K over a partial last wave (its range first /
-                       // last), 5 = split tail (GSR_OPT_SCHEDULE in gsr.h)
-  int opt_small;       // 0 = heuristic, 1 = never use the small-M kernel, 2 = always when it applies
-  int opt_small_rows;  // small-M kernel: W rows per tile (0 = heuristic)
-  int opt_small_kz;    // small-M kernel: k-blocks per copy (0 = heuristic)
-  int64_t l2_bytes;    // the device's L2 size
-  int pair_clusters;   // CTA pairs that can be resident at once
-  int quad_clusters;   // clusters of two CTA pairs that can be resident at once
-  uint64_t timeout_ns;
-};
+using gsr::log_config_enabled;
+using gsr::ok;
+using gsr::round256;
 
 namespace {
 
 thread_local std::string g_last_error;
+
+EncodeTiledFn g_encode = nullptr;
+std::once_flag g_encode_once;
+
+}  // namespace
+
+namespace gsr {
 
 gsr_status fail(gsr_status s, const char* fmt, ...) {
   char buf[512];
@@ -63,21 +59,9 @@ gsr_status fail(gsr_status s, const char* fmt, ...) {
   return s;
 }
 
-gsr_status ok() { return GSR_OK; }
-
 gsr_status cuda_fail(cudaError_t e, const char* what) {
   return fail(GSR_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point, so that the
-// library itself has no link-time dependency on the driver library.
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn g_encode = nullptr;
-std::once_flag g_encode_once;
 
 EncodeTiledFn encode_fn() {
   std::call_once(g_encode_once, [] {
@@ -90,6 +74,10 @@ EncodeTiledFn encode_fn() {
   });
   return g_encode;
 }
+
+}  // namespace gsr
+
+namespace {
 
 // cuStreamWriteValue32: a stream memory operation that writes a word without
 // running a kernel.
@@ -108,29 +96,6 @@ WriteValueFn write_value_fn() {
   });
   return g_write_value;
 }
-
-// Restores the caller's current device on scope exit.
-struct DeviceScope {
-  int prev = -1;
-  bool switched = false;
-  cudaError_t err = cudaSuccess;
-  explicit DeviceScope(int dev) {
-    err = cudaGetDevice(&prev);
-    if (err == cudaSuccess && prev != dev) {
-      err = cudaSetDevice(dev);
-      switched = (err == cudaSuccess);
-    }
-  }
-  ~DeviceScope() {
-    if (switched) cudaSetDevice(prev);
-  }
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Most output tiles any call under the plan can have: block_n = 128, and in AG
 // mode up to one extra partial m-tile per shard.
@@ -497,6 +462,10 @@ CUresult encode_kmajor(CUtensorMap* m, const void* ptr, int64_t rows, int64_t co
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+}  // namespace
+
+namespace gsr {
+
 // GSR_LOG_CONFIG (set and not "0"): every call that passes validation writes
 // its configuration to stderr, one line, before the launch. Read once.
 bool log_config_enabled() {
@@ -506,6 +475,10 @@ bool log_config_enabled() {
   }();
   return on;
 }
+
+}  // namespace gsr
+
+namespace {
 
 void log_config(const char* mode, int64_t M, int64_t N, int R, const Config& c) {
   if (!log_config_enabled()) return;
@@ -521,10 +494,18 @@ void log_config(const char* mode, int64_t M, int64_t N, int R, const Config& c) 
                (long long)c.sk_iters, c.ctas, c.ws_bytes);
 }
 
+}  // namespace
+
+namespace gsr {
+
 gsr_status check_plan(const gemm_shard_plan* P) {
   if (!P) return fail(GSR_ERR_INVALID_VALUE, "plan is NULL");
   return ok();
 }
+
+}  // namespace gsr
+
+namespace {
 
 gsr_status check_ws(const Config& c, const void* ws, size_t ws_bytes) {
   if (!ws) return fail(GSR_ERR_WORKSPACE, "workspace is NULL");
@@ -580,6 +561,10 @@ gsr_status launch(const gemm_shard_plan* P, const gsr::Params& p, const Config& 
   return ok();
 }
 
+}  // namespace
+
+namespace gsr {
+
 // Shared validation of the K-sharded (AR/RS) argument lists.
 gsr_status check_ksharded(const gemm_shard_plan* P, int64_t M, int64_t N, int R, const int64_t* K_r,
                           const void* const* X_r, const void* const* W_r) {
@@ -613,6 +598,10 @@ gsr_status check_ksharded(const gemm_shard_plan* P, int64_t M, int64_t N, int R,
                 (long long)K, (long long)P->max_K);
   return ok();
 }
+
+}  // namespace gsr
+
+namespace {
 
 gsr_status run_ksharded(const gemm_shard_plan* P, int mode, int64_t M, int64_t N, int R,
                         const int64_t* K_r, const void* const* X_r, const void* const* W_r,
