@@ -383,6 +383,130 @@ gsr_status gemm_shard_pack_gather(const gemm_shard_plan *plan, int R, const int6
                                   int64_t H, const void *const *S, int64_t rows_out, void *P,
                                   void *ws, size_t ws_bytes, gsr_stream_t stream);
 
+/* ------------------------------------------------------- routed projections
+ * Products whose weights the ROW picks: rows grouped by expert, and rows that
+ * carry a low-rank adapter beside a shared projection. (The pages this library
+ * restates have no counterpart; a tensor-parallel model runs these between the
+ * projections above, e.g. the experts between AG and AR.) Conventions as
+ * above, and:
+ *   - Routing data (ids, offsets, rows, positions, adapters) lives on the device
+ *     and is read there: no call waits for the host to see it. The host cannot
+ *     check it, so the kernels do: a value out of range never makes a read or
+ *     write out of bounds. What it gives instead is said at each call.
+ *   - Workspace: these calls share a workspace of their own, of
+ *     gemm_routed_workspace_size bytes, initialised once with
+ *     gemm_routed_workspace_init and left ready for the next call by every
+ *     call. gemm_shard_check_status reads its status word. gemm_group_route and
+ *     gemm_group_combine need none.
+ *   - Options: GSR_OPT_TIMEOUT_NS and GSR_OPT_MAX_CTAS apply; the others do not.
+ *   - Results are reproducible: sums run in an order that depends on the shapes
+ *     and the group sizes alone.
+ *   - Graphs: the calls may be recorded in a CUDA graph; a replay reads the
+ *     routing data's current contents.
+ */
+
+/* Limits of one call. */
+#define GSR_MAX_GROUPS 1024     /* E, experts                                  */
+#define GSR_MAX_TOPK 128        /* entries of one token                        */
+#define GSR_MAX_RANK 128        /* columns of an adapter                       */
+#define GSR_MAX_ADAPTERS 65536  /* L                                           */
+
+/* Bytes of workspace for every routed call under the plan; 0 for a NULL plan. */
+size_t gemm_routed_workspace_size(const gemm_shard_plan *plan);
+
+/* Zero its status word and counters (stream-ordered), once after allocating it
+ * and after a GSR_ERR_TIMEOUT. ws: 256-byte aligned, at least
+ * gemm_routed_workspace_size bytes. */
+gsr_status gemm_routed_workspace_init(const gemm_shard_plan *plan, void *ws, size_t ws_bytes,
+                                      gsr_stream_t stream);
+
+/*
+ * Route: group the entries of T tokens by expert, in a stable order.
+ *   ids       device, T x topk integers of id_bytes (4 or 8) bytes: entry i =
+ *             t * topk + j names the expert of token t's j-th entry. A value
+ *             outside 0..E-1 drops the entry.
+ *   offsets   device out, E + 1 int32: group e is the sorted rows
+ *             [offsets[e], offsets[e+1]); offsets[E] entries are kept
+ *   source    device out, T * topk int32: the token of each sorted row (i /
+ *             topk), -1 at and past offsets[E]
+ *   position  device out, T x topk int32: the sorted row of each entry, -1 for a
+ *             dropped one
+ * Within a group rows keep the entries' order. T * topk may not exceed the
+ * plan's max_M. T == 0 writes offsets (zeros) alone.
+ */
+gsr_status gemm_group_route(const gemm_shard_plan *plan, int64_t T, int topk, int E,
+                            const void *ids, int id_bytes, int32_t *offsets, int32_t *source,
+                            int32_t *position, gsr_stream_t stream);
+
+/*
+ * Grouped product: Y[i] = X[row(i)] . W[e]^T for the rows i of group e,
+ * offsets[e] <= i < offsets[e+1], row(i) = rows ? rows[i] : i.
+ *   E, M      groups (1..GSR_MAX_GROUPS) and rows of Y (<= max_M); M == 0 returns
+ *             GSR_OK with no launch
+ *   N, K      multiples of 8, <= max_N and max_K
+ *   offsets   device, E + 1 int32, non-decreasing; clamped to 0..M
+ *   T, X      X is T x K bf16; T >= M without `rows`
+ *   rows      device, M int32, or NULL; an index outside 0..T-1 reads as a row of
+ *             zeros
+ *   W         device, E x N x K bf16
+ *   Y         device, M x N bf16; rows of no group are not written
+ * Groups may have any size, 0 and M among them. The accumulation is fp32, the
+ * output rounded once. Only the weights of groups that have rows are read.
+ */
+gsr_status gemm_grouped(const gemm_shard_plan *plan, int E, int64_t M, int64_t N, int64_t K,
+                        const int32_t *offsets, int64_t T, const void *X, const int32_t *rows,
+                        const void *W, void *Y, void *ws, size_t ws_bytes, gsr_stream_t stream);
+
+/*
+ * Gated grouped product: Y[i] = silu(g) * u elementwise, with g and u the
+ * products of row(i) with the first and the last N rows of W[e]
+ * (W: E x 2N x K; silu(x) = x / (1 + exp(-x))). Both products, the activation
+ * and the product of the two stay in fp32; Y is rounded once. Otherwise as
+ * gemm_grouped.
+ */
+gsr_status gemm_grouped_gated(const gemm_shard_plan *plan, int E, int64_t M, int64_t N,
+                              int64_t K, const int32_t *offsets, int64_t T, const void *X,
+                              const int32_t *rows, const void *W, void *Y, void *ws,
+                              size_t ws_bytes, gsr_stream_t stream);
+
+/*
+ * Combine: Y[t] = base[t] + sum_j weights[t, j] * Z[position[t, j]].
+ *   H         columns (a multiple of 8, <= max_N)
+ *   Z         device, z_rows x H bf16
+ *   position  device, T x topk int32; an entry outside 0..z_rows-1 adds nothing,
+ *             whatever its weight holds
+ *   weights   device, T x topk fp32
+ *   base      device, T x H bf16, or NULL (0); may be Y
+ *   Y         device, T x H bf16
+ * fp32, j ascending after base, rounded once.
+ */
+gsr_status gemm_group_combine(const gemm_shard_plan *plan, int64_t T, int topk, int64_t H,
+                              int64_t z_rows, const void *Z, const int32_t *position,
+                              const float *weights, const void *base, void *Y,
+                              gsr_stream_t stream);
+
+/*
+ * AR with low-rank adapters: gemm_ar's sum plus each row's own adapter,
+ *     Y[m] = sum_r X_r[m] . W_r^T + scale[a] * (sum_r X_r[m] . A_r[a]^T) . B[a]^T,
+ * a = adapter[m].
+ *   L, rank   adapters (1..GSR_MAX_ADAPTERS) and their columns, a multiple of 8 up
+ *             to GSR_MAX_RANK (an adapter of a lower rank: zero rows of A_r)
+ *   A_r       host array of R device pointers, A_r[r] is L x rank x K_r bf16
+ *   B         device, L x N x rank bf16
+ *   adapter   device, M int32; a value outside 0..L-1 (e.g. -1): no adapter
+ *   scale     device, L fp32, or NULL (1)
+ * The low-rank rows (scale included) are rounded to bf16 between the two
+ * products; both products accumulate in fp32 in one accumulator with the base
+ * product, and Y is rounded once. Only adapters that some row names are read.
+ * M <= max_M; Y must not overlap an input. Other arguments as gemm_ar, with
+ * the routed workspace.
+ */
+gsr_status gemm_ar_lora(const gemm_shard_plan *plan, int64_t M, int64_t N, int R,
+                        const int64_t *K_r, const void *const *X_r, const void *const *W_r,
+                        int L, int rank, const void *const *A_r, const void *B,
+                        const int32_t *adapter, const float *scale, void *Y, void *ws,
+                        size_t ws_bytes, gsr_stream_t stream);
+
 /*
  * Synchronise `stream`, read the workspace status word, clear it and return
  * GSR_OK or GSR_ERR_TIMEOUT (the code of the first wait that ran out is

@@ -55,6 +55,8 @@ EXPORTED = (
     "gemm_ag", "gemm_shard_check_status", "gsr_last_error_string", "gemm_shard_describe",
     "gemm_ar_noalloc", "gemm_ag_flagged", "gemm_shard_signal", "gemm_ar_replicated",
     "gemm_shard_pack_gather", "gemm_ar_noalloc_check_status",
+    "gemm_routed_workspace_size", "gemm_routed_workspace_init", "gemm_group_route",
+    "gemm_grouped", "gemm_grouped_gated", "gemm_group_combine", "gemm_ar_lora",
 )
 
 
@@ -112,11 +114,21 @@ def load_library() -> ctypes.CDLL:
     lib.gemm_shard_pack_gather.argtypes = [vp, i32, i64_arr, i32, i64, ptr_arr, i64, vp, vp, sz, vp]
     lib.gemm_shard_check_status.argtypes = [vp, vp, vp]
     lib.gemm_ar_noalloc_check_status.argtypes = [vp, vp]
+    lib.gemm_routed_workspace_size.argtypes = [vp]
+    lib.gemm_routed_workspace_size.restype = sz
+    lib.gemm_routed_workspace_init.argtypes = [vp, vp, sz, vp]
+    lib.gemm_group_route.argtypes = [vp, i64, i32, i32, vp, i32, vp, vp, vp, vp]
+    lib.gemm_grouped.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    lib.gemm_grouped_gated.argtypes = lib.gemm_grouped.argtypes
+    lib.gemm_group_combine.argtypes = [vp, i64, i32, i64, i64, vp, vp, vp, vp, vp, vp]
+    lib.gemm_ar_lora.argtypes = [vp, i64, i64, i32, i64_arr, ptr_arr, ptr_arr, i32, i32, ptr_arr,
+                                 vp, vp, vp, vp, vp, sz, vp]
     lib.gsr_last_error_string.restype = ctypes.c_char_p
     lib.gemm_shard_describe.argtypes = [vp, i32, i64, i64, i64, i32, i64_arr,
                                         ctypes.POINTER(GsrConfig)]
     for name in EXPORTED:
-        if name not in ("gemm_shard_workspace_size", "gsr_last_error_string"):
+        if name not in ("gemm_shard_workspace_size", "gemm_routed_workspace_size",
+                        "gsr_last_error_string"):
             getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -490,3 +502,182 @@ def prepare_pack_gather(plan: Plan, S, rows_out, P, ws, stream=None) -> Prepared
     """gemm_shard_pack_gather on fixed buffers, validated and marshalled once."""
     args, keep = _pack_args(plan, S, rows_out, P, ws)
     return PreparedCall(load_library().gemm_shard_pack_gather, args, keep, stream)
+
+
+# ------------------------------------------------------------ routed projections
+
+def gemm_routed_workspace_size(plan: Plan) -> int:
+    return int(load_library().gemm_routed_workspace_size(plan.handle))
+
+
+def gemm_routed_workspace_alloc(plan: Plan) -> torch.Tensor:
+    """A workspace tensor of gemm_routed_workspace_size bytes (torch allocates it)."""
+    n = gemm_routed_workspace_size(plan)
+    return torch.empty(n, dtype=torch.uint8, device=f"cuda:{plan.device}")
+
+
+def gemm_routed_workspace_init(plan: Plan, ws: torch.Tensor, stream=None) -> None:
+    p, n = _ws(ws)
+    _check(load_library().gemm_routed_workspace_init(plan.handle, p, n, _stream(stream)))
+
+
+def _dense(t: torch.Tensor, name: str, dtype, shape=None, dim=None) -> None:
+    """A contiguous CUDA tensor of the dtype and, where given, shape (None: any size)."""
+    dim = dim if shape is None else len(shape)
+    ok = t.dtype is dtype and t.is_cuda and t.dim() == dim and t.is_contiguous()
+    if ok and shape is not None:
+        ok = all(want is None or want == have for want, have in zip(shape, t.shape))
+    if not ok:
+        size = f"{dim}-D" if shape is None else "x".join("?" if s is None else str(s) for s in shape)
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {size}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+
+
+def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
+    return ctypes.c_void_p(t.data_ptr() if t is not None and t.numel() else 0)
+
+
+def _route_args(plan, ids, E, offsets, source, position):
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be int32 or int64")
+    _dense(ids, "ids", ids.dtype, dim=2)
+    T, topk = ids.shape
+    _dense(offsets, "offsets", torch.int32, (int(E) + 1,))
+    _dense(source, "source", torch.int32, (T * topk,))
+    _dense(position, "position", torch.int32, (T, topk))
+    args = (plan.handle, T, topk, int(E), _ptr(ids), ids.element_size(), _ptr(offsets),
+            _ptr(source), _ptr(position))
+    return args, (ids, offsets, source, position)
+
+
+def gemm_group_route(plan: Plan, ids: torch.Tensor, E: int, offsets: torch.Tensor,
+                     source: torch.Tensor, position: torch.Tensor, stream=None):
+    """Group the entries of ids (T x topk, int32 or int64; outside 0..E-1: dropped) by expert.
+
+    Writes offsets (E + 1), source (T * topk: the token of each sorted row, -1
+    past the kept ones) and position (T x topk: the sorted row of each entry, -1
+    if dropped), all int32, and returns them."""
+    args, _ = _route_args(plan, ids, E, offsets, source, position)
+    _check(load_library().gemm_group_route(*args, _stream(stream)))
+    return offsets, source, position
+
+
+def prepare_group_route(plan: Plan, ids, E, offsets, source, position, stream=None) -> PreparedCall:
+    """gemm_group_route on fixed buffers, validated and marshalled once."""
+    args, keep = _route_args(plan, ids, E, offsets, source, position)
+    return PreparedCall(load_library().gemm_group_route, args, keep, stream)
+
+
+def _grouped_args(plan, X, W, offsets, Y, ws, rows, gated):
+    _bf16_2d(X, "X")
+    _dense(W, "W", _BF16, dim=3)
+    E, wide, K = W.shape
+    if gated and wide % 2:
+        raise ValueError("W must hold as many gate as up rows")
+    N = wide // 2 if gated else wide
+    _dense(Y, "Y", _BF16, (None, N))
+    M = Y.shape[0]
+    _dense(offsets, "offsets", torch.int32, (E + 1,))
+    if X.shape[1] != K or (rows is None and X.shape[0] < M):
+        raise ValueError(f"X must have K={K} columns" + ("" if rows is not None else f" and at least {M} rows"))
+    if rows is not None:
+        _dense(rows, "rows", torch.int32, (M,))
+    wsp, wsn = _ws(ws)
+    args = (plan.handle, E, M, N, K, _ptr(offsets), X.shape[0], _ptr(X), _ptr(rows), _ptr(W), _ptr(Y),
+            wsp, wsn)
+    return args, (X, W, offsets, Y, ws, rows)
+
+
+def gemm_grouped(plan: Plan, X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor,
+                 Y: torch.Tensor, ws: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Y[i] = X[i] @ W[e].T for offsets[e] <= i < offsets[e+1] (W: E x N x K); with
+    `rows`, X[rows[i]] in place of X[i]. Rows of no group are not written."""
+    args, _ = _grouped_args(plan, X, W, offsets, Y, ws, rows, False)
+    _check(load_library().gemm_grouped(*args, _stream(stream)))
+    return Y
+
+
+def prepare_grouped(plan: Plan, X, W, offsets, Y, ws, rows=None, stream=None) -> PreparedCall:
+    """gemm_grouped on fixed buffers, validated and marshalled once."""
+    args, keep = _grouped_args(plan, X, W, offsets, Y, ws, rows, False)
+    return PreparedCall(load_library().gemm_grouped, args, keep, stream)
+
+
+def gemm_grouped_gated(plan: Plan, X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor,
+                       Y: torch.Tensor, ws: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """Y[i] = silu(X[i] @ W[e, :N].T) * (X[i] @ W[e, N:].T) (W: E x 2N x K); otherwise
+    as gemm_grouped."""
+    args, _ = _grouped_args(plan, X, W, offsets, Y, ws, rows, True)
+    _check(load_library().gemm_grouped_gated(*args, _stream(stream)))
+    return Y
+
+
+def prepare_grouped_gated(plan: Plan, X, W, offsets, Y, ws, rows=None, stream=None) -> PreparedCall:
+    """gemm_grouped_gated on fixed buffers, validated and marshalled once."""
+    args, keep = _grouped_args(plan, X, W, offsets, Y, ws, rows, True)
+    return PreparedCall(load_library().gemm_grouped_gated, args, keep, stream)
+
+
+def _combine_args(plan, Z, position, weights, Y, base):
+    _bf16_2d(Z, "Z")
+    _dense(position, "position", torch.int32, dim=2)
+    T, topk = position.shape
+    _dense(weights, "weights", torch.float32, (T, topk))
+    _dense(Y, "Y", _BF16, (T, Z.shape[1]))
+    if base is not None:
+        _dense(base, "base", _BF16, (T, Z.shape[1]))
+    args = (plan.handle, T, topk, Z.shape[1], Z.shape[0], _ptr(Z), _ptr(position), _ptr(weights),
+            _ptr(base), _ptr(Y))
+    return args, (Z, position, weights, Y, base)
+
+
+def gemm_group_combine(plan: Plan, Z: torch.Tensor, position: torch.Tensor, weights: torch.Tensor,
+                       Y: torch.Tensor, base: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y[t] = base[t] + sum_j weights[t, j] * Z[position[t, j]] (position and weights:
+    T x topk, int32 and fp32; a position outside Z adds nothing)."""
+    args, _ = _combine_args(plan, Z, position, weights, Y, base)
+    _check(load_library().gemm_group_combine(*args, _stream(stream)))
+    return Y
+
+
+def prepare_group_combine(plan: Plan, Z, position, weights, Y, base=None, stream=None) -> PreparedCall:
+    """gemm_group_combine on fixed buffers, validated and marshalled once."""
+    args, keep = _combine_args(plan, Z, position, weights, Y, base)
+    return PreparedCall(load_library().gemm_group_combine, args, keep, stream)
+
+
+def _lora_args(plan, X_r, W_r, A_r, B, adapter, Y, ws, scale):
+    base, keep = _ar_args(plan, X_r, W_r, Y, ws)
+    M, N = Y.shape
+    if len(A_r) != len(X_r):
+        raise ValueError("A_r needs one tensor per shard")
+    _dense(B, "B", _BF16, (None, N, None))
+    L, _, rank = B.shape
+    for r, a in enumerate(A_r):
+        _dense(a, f"A_r[{r}]", _BF16, (L, rank, X_r[r].shape[1]))
+    _dense(adapter, "adapter", torch.int32, (M,))
+    if scale is not None:
+        _dense(scale, "scale", torch.float32, (L,))
+    ap, aa = _ptrs(A_r)
+    args = base[:7] + (L, rank, ap, _ptr(B), _ptr(adapter), _ptr(scale)) + base[7:]
+    return args, (keep, aa, A_r, B, adapter, scale)
+
+
+def gemm_ar_lora(plan: Plan, X_r: Sequence[torch.Tensor], W_r: Sequence[torch.Tensor],
+                 A_r: Sequence[torch.Tensor], B: torch.Tensor, adapter: torch.Tensor,
+                 Y: torch.Tensor, ws: torch.Tensor, scale: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """gemm_ar's sum plus each row's low-rank adapter a = adapter[m] (int32; outside
+    0..L-1: none): scale[a] * (sum_r X_r @ A_r[a].T) @ B[a].T (A_r: L x rank x K_r,
+    B: L x N x rank, scale: fp32 or None)."""
+    args, _ = _lora_args(plan, X_r, W_r, A_r, B, adapter, Y, ws, scale)
+    _check(load_library().gemm_ar_lora(*args, _stream(stream)))
+    return Y
+
+
+def prepare_ar_lora(plan: Plan, X_r, W_r, A_r, B, adapter, Y, ws, scale=None, stream=None) -> PreparedCall:
+    """gemm_ar_lora on fixed buffers, validated and marshalled once."""
+    args, keep = _lora_args(plan, X_r, W_r, A_r, B, adapter, Y, ws, scale)
+    return PreparedCall(load_library().gemm_ar_lora, args, keep, stream)

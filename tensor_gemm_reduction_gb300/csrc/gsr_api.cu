@@ -21,6 +21,7 @@
 #include "gsr.h"
 #include "gsr_host.h"
 #include "gsr_params.h"
+#include "gsr_routed.h"
 
 using gsr::aligned16;
 using gsr::BK;
@@ -746,6 +747,9 @@ gsr_status gemm_shard_plan_create(gemm_shard_plan** out, int device, int64_t max
     e = gsr::prepare_kernels(device, &pair_clusters, &quad_clusters);
     if (e == cudaSuccess) e = gsr::prepare_small_kernel();
     if (e == cudaSuccess) e = gsr::prepare_pack_kernel();
+    if (e == cudaSuccess) e = gsr::prepare_routed_kernels();
+    if (e == cudaSuccess) e = gsr::prepare_lowrank_kernels();
+    if (e == cudaSuccess) e = gsr::prepare_route_kernels();
     if (e != cudaSuccess) return cuda_fail(e, "configuring the kernels");
   }
   *out = new_plan(device, prop.multiProcessorCount, max_M, max_N, max_K, max_R);

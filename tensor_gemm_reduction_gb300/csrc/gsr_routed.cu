@@ -1,0 +1,979 @@
+// gsr_routed.cu -- products whose weights the row picks, for GB300 (sm_103a).
+//
+//   kGrouped  Y[i] = X[i] . W[e]^T          for the rows i of group e
+//   kGated    Y[i] = silu(g) * u, g = X[i] . Wg[e]^T, u = X[i] . Wu[e]^T
+//   kLora     Y[i] = sum_r X_r[i] . W_r^T + low[i] . B[a]^T, a = adapter[i]
+//
+// The groups' sizes are known on the device only, from none to every row. So
+// the weights' rows, not the tokens, are the MMA's M: a CTA pair owns a tile of
+// 256 weight rows (tcgen05.mma.cta_group::2, 128 rows per CTA) against n
+// tokens of one group, n any multiple of 16 up to the instance's capacity, as
+// the MMA's N. A group of one row costs 16 columns of an MMA and not 128, and
+// with few rows the kernel is a stream of weights; with many it is a 256 x 256
+// tile. A group's tokens are cut into tiles of equal width.
+//
+// Every CTA counts the tiles itself from the offsets (a scan over the groups in
+// shared memory). Whole waves of tiles are dealt round-robin; the k-range of
+// the remaining ones is cut into equal contiguous ranges (stream-K), walked
+// first, whose fp32 partials the last piece to arrive sums in k order. The
+// cuts depend on the group sizes alone, so results are reproducible.
+//
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (the pair's leader), warps 2..5
+// epilogue; kLora has warps 6..9 besides, which place the low-rank rows: the
+// adapters of a token tile are more steps over k, in which the weights are
+// B[a] and a token's row is low[i] if its adapter is a and zero if not, so the
+// sum stays in the same fp32 accumulator. Those masked rows exist in shared
+// memory alone.
+//
+// Epilogue: a thread holds one output column of 32 tokens; neighbouring lanes
+// exchange halves so that each store writes two columns of one row (64-byte
+// segments per row and warp).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gsr_device.cuh"
+#include "gsr_routed.h"
+
+namespace gsr {
+namespace {
+
+constexpr int kEpi = 128;              // epilogue threads
+constexpr int kPlacers = 4;            // kLora: warps that place low-rank rows
+constexpr uint32_t kRolePlacer = 4;
+// kLora: tiles in flight between the placing warps and the epilogue, at most: a
+// ring of single-stage tiles and two accumulators.
+constexpr int kMarks = 8;
+
+// Called by the lanes that issue (no election inside).
+__device__ __forceinline__ void copy_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                        int y, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(pol)
+      : "memory");
+}
+__device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                        int y, int z, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(pol)
+      : "memory");
+}
+// Four rows of a matrix, one below the other.
+__device__ __forceinline__ void copy_rows4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                           int4 r, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z),
+      "r"(r.w), "l"(pol)
+      : "memory");
+}
+__device__ __forceinline__ void arm(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------------ geometry
+
+template <int KIND_, bool GATHER_, int TOK_, int STAGES_>
+struct Cfg {
+  static constexpr int KIND = KIND_, TOK = TOK_, S = STAGES_, KZ = kRoutedKblocks;
+  static constexpr bool GATHER = GATHER_;
+  static constexpr int kThreads = KIND == kLora ? 64 + kEpi + 32 * kPlacers : 64 + kEpi;
+  static constexpr uint32_t kW = 128 * 128;             // a k-block of this CTA's weight rows
+  static constexpr uint32_t kX = TOK / 2 * 128;         // a k-block of this CTA's tokens
+  static constexpr uint32_t kStage = KZ * (kW + kX);
+  static constexpr uint32_t kRing = S * kStage;
+  // full[S], empty[S], tmem_full[2], tmem_empty[2], drain; kLora: adapter[S]
+  static constexpr uint32_t kBars = (2 * S + 5 + (KIND == kLora ? S : 0)) * 8;
+  static constexpr uint32_t kAdapterBarOff = (2 * S + 5) * 8;
+  static constexpr uint32_t kGroups = KIND == kLora ? 0 : 4 * (3 * kMaxGroups + 1 + 32);
+  static constexpr uint32_t kSwap = KIND == kGated ? 2 * 2 * 16 * 32 * 4 : 0;
+  static constexpr uint32_t kBarsOff = kRing;
+  static constexpr uint32_t kMiscOff = kBarsOff + kBars;
+  static constexpr uint32_t kSwapOff = (kMiscOff + 16 + 4 * kMarks + 127) / 128 * 128;
+  static constexpr uint32_t kGroupsOff = kSwapOff + kSwap;
+  static constexpr uint32_t kSmem = 1024 + kGroupsOff + kGroups;
+  static_assert(kSmem <= kSmallSmemLimit, "shared memory");
+  static_assert(kX % 1024 == 0, "swizzle atoms");
+  static constexpr int kColsPerCta = KIND == kGated ? 64 : 128;   // output columns
+  static constexpr uint32_t kTmemCols = 2 * TOK;
+};
+
+// The groups as every CTA counts them (shared memory).
+struct Groups {
+  int *row, *count, *tile;    // first row, rows, first token tile (E + 1)
+};
+
+struct Tile {
+  int row0, rows, n;          // first row of Y, rows, MMA columns (a multiple of 16)
+  int col0;                   // first output column of the pair
+  int group, m;               // group; lora: token tile
+  int piece, npieces, slot, cut;    // cut: index among the cut tiles
+  int st, st_end;             // stages
+};
+
+template <class C>
+__device__ __forceinline__ void place(const RoutedParams& p, const Groups& g, int id, Tile& t) {
+  int local, mt, width, count;
+  if constexpr (C::KIND == kLora) {
+    local = id;
+    mt = p.m_tiles;
+    width = p.tile_tokens;
+    count = p.M;
+    t.row0 = 0;
+    t.group = 0;
+  } else {
+    // The last group whose first token tile is at or below this one (empty
+    // groups share their successor's).
+    const int key = id / p.n_tiles;
+    int lo = 0, hi = p.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (g.tile[mid] <= key) lo = mid; else hi = mid;
+    }
+    t.group = lo;
+    mt = g.tile[lo + 1] - g.tile[lo];
+    local = id - g.tile[lo] * p.n_tiles;
+    count = g.count[lo];
+    t.row0 = g.row[lo];
+    width = ((count + mt - 1) / mt + 15) & ~15;
+  }
+  // Raster: 16 token tiles at a time, tokens fastest, so that concurrent pairs
+  // share weight rows.
+  const int span = 16 * p.n_tiles;
+  const int sup = local / span;
+  const int gm = min(mt - sup * 16, 16);
+  const int in = local - sup * span;
+  t.m = sup * 16 + in % gm;
+  t.col0 = in / gm * (2 * C::kColsPerCta);
+  t.row0 += t.m * width;
+  t.rows = min(width, count - t.m * width);
+  t.n = C::KIND == kLora ? width : (t.rows + 15) & ~15;
+}
+
+// Every role walks the same tiles: this worker's range of the cut tiles, then
+// its whole tiles.
+struct Walk {
+  int w, G, Gc, next, whole, S;
+  uint32_t it, it_end, iters;
+
+  __device__ __forceinline__ void begin(const RoutedParams& p, int tiles) {
+    w = static_cast<int>(blockIdx.x) >> 1;
+    G = static_cast<int>(gridDim.x) >> 1;
+    S = p.stages_per_tile;
+    const int rem = tiles % G;
+    whole = tiles - rem;
+    next = w;
+    Gc = rem;
+    if (rem > 0 && rem < p.whole_from && p.max_pieces > 1) {
+      const int most = static_cast<int>(min(static_cast<long long>(rem) * p.max_pieces,
+                                            static_cast<long long>(rem) * S / p.min_piece));
+      Gc = max(rem, min(G, most));
+    }
+    iters = static_cast<uint32_t>(rem) * static_cast<uint32_t>(S);
+    it = it_end = 0;
+    if (w < Gc) {
+      if (Gc == rem) {
+        it = static_cast<uint32_t>(w) * S;
+        it_end = it + S;
+      } else {
+        it = static_cast<uint32_t>(w) * iters / Gc;
+        it_end = static_cast<uint32_t>(w + 1) * iters / Gc;
+      }
+    }
+  }
+  __device__ __forceinline__ int worker_of(uint32_t i) const {
+    return static_cast<int>(((i + 1) * Gc + iters - 1) / iters) - 1;
+  }
+
+  template <class C>
+  __device__ __forceinline__ bool step(const RoutedParams& p, const Groups& g, Tile& t) {
+    int id;
+    if (it < it_end) {
+      const uint32_t cut = it / S, lo = it - cut * S;
+      const uint32_t hi = min(static_cast<uint32_t>(S), lo + (it_end - it));
+      it += hi - lo;
+      id = whole + static_cast<int>(cut);
+      t.cut = static_cast<int>(cut);
+      t.st = static_cast<int>(lo);
+      t.st_end = static_cast<int>(hi);
+      t.piece = 0;
+      t.npieces = 1;
+      t.slot = 0;
+      if (Gc > static_cast<int>(iters / S)) {
+        const int first = worker_of(cut * S), last = worker_of((cut + 1) * S - 1);
+        t.piece = w - first;
+        t.npieces = last - first + 1;
+        t.slot = t.cut + first;   // tile + worker numbers the pieces without collision
+      }
+    } else {
+      if (next >= whole) return false;
+      id = next;
+      next += G;
+      t.cut = 0;
+      t.st = 0;
+      t.st_end = S;
+      t.piece = 0;
+      t.npieces = 1;
+      t.slot = 0;
+    }
+    place<C>(p, g, id, t);
+    return true;
+  }
+};
+
+// The groups' rows clamped to the matrix, and the prefix of their token tiles:
+// each thread scans a run of groups, warps and then the block add up. Called by
+// all threads of the block.
+template <class C>
+__device__ int count_groups(const RoutedParams& p, const Groups& g, int* sums) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = C::kThreads / 32;
+  const int per = (p.E + C::kThreads - 1) / C::kThreads;
+  const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int lo = min(max(p.offsets[e], 0), p.M), hi = min(max(p.offsets[e + 1], 0), p.M);
+    const int count = max(hi - lo, 0);
+    g.row[e] = lo;
+    g.count[e] = count;
+    mine += (count + C::TOK - 1) / C::TOK;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int at = incl - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) at += sums[i];
+    total += sums[i];
+  }
+  for (int e = e0; e < e1; ++e) {
+    g.tile[e] = at;
+    at += (g.count[e] + C::TOK - 1) / C::TOK;
+  }
+  if (tid == 0) g.tile[p.E] = total;
+  __syncthreads();
+  return total;
+}
+
+// ------------------------------------------------------------ adapters of a tile
+
+// The steps over the adapters of token tile m that belong to piece `piece`: each
+// piece of a cut tile takes an equal share. Read by whole warps, after the
+// low-rank kernel has completed.
+struct AdapterSteps {
+  const int32_t* ids;
+  int units, st, st_end, per_stage;
+  template <class C>
+  __device__ __forceinline__ void begin(const RoutedParams& p, const Tile& t) {
+    const int32_t* list = p.lists + static_cast<size_t>(t.m) * kAdapterListStride;
+    ids = list + 1;
+    units = __ldcg(list) * p.units_per_adapter;
+    per_stage = C::KZ * 64 / p.unit_cols;
+    const int stages = (units + per_stage - 1) / per_stage;
+    st = t.piece * stages / t.npieces;
+    st_end = (t.piece + 1) * stages / t.npieces;
+  }
+  __device__ __forceinline__ int units_in(int s) const { return min(per_stage, units - s * per_stage); }
+};
+
+// Matrix descriptor of rows of `cols` bf16 (16, 32 or 64), swizzled over 32, 64
+// or 128 bytes: 8-row groups 16 * cols bytes apart.
+__device__ __forceinline__ uint64_t unit_desc(uint32_t saddr, int cols) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(cols) << 32;               // 16 * cols >> 4
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(cols == 64 ? 2 : cols == 32 ? 4 : 6) << 61;
+  return d;
+}
+
+// ------------------------------------------------------------ roles
+
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  template <int S>
+  __device__ __forceinline__ void next() {
+    if (++slot == S) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+template <class C>
+__device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
+                        uint32_t rank, const Ctl& ctl) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::S;
+  const uint32_t lead0 = map_shared_to_rank(full0, 0);
+  const uint64_t pol_w = make_l2_policy(p.policy_w), pol_x = make_l2_policy(p.policy_x);
+  int begins = 0;
+  if constexpr (C::KIND == kLora) begins = p.shard_st_begin[lane <= kMaxShards ? lane : kMaxShards];
+  Ring ring;
+  uint32_t issued = 0;
+  bool ok = true, waited = C::KIND != kLora;
+  Walk walk;
+  walk.begin(p, tiles);
+  Tile t;
+  while (ok && walk.step<C>(p, g, t)) {
+    const int half = t.n / 2;
+    const int w_row = t.col0 + static_cast<int>(rank) * C::kColsPerCta;
+    const int x_row = t.row0 + static_cast<int>(rank) * half;
+    const uint32_t bytes = 2 * C::KZ * (C::kW + static_cast<uint32_t>(half) * 128);
+    int4 four = make_int4(0, 0, 0, 0);
+    if constexpr (C::GATHER) {
+      // This lane's four rows; past the tile's rows its last one again (never
+      // stored), and an index outside X as the row past X, which reads as zeros.
+      const int last = t.row0 + t.rows - 1, at = x_row + 4 * lane;
+      auto row = [&](int i) {
+        const int r = 4 * lane < half ? p.rows[min(i, last)] : 0;
+        return r >= 0 && r < p.T ? r : p.T;
+      };
+      four = make_int4(row(at), row(at + 1), row(at + 2), row(at + 3));
+    }
+    int shard = 0, shard_begin = 0, shard_end = 0;
+    if constexpr (C::KIND == kLora) {
+      shard_end = __shfl_sync(0xffffffffu, begins, 1);
+      while (shard_end <= t.st) shard_end = __shfl_sync(0xffffffffu, begins, ++shard + 1);
+      shard_begin = __shfl_sync(0xffffffffu, begins, shard);
+    }
+    for (int st = t.st; st < t.st_end; ++st) {
+      ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRoleProducer << 8) | 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t lead = lead0 + 8 * ring.slot;
+      const uint32_t sw = base + ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
+      if constexpr (C::KIND == kLora) {
+        while (shard_end <= st) {
+          shard_begin = shard_end;
+          shard_end = __shfl_sync(0xffffffffu, begins, ++shard + 1);
+        }
+      }
+      const int kx = (st - shard_begin) * (C::KZ * BK);
+      if (lane == 0) {
+        if (rank == 0) arm(full0 + 8 * ring.slot, bytes);
+#pragma unroll
+        for (int j = 0; j < C::KZ; ++j) {
+          const uint32_t dw = sw + j * C::kW;
+          if constexpr (C::KIND == kLora) {
+            copy_2d(dw, &p.tmap_w[shard], lead, kx + j * BK, w_row, pol_w);
+            copy_2d(sx + j * C::kX, &p.tmap_x[shard], lead, kx + j * BK, x_row, pol_x);
+          } else {
+            copy_3d(dw, &p.tmap_w[0], lead, kx + j * BK, w_row, t.group, pol_w);
+            if constexpr (C::KIND == kGated)
+              copy_3d(dw + C::kW / 2, &p.tmap_w[0], lead, kx + j * BK, p.N + w_row, t.group, pol_w);
+            if constexpr (!C::GATHER) {
+              // half rows (a multiple of 8) as boxes of 128, 64, 32, 16 and 8 rows
+              int r = 0;
+#pragma unroll
+              for (int b = 0; b < 5; ++b) {
+                const int box = 128 >> b;
+                if (half & box) {
+                  copy_2d(sx + j * C::kX + r * 128, &p.tmap_x[b], lead, kx + j * BK, x_row + r, pol_x);
+                  r += box;
+                }
+              }
+            }
+          }
+        }
+      }
+      if constexpr (C::GATHER) {
+        __syncwarp();
+        if (4 * lane < half) {
+#pragma unroll
+          for (int j = 0; j < C::KZ; ++j)
+            copy_rows4(sx + j * C::kX + lane * 512, &p.tmap_x[0], lead, kx + j * BK, four, pol_x);
+        }
+        __syncwarp();
+      }
+      ++issued;
+      ring.next<C::S>();
+    }
+    if constexpr (C::KIND == kLora) {
+      if (!ok) break;
+      if (!waited) {
+        grid_dependency_wait();
+        waited = true;
+      }
+      AdapterSteps a{};
+      a.template begin<C>(p, t);
+      const uint32_t unit_w = 256u * p.unit_cols;
+      for (int st = a.st; st < a.st_end; ++st) {
+        ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRoleProducer << 8) | 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int units = a.units_in(st), u0 = st * a.per_stage;
+        const uint32_t landed = full0 + C::kAdapterBarOff + 8 * ring.slot;
+        if (lane == 0) {
+          arm(landed, unit_w * units);
+          if (rank == 0) mbar_arrive(full0 + 8 * ring.slot);
+        }
+        __syncwarp();
+        // One lane per unit (at most 8): its adapter's columns of B. They complete
+        // on this CTA's own barrier: the placing warps look them over first.
+        if (lane < units) {
+          const int u = u0 + lane, i = u / p.units_per_adapter;
+          copy_3d(base + ring.slot * C::kStage + lane * unit_w, &p.tmap_b, landed,
+                  (u - i * p.units_per_adapter) * p.unit_cols, w_row, __ldcg(a.ids + i), pol_w);
+        }
+        __syncwarp();
+        ++issued;
+        ring.next<C::S>();
+      }
+    }
+  }
+  if (!ok) {
+    // Let the copies already issued land before the shared memory goes away:
+    // they complete on the leader's barriers, whose MMAs free the slots.
+    const uint32_t first = issued > C::S ? issued - C::S : 0;
+    for (uint32_t i = first; i < issued; ++i) {
+      if (rank == 0)
+        wait_drain(full0 + 8 * (i % C::S), (i / C::S) & 1u, 100000000ull);
+      else
+        wait_drain(empty0 + 8 * (i % C::S), (i / C::S) & 1u, 100000000ull);
+    }
+    // Adapter copies complete on barriers that only the placing warps follow.
+    if constexpr (C::KIND == kLora) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
+    }
+  }
+}
+
+// The pair's MMAs (rank 0).
+template <class C>
+__device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
+                         uint32_t tmem, const Ctl& ctl) {
+  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::S;
+  const uint32_t tfull0 = empty0 + 8 * C::S, tempty0 = tfull0 + 16, drain = tempty0 + 16;
+  Ring ring;
+  uint32_t local = 0;
+  bool ok = true, issued = false, waited = C::KIND != kLora;
+  Walk walk;
+  walk.begin(p, tiles);
+  Tile t, tn;
+  bool have = walk.step<C>(p, g, t);
+  for (; ok && have; ++local) {
+    const uint32_t acc = local & 1u;
+    ok = wait_bounded(tempty0 + 8 * acc, ((local >> 1) & 1u) ^ 1u, ctl, (kRoleMma << 8) | 1);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    tc_fence_after_sync();
+    const uint32_t d = tmem + acc * C::TOK;
+    const uint32_t idesc = make_idesc(256, static_cast<uint32_t>(t.n));
+    bool looked = false, have_next = false;
+    for (int st = t.st; st < t.st_end; ++st) {
+      ok = wait_bounded(full0 + 8 * ring.slot, ring.phase, ctl, (kRoleMma << 8) | 2);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t sw = base + ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
+#pragma unroll
+      for (int j = 0; j < C::KZ; ++j)
+        mma4_bf16_pair(d, smem_desc_sw128(sw + j * C::kW), smem_desc_sw128(sx + j * C::kX), idesc,
+                       (st > t.st || j > 0) ? 1u : 0u);
+      issued = true;
+      mma_commit_pair(empty0 + 8 * ring.slot, 0x3);
+      ring.next<C::S>();
+      if (!looked) {   // place the next tile while this one's first stage runs
+        have_next = walk.step<C>(p, g, tn);
+        looked = true;
+      }
+    }
+    if constexpr (C::KIND == kLora) {
+      if (!ok) break;
+      if (!waited) {
+        grid_dependency_wait();
+        waited = true;
+      }
+      AdapterSteps a{};
+      a.template begin<C>(p, t);
+      const int cols = p.unit_cols;
+      const uint32_t unit_w = 256u * cols, unit_x = static_cast<uint32_t>(C::TOK) * cols;
+      for (int st = a.st; st < a.st_end; ++st) {
+        ok = wait_bounded(full0 + 8 * ring.slot, ring.phase, ctl, (kRoleMma << 8) | 2);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t sw = base + ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
+        const int units = a.units_in(st);
+        for (int u = 0; u < units; ++u) {
+          const uint64_t dw = unit_desc(sw + u * unit_w, cols), dx = unit_desc(sx + u * unit_x, cols);
+          for (int k = 0; k < cols / 16; ++k) mma_bf16_ss_pair(d, dw + 2 * k, dx + 2 * k, idesc, 1u);
+        }
+        issued = true;
+        mma_commit_pair(empty0 + 8 * ring.slot, 0x3);
+        ring.next<C::S>();
+      }
+    }
+    if (!ok) break;
+    mma_commit_pair(tfull0 + 8 * acc, 0x3);
+    if (!looked) have_next = walk.step<C>(p, g, tn);
+    t = tn;
+    have = have_next;
+  }
+  if (!ok && issued) {
+    mma_commit_pair(drain, 0x1);
+    wait_drain(drain, 0, 100000000ull);
+  }
+}
+
+// The low-rank rows of the ring's adapter stages: warp `pw` of 4 places rows pw *
+// 32 .. + 32 of this CTA's tokens, one per lane, and signs every stage on the
+// leader's full barrier (also those without rows to place, which keeps it in
+// step with the ring).
+template <class C>
+__device__ void place_rows(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
+                           uint32_t rank, volatile int* marks, const Ctl& ctl) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const int i = static_cast<int>(threadIdx.x) - 64 - kEpi;   // row of this CTA's tokens
+  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::S;
+  const uint32_t lead0 = map_shared_to_rank(full0, 0);
+  Ring ring;
+  bool ok = true, waited = false;
+  uint32_t landed_phase = 0, local = 0;   // bit s: phase of slot s's adapter barrier
+  Walk walk;
+  walk.begin(p, tiles);
+  Tile t;
+  for (; ok && walk.step<C>(p, g, t); ++local) {
+    for (int st = t.st; st < t.st_end; ++st) {
+      ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRolePlacer << 8) | 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_cluster(lead0 + 8 * ring.slot);
+      ring.next<C::S>();
+    }
+    if (!ok) break;
+    if (!waited) {
+      grid_dependency_wait();
+      waited = true;
+    }
+    AdapterSteps a{};
+    a.template begin<C>(p, t);
+    if (a.st >= a.st_end) continue;
+    const int half = t.n / 2, m = t.row0 + static_cast<int>(rank) * half + i;
+    const bool mine = i < half;
+    int id = -1;
+    uint4 v[kMaxRank / 8];
+    if (mine && m < p.M) id = p.adapter[m];
+    const bool live = id >= 0 && id < p.L;
+#pragma unroll
+    for (int c = 0; c < kMaxRank / 8; ++c)
+      v[c] = live && 8 * c < p.rank_pad
+                 ? __ldcg(reinterpret_cast<const uint4*>(p.low + static_cast<size_t>(m) * p.rank_pad) + c)
+                 : make_uint4(0, 0, 0, 0);
+    const int cols = p.unit_cols;
+    const uint32_t unit_x = static_cast<uint32_t>(C::TOK) * cols;
+    const uint32_t mask = cols == 64 ? 7u : cols == 32 ? 3u : 1u;
+    const uint32_t row_off = static_cast<uint32_t>(i) * cols * 2;
+    for (int st = a.st; st < a.st_end; ++st) {
+      ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRolePlacer << 8) | 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t sx = base + ring.slot * C::kStage + C::KZ * C::kW;
+      const int units = a.units_in(st), u0 = st * a.per_stage;
+      // The stage's adapters in the warp's lanes.
+      const int at = (u0 + (lane < units ? lane : 0)) / p.units_per_adapter;
+      const int ids = __ldcg(a.ids + at);
+      for (int u = 0; u < units; ++u) {
+        const int adapter = __shfl_sync(0xffffffffu, ids, u);
+        const bool hit = live && adapter == id;
+        const bool upper = p.units_per_adapter == 2 && ((u0 + u) & 1);   // columns 64..127
+        if (mine) {
+          const uint32_t dst = sx + u * unit_x;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (8 * c < cols) {
+              const uint4 w = upper ? v[8 + c] : v[c];
+              uint32_t off = row_off + 16u * c;
+              off ^= ((off >> 7) & mask) << 4;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + off),
+                           "r"(hit ? w.x : 0u), "r"(hit ? w.y : 0u), "r"(hit ? w.z : 0u),
+                           "r"(hit ? w.w : 0u)
+                           : "memory");
+            }
+          }
+        }
+      }
+      // A masked row times an infinite or NaN weight would be NaN: an adapter's
+      // weights that are not finite become 0 here, and the epilogue adds their
+      // products to the rows that have the adapter.
+      ok = wait_bounded(full0 + C::kAdapterBarOff + 8 * ring.slot, (landed_phase >> ring.slot) & 1u, ctl,
+                        (kRolePlacer << 8) | 2);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      landed_phase ^= 1u << ring.slot;
+      const uint32_t sw = base + ring.slot * C::kStage, bytes = 256u * cols * units;
+      bool marked = false;
+      for (uint32_t at = 16u * i; at < bytes; at += 16u * 32 * kPlacers) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(sw + at)
+                     : "memory");
+        uint32_t odd[4], any = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          odd[j] = ((w[j] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;   // exponent all ones
+          any |= odd[j];
+        }
+        if (any) {
+          marked = true;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] &= ~((odd[j] >> 15) * 0xffffu);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sw + at), "r"(w[0]), "r"(w[1]),
+                       "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+      }
+      if (marked) marks[local % kMarks] = 1;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead0 + 8 * ring.slot);
+      ring.next<C::S>();
+    }
+  }
+}
+
+// The products of adapter weights that are not finite, which the placing warps
+// took out of the tile: column `col` of 32 tokens from token 32 * c on, for the
+// adapters of this piece.
+template <class C>
+__device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t, int c, int col,
+                                           float (&v)[32]) {
+  AdapterSteps a{};
+  a.template begin<C>(p, t);
+  const int u0 = a.st * a.per_stage, u1 = min(a.st_end * a.per_stage, a.units);
+  if (col >= p.N) return;
+#pragma unroll 1
+  for (int j = 0; j < 32; ++j) {
+    const int m = t.row0 + 32 * c + j;
+    if (32 * c + j >= t.rows) break;
+    const int id = p.adapter[m];
+    if (id < 0 || id >= p.L) continue;
+    int at = 0;
+    while (__ldcg(a.ids + at) != id) ++at;   // the tile's list has every row's adapter
+    float sum = 0.f;
+    bool any = false;
+    for (int k = 0; k < p.rank; ++k) {
+      const int u = at * p.units_per_adapter + k / p.unit_cols;
+      if (u < u0 || u >= u1) continue;
+      const uint32_t w = p.b[(static_cast<size_t>(id) * p.N + col) * p.rank + k];
+      if ((w & 0x7f80u) != 0x7f80u) continue;
+      const uint32_t x = __ldcg(p.low + static_cast<size_t>(m) * p.rank_pad + k);
+      sum += __uint_as_float(w << 16) * __uint_as_float(x << 16);
+      any = true;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (any && i == j) v[i] += sum;
+  }
+}
+
+// Stores two columns (this lane's and its neighbour's) of the chunk's tokens:
+// v[j] is token j, this lane's column. COUNT tokens, the first at `row`.
+template <int COUNT>
+__device__ __forceinline__ void store_tokens(uint16_t* y, int N, int row, int valid, int col,
+                                             const float* v) {
+  const bool odd = threadIdx.x & 1;
+  uint16_t* at = y + static_cast<size_t>(row) * N + (col & ~1);
+#pragma unroll
+  for (int j = 0; j < COUNT; j += 2) {
+    const uint32_t own = pack_bf16x2(__float_as_uint(v[j]), __float_as_uint(v[j + 1]));
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+    const uint32_t out = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+    const int token = j + (odd ? 1 : 0);
+    if (token < valid && col < N)
+      *reinterpret_cast<uint32_t*>(at + static_cast<size_t>(token) * N) = out;
+  }
+}
+
+template <class C>
+__device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
+                       uint8_t* base_ptr, uint32_t tmem, uint32_t rank, volatile int* last_flag,
+                       volatile int* marks, const Ctl& ctl) {
+  const uint32_t tfull0 = base + C::kBarsOff + 16 * C::S, tempty0 = tfull0 + 16;
+  const int et = static_cast<int>(threadIdx.x) - 64;
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const int quad = (static_cast<int>(threadIdx.x) >> 5) & 3;   // TMEM lanes this warp may read
+  const int wrow = quad * 32 + lane;                            // weight row of this CTA
+  const uint32_t lead_tempty = map_shared_to_rank(tempty0, 0);
+  float* swap = reinterpret_cast<float*>(base_ptr + C::kSwapOff);
+  uint32_t local = 0;
+  Walk walk;
+  walk.begin(p, tiles);
+  Tile t;
+  for (; walk.step<C>(p, g, t); ++local) {
+    const uint32_t acc = local & 1u;
+    const bool ok = wait_bounded(tfull0 + 8 * acc, (local >> 1) & 1u, ctl, (kRoleEpilogue << 8) | 1);
+    if (!epilogue_bar_and(ok)) break;
+    tc_fence_after_sync();
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::TOK;
+    const int chunks = (t.rows + 31) >> 5;
+    const int col0 = t.col0 + static_cast<int>(rank) * C::kColsPerCta;
+    bool marked = false;
+    if constexpr (C::KIND == kLora) {
+      marked = marks[local % kMarks] != 0;
+      epilogue_bar_sync();
+      if (marked && et == 0) marks[local % kMarks] = 0;
+    }
+
+    // 32 columns of the accumulator, fp32.
+    auto load = [&](int c, float (&v)[32]) {
+      uint32_t r[32];
+      tmem_ld_32cols(taddr + 32 * c, r);
+      tmem_ld_wait(r);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+      if constexpr (C::KIND == kLora) {
+        if (marked) add_unbounded<C>(p, t, c, col0 + wrow, v);
+      }
+    };
+    auto release = [&]() {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead_tempty + 8 * acc);
+    };
+    // 32 tokens of the tile from token 32 * c on: this lane's column.
+    auto emit = [&](int c, const float (&v)[32]) {
+      const int row = t.row0 + 32 * c, valid = t.rows - 32 * c;
+      if constexpr (C::KIND != kGated) {
+        store_tokens<32>(p.y, p.N, row, valid, col0 + wrow, v);
+      } else {
+        // Quads 0 and 1 hold the gates, 2 and 3 the ups, of the same columns.
+        // Each pair of warps swaps halves: the gate's warp finishes tokens
+        // 0..15, the up's warp 16..31.
+        const int pair = quad & 1, up = quad >> 1;
+        float* buf = swap + pair * (2 * 16 * 32);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) buf[up * 512 + j * 32 + lane] = up ? v[j] : v[16 + j];
+        named_sync(2 + pair, 64);
+        float out[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float other = buf[(1 - up) * 512 + j * 32 + lane];
+          const float gate = up ? other : v[j], mul = up ? v[16 + j] : other;
+          out[j] = gate / (1.f + __expf(-gate)) * mul;
+        }
+        named_sync(2 + pair, 64);   // read before the next chunk's halves come
+        store_tokens<16>(p.y, p.N, row + 16 * up, valid - 16 * up, col0 + pair * 32 + lane, out);
+      }
+    };
+
+    if (t.npieces == 1) {
+      for (int c = 0; c < chunks; ++c) {
+        float v[32];
+        load(c, v);
+        emit(c, v);
+      }
+      release();
+      continue;
+    }
+
+    // A piece of a cut tile: publish the fp32 partial ([token][weight row]) and
+    // count it; the piece that finds all others counted sums them in k order.
+    constexpr size_t kSlot = static_cast<size_t>(C::TOK) * 128;
+    float* slot = p.partials + (static_cast<size_t>(t.slot + t.piece) * 2 + rank) * kSlot;
+    for (int c = 0; c < chunks; ++c) {
+      float v[32];
+      load(c, v);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) __stcg(slot + (32 * c + j) * 128 + wrow, v[j]);
+    }
+    release();
+    __threadfence();
+    epilogue_bar_sync();
+    uint32_t* counter = p.counters + 2 * t.cut + rank;
+    if (et == 0) *last_flag = atomicAdd(counter, 1u) == static_cast<uint32_t>(t.npieces - 1);
+    epilogue_bar_sync();
+    const bool last = *last_flag != 0;
+    epilogue_bar_sync();   // read by all before the next tile writes it
+    if (!last) continue;
+    __threadfence();
+    const float* first = p.partials + (static_cast<size_t>(t.slot) * 2 + rank) * kSlot;
+    for (int c = 0; c < chunks; ++c) {
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __ldcg(first + (32 * c + j) * 128 + wrow);
+      for (int s = 1; s < t.npieces; ++s) {
+        const float* src = first + static_cast<size_t>(s) * 2 * kSlot;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __ldcg(src + (32 * c + j) * 128 + wrow);
+      }
+      emit(c, v);
+    }
+    if (et == 0) atomicExch(counter, 0u);   // ready for the next call
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid_constant__ RoutedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 8);
+  volatile int* marks = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 16);
+  const int warp = static_cast<int>(threadIdx.x) >> 5;
+  const uint32_t rank = cluster_rank();
+  const uint32_t bars = base + C::kBarsOff;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::S; ++i) {
+      // full: the leader's expect_tx (and, kLora, both CTAs' placing warps)
+      mbar_init(bars + 8 * i, C::KIND == kLora ? 1 + 2 * kPlacers : 1);
+      mbar_init(bars + 8 * (C::S + i), 1);                   // empty: the MMAs' commit
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 16 * C::S + 8 * i, 1);                // accumulator full
+      mbar_init(bars + 16 * C::S + 16 + 8 * i, 8);           // empty: the pair's epilogue warps
+    }
+    mbar_init(bars + 16 * C::S + 32, 1);
+    if constexpr (C::KIND == kLora)
+      for (int i = 0; i < C::S; ++i) mbar_init(bars + C::kAdapterBarOff + 8 * i, 1);
+    for (int i = 0; i < kMarks; ++i) marks[i] = 0;
+    *abort_flag = 0;
+    *last_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  cluster_barrier();
+  tc_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  // Programmatic dependent launch. The grouped kinds wait here for the previous
+  // kernel. kLora follows the low-rank kernel, which lets it start only once
+  // everything before that kernel has completed: X and W may be read at once,
+  // and the roles wait before they read what the low-rank kernel writes.
+  Groups g{};
+  int tiles;
+  if constexpr (C::KIND == kLora) {
+    tiles = p.m_tiles * p.n_tiles;
+  } else {
+    grid_dependency_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int* mem = reinterpret_cast<int*>(base_ptr + C::kGroupsOff);
+    g.row = mem;
+    g.count = mem + kMaxGroups;
+    g.tile = mem + 2 * kMaxGroups;
+    tiles = count_groups<C>(p, g, mem + 3 * kMaxGroups + 1) * p.n_tiles;
+  }
+
+  Ctl ctl{abort_flag, p.status, p.timeout_ns};
+  if (warp == 0) {
+    produce<C>(p, g, tiles, base, rank, ctl);
+  } else if (warp == 1) {
+    if (rank == 0) multiply<C>(p, g, tiles, base, tmem, ctl);
+  } else if (warp < 6) {
+    finish<C>(p, g, tiles, base, base_ptr, tmem, rank, last_flag, marks, ctl);
+  } else if constexpr (C::KIND == kLora) {
+    place_rows<C>(p, g, tiles, base, rank, marks, ctl);
+  }
+  __syncwarp();
+  if constexpr (C::KIND == kLora) {
+    // Every thread, also one without a tile: this grid must not complete before
+    // the low-rank kernel has.
+    grid_dependency_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
+  tc_fence_before_sync();
+  cluster_barrier();   // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, C::kTmemCols);
+  }
+}
+
+// Ring depths that fill shared memory.
+template <int KIND, bool GATHER, int TOK>
+using Instance = Cfg<KIND, GATHER, TOK, TOK == kRoutedSmall ? 5 : TOK == kRoutedMid ? 4 : 3>;
+
+template <class C>
+cudaError_t set_limit() {
+  return cudaFuncSetAttribute(gsr_routed_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(C::kSmem));
+}
+
+template <class C>
+cudaError_t launch_one(const RoutedParams& p, int ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gsr_routed_kernel<C>, p);
+}
+
+template <int KIND, bool GATHER>
+cudaError_t set_limits() {
+  cudaError_t e = set_limit<Instance<KIND, GATHER, kRoutedSmall>>();
+  if (e == cudaSuccess) e = set_limit<Instance<KIND, GATHER, kRoutedMid>>();
+  if (e == cudaSuccess) e = set_limit<Instance<KIND, GATHER, kRoutedWide>>();
+  return e;
+}
+
+template <int KIND, bool GATHER>
+cudaError_t launch_kind(const RoutedParams& p, int tokens, int ctas, cudaStream_t stream) {
+  if (tokens == kRoutedSmall) return launch_one<Instance<KIND, GATHER, kRoutedSmall>>(p, ctas, stream);
+  if (tokens == kRoutedMid) return launch_one<Instance<KIND, GATHER, kRoutedMid>>(p, ctas, stream);
+  return launch_one<Instance<KIND, GATHER, kRoutedWide>>(p, ctas, stream);
+}
+
+}  // namespace
+
+cudaError_t prepare_routed_kernels() {
+  cudaError_t e = set_limits<kGrouped, false>();
+  if (e == cudaSuccess) e = set_limits<kGrouped, true>();
+  if (e == cudaSuccess) e = set_limits<kGated, false>();
+  if (e == cudaSuccess) e = set_limits<kGated, true>();
+  if (e == cudaSuccess) e = set_limits<kLora, false>();
+  return e;
+}
+
+cudaError_t launch_routed(const RoutedParams& p, int kind, bool gather, int tokens, int ctas,
+                          cudaStream_t stream) {
+  if (kind == kLora) return launch_kind<kLora, false>(p, tokens, ctas, stream);
+  if (kind == kGated)
+    return gather ? launch_kind<kGated, true>(p, tokens, ctas, stream)
+                  : launch_kind<kGated, false>(p, tokens, ctas, stream);
+  return gather ? launch_kind<kGrouped, true>(p, tokens, ctas, stream)
+                : launch_kind<kGrouped, false>(p, tokens, ctas, stream);
+}
+
+}  // namespace gsr

@@ -1,0 +1,114 @@
+// gsr_routed.h -- launch parameters of the routed projections (internal to the
+// library): products grouped by expert, the gated form, the K-sharded
+// projection with per-row adapters, the route and the combine.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gsr_params.h"
+
+namespace gsr {
+
+constexpr int kMaxGroups = 1024;
+constexpr int kMaxTopk = 128;
+constexpr int kMaxRank = 128;       // columns of an adapter
+constexpr int kMaxAdapters = 65536;
+
+// kGrouped: Y = X . W[group]^T. kGated: Y = silu(X . Wg^T) * (X . Wu^T), gate and
+// up rows in one W. kLora: the K-sharded projection plus the adapters' products.
+enum RoutedKind : int { kGrouped = 0, kGated = 1, kLora = 2 };
+
+// Workspace of the routed calls (bytes): [0, 256) header (status word at 0);
+// [256, 256 + kRoutedCounterBytes) arrival counters of cut tiles; then the
+// fp32 partials of cut tiles; then the adapters' low-rank rows and lists.
+constexpr size_t kRoutedCounterBytes = 8192;
+constexpr int kRoutedTileRows = 256;        // weight rows of a CTA pair's tile
+constexpr int kRoutedMaxTokens = 256;       // tokens of a tile, at most
+// One adapter list per token tile: a count, then the tile's adapters ascending.
+constexpr int kAdapterListStride = kRoutedMaxTokens + 8;
+
+struct RoutedParams {  // 128-byte aligned through its CUtensorMap members
+  // Weights. Grouped: tmap_w[0] = W as {K, rows, E}, boxes of 64 x 128 rows (64
+  // rows when gated). Lora: tmap_w[r] = W_r, boxes of 64 x 128.
+  CUtensorMap tmap_w[kMaxShards];
+  // Tokens. Grouped: tmap_x[i] = X in boxes of 64 x (128 >> i) rows, i < 5, or,
+  // gathered, tmap_x[0] in boxes of one row. Lora: tmap_x[r] = X_r in boxes of
+  // 64 x tile_tokens / 2.
+  CUtensorMap tmap_x[kMaxShards];
+  CUtensorMap tmap_b;               // lora: B as {rank, N, L}, boxes of unit_cols x 128
+
+  const int32_t* offsets;           // grouped: E + 1 row offsets
+  const int32_t* rows;              // grouped: row of X of each row of Y (gathered)
+  const int32_t* adapter;           // lora: the adapter of each row
+  const int32_t* lists;             // lora: adapter lists of the token tiles
+  const uint16_t* low;              // lora: M x rank_pad, the scaled low-rank rows
+  const uint16_t* b;                // lora: L x N x rank
+  uint16_t* y;                      // M x N
+  uint32_t* status;
+  uint32_t* counters;
+  float* partials;
+  uint64_t timeout_ns;
+
+  int E, M, N, T, R, L, rank;       // T: rows of X (grouped)
+  int n_tiles;                      // tiles of output columns
+  int stages_per_tile;              // ring stages of a whole tile (the base product)
+  int m_tiles, tile_tokens;         // lora: token tiles and their width
+  int max_pieces, min_piece;        // of a cut tile: pieces at most, stages at least
+  int whole_from;                   // remainders of at least this many tiles are not cut
+  int unit_cols, units_per_adapter; // lora: columns of one step over an adapter
+  int rank_pad;                     // lora: unit_cols * units_per_adapter
+  int policy_w, policy_x;
+  int shard_st_begin[kMaxShards + 1];  // lora: first stage of shard r
+};
+
+// The low-rank rows: low[m, :] = scale[a] * sum_r X_r[m] . A_r[a]^T, a = adapter[m],
+// in bf16, and the adapter lists of the token tiles.
+struct LowRankParams {
+  const uint16_t* x[kMaxShards];    // M x K_r
+  const uint16_t* a[kMaxShards];    // L x rank x K_r
+  int64_t k[kMaxShards];
+  int unit_begin[kMaxShards + 1];   // first 64-column unit of shard r
+  const int32_t* adapter;
+  const float* scale;               // NULL: 1
+  uint16_t* low;
+  int32_t* lists;
+  int M, R, L, rank, rank_pad;
+  int tile_tokens, m_tiles;         // of the product that reads the lists
+  int rows_per_cta;                 // 16 (the warps share the reduction) or 128
+};
+
+struct RouteParams {
+  const void* ids;                  // T x topk
+  int32_t* offsets;
+  int32_t* source;
+  int32_t* position;
+  int n, topk, E, wide;             // wide: 64-bit ids
+};
+
+struct CombineParams {
+  const uint16_t* z;
+  const int32_t* position;
+  const float* weights;
+  const uint16_t* base;             // or NULL
+  uint16_t* y;
+  int64_t T, z_rows;
+  int topk, vecs;                   // 16-byte vectors of a row
+};
+
+// Token capacities of the routed product's instances.
+constexpr int kRoutedSmall = 64, kRoutedMid = 128, kRoutedWide = 256;
+// k-blocks of 64 in one ring stage.
+constexpr int kRoutedKblocks = 2;
+
+cudaError_t prepare_routed_kernels();
+cudaError_t prepare_lowrank_kernels();
+cudaError_t prepare_route_kernels();
+cudaError_t launch_routed(const RoutedParams& p, int kind, bool gather, int tokens, int ctas,
+                          cudaStream_t stream);
+cudaError_t launch_low_rank(const LowRankParams& p, cudaStream_t stream);
+cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);
+cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
+
+}  // namespace gsr
