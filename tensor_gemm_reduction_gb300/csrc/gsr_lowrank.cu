@@ -19,11 +19,13 @@
 // CTA too); the fp32 shares meet in distributed shared memory and are added in
 // a fixed order.
 //
-// The first CTA of a row block also writes the adapter list of a token tile of
-// the product that follows (ascending, without repeats).
+// Blocks past the rows write the adapter lists of the token tiles of the product
+// that follows (ascending, without repeats).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "gsr_routed.h"
 
@@ -32,7 +34,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreadsLow = 32 * kWarps;
-constexpr int kCluster = 8;          // CTAs that share the reduction
+constexpr int kMaxCluster = 8;       // CTAs that share the reduction, at most
 constexpr int kUnit = 64;            // k per step of a warp (128 bytes of a row)
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -62,42 +64,56 @@ __device__ __forceinline__ void cluster_sync_all() {
           : "memory");
 }
 
-// Distinct adapters of rows [row0, row0 + n), n <= 256, ascending. All threads.
-__device__ void write_list(const LowRankParams& p, int tile, int* ids, int* firsts) {
-  const int tid = static_cast<int>(threadIdx.x);
+// Distinct adapters of a token tile's rows, ascending: a bit per adapter, then
+// every thread lists the bits of its words behind those of the threads before.
+__device__ void write_list(const LowRankParams& p, int tile, uint32_t* bits, int* sums) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int words = (p.L + 31) / 32, per = (words + kThreadsLow - 1) / kThreadsLow;
+  const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
   const int row = tile * p.tile_tokens + tid;
-  int id = tid < p.tile_tokens && row < p.M ? p.adapter[row] : -1;
-  if (id < 0 || id >= p.L) id = -1;
-  ids[tid] = id;
+  const int id = tid < p.tile_tokens && row < p.M ? p.adapter[row] : -1;
+  for (int w = w0; w < w1; ++w) bits[w] = 0;
   __syncthreads();
-  bool first = id >= 0;
-  for (int j = 0; j < tid && first; ++j) first = ids[j] != id;
-  firsts[tid] = first ? id : -1;
+  if (id >= 0 && id < p.L) atomicOr(&bits[id >> 5], 1u << (id & 31));
   __syncthreads();
-  int rank = 0;
-  if (first)
-    for (int j = 0; j < kThreadsLow; ++j) rank += firsts[j] >= 0 && firsts[j] < id;
-  const int count = __syncthreads_count(first);
+  int mine = 0;
+  for (int w = w0; w < w1; ++w) mine += __popc(bits[w]);
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int at = incl - mine, total = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) at += sums[i];
+    total += sums[i];
+  }
   int32_t* list = p.lists + static_cast<size_t>(tile) * kAdapterListStride;
-  if (first) list[1 + rank] = id;
-  if (tid == 0) list[0] = count;
-  __syncthreads();
+  if (tid == 0) list[0] = total;
+  for (int w = w0; w < w1; ++w)
+    for (uint32_t b = bits[w]; b; b &= b - 1u) list[1 + at++] = 32 * w + __ffs(b) - 1;
 }
 
 // NT: 8-column tiles of the padded rank. SPLIT: the warps of a CTA share k (16
 // rows per CTA) or take 16 rows each (128 rows per CTA).
 template <int NT, bool SPLIT>
-__global__ void __launch_bounds__(kThreadsLow) gsr_lowrank_kernel(const __grid_constant__ LowRankParams p) {
+__global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __grid_constant__ LowRankParams p) {
   extern __shared__ float share[];                 // [kWarps][16][8 * NT]
-  __shared__ int ids[kThreadsLow], firsts[kThreadsLow];
+  __shared__ int ids[kWarps], keeps[16 * kWarps];
   constexpr int kCols = 8 * NT;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  const int z = static_cast<int>(blockIdx.z);
-  // The product's token tiles are never more than this kernel's row blocks.
-  if (blockIdx.y == 0 && z == 0 && static_cast<int>(blockIdx.x) < p.m_tiles)
-    write_list(p, static_cast<int>(blockIdx.x), ids, firsts);
+  const int z = static_cast<int>(blockIdx.z), ctas = static_cast<int>(gridDim.z);
+  const int blocks = (p.M + (SPLIT ? 16 : 16 * kWarps) - 1) / (SPLIT ? 16 : 16 * kWarps);
+  if (static_cast<int>(blockIdx.x) >= blocks) {   // whole clusters
+    if (blockIdx.y == 0 && z == 0)
+      write_list(p, static_cast<int>(blockIdx.x) - blocks, reinterpret_cast<uint32_t*>(share), ids);
+    return;
+  }
 
   const int row0 = static_cast<int>(blockIdx.x) * (SPLIT ? 16 : 16 * kWarps) + (SPLIT ? 0 : 16 * warp);
   const int group = lane >> 2, quad = lane & 3;
@@ -116,7 +132,7 @@ __global__ void __launch_bounds__(kThreadsLow) gsr_lowrank_kernel(const __grid_c
     for (int i = 0; i < kWarps; ++i) most = max(most, ids[i]);
   }
   const int units = p.unit_begin[p.R];
-  const int parts = SPLIT ? kCluster * kWarps : kCluster;
+  const int parts = SPLIT ? ctas * kWarps : ctas;
   const int part = SPLIT ? z * kWarps + warp : z;
   const int u0 = static_cast<int>(static_cast<long long>(part) * units / parts);
   const int u1 = static_cast<int>(static_cast<long long>(part + 1) * units / parts);
@@ -133,22 +149,24 @@ __global__ void __launch_bounds__(kThreadsLow) gsr_lowrank_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
     if (a >= 0) {
-      int r = 0;
-      for (int u = u0; u < u1; ++u) {
-        while (p.unit_begin[r + 1] <= u) ++r;
+      for (int r = 0; r < p.R; ++r) {
+        const int lo = max(u0, p.unit_begin[r]), hi = min(u1, p.unit_begin[r + 1]);
+        if (lo >= hi) continue;
         const int64_t K = p.k[r];
-        const int64_t k0 = static_cast<int64_t>(u - p.unit_begin[r]) * kUnit + quad * 8;
-        const uint16_t* xa = p.x[r] + static_cast<int64_t>(row0 + group) * K + k0;
-        const uint16_t* aa = p.a[r] + (static_cast<int64_t>(a) * p.rank + group) * K + k0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool in = k0 + 32 * h < K;
-          const uint4 f = load16(xa + 32 * h, in && row_a);
-          const uint4 s = load16(xa + 8 * K + 32 * h, in && row_b);
+        int k = (lo - p.unit_begin[r]) * kUnit + quad * 8;
+        const int k_end = min(static_cast<int>(K), (hi - p.unit_begin[r]) * kUnit);
+        const uint16_t* xa = p.x[r] + static_cast<int64_t>(row0 + group) * K;
+        const uint16_t* xb = xa + 8 * K;
+        const uint16_t* aa = p.a[r] + (static_cast<int64_t>(a) * p.rank + group) * K;
+#pragma unroll 2
+        for (; k - quad * 8 < k_end; k += 32) {
+          const bool in = k < k_end;
+          const uint4 f = load16(xa + k, in && row_a);
+          const uint4 s = load16(xb + k, in && row_b);
           uint4 b[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            b[n] = load16(aa + static_cast<int64_t>(8 * n) * K + 32 * h, in && 8 * n + group < p.rank);
+            b[n] = load16(aa + static_cast<int64_t>(8 * n) * K + k, in && 8 * n + group < p.rank);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             mma_16816(acc[n], f.x, s.x, f.y, s.y, b[n].x, b[n].y);
@@ -166,19 +184,19 @@ __global__ void __launch_bounds__(kThreadsLow) gsr_lowrank_kernel(const __grid_c
       mine[(group + 8) * kCols + 8 * n + 2 * quad + 1] = acc[n][3];
     }
     if constexpr (!SPLIT) {
-      if (lane < 16) firsts[warp * 16 + lane] = a >= 0 && id == a ? a : -1;   // rows to keep
+      if (lane < 16) keeps[warp * 16 + lane] = a >= 0 && id == a ? a : -1;   // rows to keep
     } else {
-      if (warp == 0 && lane < 16) firsts[lane] = id == a ? a : -1;
+      if (warp == 0 && lane < 16) keeps[lane] = id == a ? a : -1;
     }
     cluster_sync_all();
     // Each CTA of the cluster adds up a share of the elements, in k order.
     constexpr int kElems = (SPLIT ? 16 : 16 * kWarps) * kCols;
-    for (int e = z * kThreadsLow + tid; e < kElems; e += kCluster * kThreadsLow) {
+    for (int e = z * kThreadsLow + tid; e < kElems; e += ctas * kThreadsLow) {
       const int row = e / kCols, col = e - row * kCols;
-      const int keep = firsts[row];
+      const int keep = keeps[row];
       if (keep < 0) continue;
       float sum = 0.f;
-      for (int c = 0; c < kCluster; ++c) {
+      for (int c = 0; c < ctas; ++c) {
         const uint32_t at = cluster_shared_addr(share, static_cast<uint32_t>(c));
 #pragma unroll
         for (int w = 0; w < (SPLIT ? kWarps : 1); ++w) {
@@ -198,8 +216,19 @@ __global__ void __launch_bounds__(kThreadsLow) gsr_lowrank_kernel(const __grid_c
   }
 }
 
+// The warps' shares, or a bit per adapter.
+template <int NT>
+constexpr int smem_bytes() { return kWarps * 16 * 8 * NT * 4 > kMaxAdapters / 8 ? kWarps * 16 * 8 * NT * 4 : kMaxAdapters / 8; }
+
 template <int NT, bool SPLIT>
 cudaError_t launch_nt(const LowRankParams& p, cudaStream_t stream) {
+  const int rows = SPLIT ? 16 : 16 * kWarps, blocks = (p.M + rows - 1) / rows;
+  // 16 rows have at most 16 adapters, each a turn of its own. k is cut until the
+  // CTAs are about twice the SMs (the reduction over a cluster costs more).
+  const int turns = SPLIT ? std::min(16, std::min(p.L, p.M)) : 1;
+  int cluster = kMaxCluster;
+  if (SPLIT)
+    while (cluster > 1 && blocks * turns * cluster > 304) cluster /= 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -207,12 +236,10 @@ cudaError_t launch_nt(const LowRankParams& p, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = kCluster;
-  const int rows = SPLIT ? 16 : 16 * kWarps;
-  const int turns = SPLIT ? (p.L < 16 ? p.L : 16) : 1;
-  cfg.gridDim = dim3((p.M + rows - 1) / rows, turns, kCluster);
+  attr[1].val.clusterDim.z = cluster;
+  cfg.gridDim = dim3(blocks + p.m_tiles, turns, cluster);
   cfg.blockDim = dim3(kThreadsLow, 1, 1);
-  cfg.dynamicSmemBytes = kWarps * 16 * 8 * NT * sizeof(float);
+  cfg.dynamicSmemBytes = smem_bytes<NT>();
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -223,11 +250,11 @@ template <int NT>
 cudaError_t set_limit() {
   cudaError_t e = cudaFuncSetAttribute(gsr_lowrank_kernel<NT, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kWarps * 16 * 8 * NT * static_cast<int>(sizeof(float)));
+                                       smem_bytes<NT>());
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(gsr_lowrank_kernel<NT, false>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kWarps * 16 * 8 * NT * static_cast<int>(sizeof(float)));
+                              smem_bytes<NT>());
 }
 
 }  // namespace

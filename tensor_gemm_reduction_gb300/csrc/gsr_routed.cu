@@ -19,7 +19,8 @@
 // cuts depend on the group sizes alone, so results are reproducible.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (the pair's leader), warps 2..5
-// epilogue; kLora has warps 6..9 besides, which place the low-rank rows: the
+// epilogue. With gathered rows, warps 6..9 copy them and warp 10 signs them.
+// kLora has warps 6..9 besides, which place the low-rank rows: the
 // adapters of a token tile are more steps over k, in which the weights are
 // B[a] and a token's row is low[i] if its adapter is a and zero if not, so the
 // sum stays in the same fp32 accumulator. Those masked rows exist in shared
@@ -63,19 +64,25 @@ __device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap* map, ui
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(pol)
       : "memory");
 }
-// Four rows of a matrix, one below the other.
-__device__ __forceinline__ void copy_rows4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
-                                           int4 r, uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z),
-      "r"(r.w), "l"(pol)
-      : "memory");
+// 16 bytes to shared memory, or 16 zeros; asynchronous.
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0)
+               : "memory");
+}
+// Arrives on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void sign_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void arm(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
+}
+// Arrives on a barrier of the pair (its shared::cluster address). The arrival
+// publishes this CTA's own shared memory to the tensor cores, which a proxy
+// fence before it does; a release at cluster scope would besides wait for a
+// memory barrier over the GPU (about 1 us, once per ring stage).
+__device__ __forceinline__ void sign_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -90,14 +97,18 @@ template <int KIND_, bool GATHER_, int TOK_, int STAGES_>
 struct Cfg {
   static constexpr int KIND = KIND_, TOK = TOK_, S = STAGES_, KZ = kRoutedKblocks;
   static constexpr bool GATHER = GATHER_;
-  static constexpr int kThreads = KIND == kLora ? 64 + kEpi + 32 * kPlacers : 64 + kEpi;
+  static constexpr int kThreads = 64 + kEpi + (KIND == kLora ? 32 * kPlacers : GATHER ? 32 * (kPlacers + 1) : 0);
+  // Arrivals that complete a full barrier: the leader's expect_tx and, from both
+  // CTAs, the placing warps or the warp that signs for the gathered rows.
+  static constexpr uint32_t kSigns = 1 + (KIND == kLora ? 2 * kPlacers : GATHER ? 2 : 0);
   static constexpr uint32_t kW = 128 * 128;             // a k-block of this CTA's weight rows
   static constexpr uint32_t kX = TOK / 2 * 128;         // a k-block of this CTA's tokens
   static constexpr uint32_t kStage = KZ * (kW + kX);
   static constexpr uint32_t kRing = S * kStage;
-  // full[S], empty[S], tmem_full[2], tmem_empty[2], drain; kLora: adapter[S]
-  static constexpr uint32_t kBars = (2 * S + 5 + (KIND == kLora ? S : 0)) * 8;
-  static constexpr uint32_t kAdapterBarOff = (2 * S + 5) * 8;
+  // full[S], empty[S], tmem_full[2], tmem_empty[2], drain; landed[S]: this CTA's
+  // adapter weights (kLora) or gathered rows
+  static constexpr uint32_t kBars = (2 * S + 5 + (KIND == kLora || GATHER ? S : 0)) * 8;
+  static constexpr uint32_t kLandedOff = (2 * S + 5) * 8;
   static constexpr uint32_t kGroups = KIND == kLora ? 0 : 4 * (3 * kMaxGroups + 1 + 32);
   static constexpr uint32_t kSwap = KIND == kGated ? 2 * 2 * 16 * 32 * 4 : 0;
   static constexpr uint32_t kBarsOff = kRing;
@@ -124,6 +135,15 @@ struct Tile {
   int st, st_end;             // stages
 };
 
+// a / b for small operands by a float reciprocal: (a + 1/2) / b is at least 1 / 2b
+// from an integer and the quotient's error below a / b * 2^-21, so it is exact
+// while a < 2^19. An integer division takes some hundred cycles, and a tile's
+// place takes four.
+__device__ __forceinline__ int quotient(int a, int b) {
+  if (a >= (1 << 19)) return a / b;
+  return static_cast<int>(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b)));
+}
+
 template <class C>
 __device__ __forceinline__ void place(const RoutedParams& p, const Groups& g, int id, Tile& t) {
   int local, mt, width, count;
@@ -137,7 +157,7 @@ __device__ __forceinline__ void place(const RoutedParams& p, const Groups& g, in
   } else {
     // The last group whose first token tile is at or below this one (empty
     // groups share their successor's).
-    const int key = id / p.n_tiles;
+    const int key = quotient(id, p.n_tiles);
     int lo = 0, hi = p.E;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -148,16 +168,16 @@ __device__ __forceinline__ void place(const RoutedParams& p, const Groups& g, in
     local = id - g.tile[lo] * p.n_tiles;
     count = g.count[lo];
     t.row0 = g.row[lo];
-    width = ((count + mt - 1) / mt + 15) & ~15;
+    width = (quotient(count + mt - 1, mt) + 15) & ~15;
   }
   // Raster: 16 token tiles at a time, tokens fastest, so that concurrent pairs
   // share weight rows.
   const int span = 16 * p.n_tiles;
-  const int sup = local / span;
+  const int sup = quotient(local, span);
   const int gm = min(mt - sup * 16, 16);
-  const int in = local - sup * span;
-  t.m = sup * 16 + in % gm;
-  t.col0 = in / gm * (2 * C::kColsPerCta);
+  const int in = local - sup * span, col = quotient(in, gm);
+  t.m = sup * 16 + in - col * gm;
+  t.col0 = col * (2 * C::kColsPerCta);
   t.row0 += t.m * width;
   t.rows = min(width, count - t.m * width);
   t.n = C::KIND == kLora ? width : (t.rows + 15) & ~15;
@@ -334,23 +354,14 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
   bool ok = true, waited = C::KIND != kLora;
   Walk walk;
   walk.begin(p, tiles);
-  Tile t;
-  while (ok && walk.step<C>(p, g, t)) {
+  Tile t, tn;
+  bool have = walk.step<C>(p, g, t);
+  while (ok && have) {
+    bool looked = false, have_next = false;
     const int half = t.n / 2;
     const int w_row = t.col0 + static_cast<int>(rank) * C::kColsPerCta;
     const int x_row = t.row0 + static_cast<int>(rank) * half;
-    const uint32_t bytes = 2 * C::KZ * (C::kW + static_cast<uint32_t>(half) * 128);
-    int4 four = make_int4(0, 0, 0, 0);
-    if constexpr (C::GATHER) {
-      // This lane's four rows; past the tile's rows its last one again (never
-      // stored), and an index outside X as the row past X, which reads as zeros.
-      const int last = t.row0 + t.rows - 1, at = x_row + 4 * lane;
-      auto row = [&](int i) {
-        const int r = 4 * lane < half ? p.rows[min(i, last)] : 0;
-        return r >= 0 && r < p.T ? r : p.T;
-      };
-      four = make_int4(row(at), row(at + 1), row(at + 2), row(at + 3));
-    }
+    const uint32_t bytes = 2 * C::KZ * (C::kW + (C::GATHER ? 0u : static_cast<uint32_t>(half) * 128));
     int shard = 0, shard_begin = 0, shard_end = 0;
     if constexpr (C::KIND == kLora) {
       shard_end = __shfl_sync(0xffffffffu, begins, 1);
@@ -382,29 +393,16 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
             copy_3d(dw, &p.tmap_w[0], lead, kx + j * BK, w_row, t.group, pol_w);
             if constexpr (C::KIND == kGated)
               copy_3d(dw + C::kW / 2, &p.tmap_w[0], lead, kx + j * BK, p.N + w_row, t.group, pol_w);
-            if constexpr (!C::GATHER) {
-              // half rows (a multiple of 8) as boxes of 128, 64, 32, 16 and 8 rows
-              int r = 0;
-#pragma unroll
-              for (int b = 0; b < 5; ++b) {
-                const int box = 128 >> b;
-                if (half & box) {
-                  copy_2d(sx + j * C::kX + r * 128, &p.tmap_x[b], lead, kx + j * BK, x_row + r, pol_x);
-                  r += box;
-                }
-              }
-            }
+            // The map whose boxes are exactly this tile's rows.
+            if constexpr (!C::GATHER)
+              copy_2d(sx + j * C::kX, &p.tmap_x[half / 8 - 1], lead, kx + j * BK, x_row, pol_x);
           }
         }
       }
-      if constexpr (C::GATHER) {
-        __syncwarp();
-        if (4 * lane < half) {
-#pragma unroll
-          for (int j = 0; j < C::KZ; ++j)
-            copy_rows4(sx + j * C::kX + lane * 512, &p.tmap_x[0], lead, kx + j * BK, four, pol_x);
-        }
-        __syncwarp();
+      __syncwarp();
+      if (!looked && st - t.st == C::S - 1) {   // place the next tile while the ring is full
+        have_next = walk.step<C>(p, g, tn);
+        looked = true;
       }
       ++issued;
       ring.next<C::S>();
@@ -423,7 +421,7 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int units = a.units_in(st), u0 = st * a.per_stage;
-        const uint32_t landed = full0 + C::kAdapterBarOff + 8 * ring.slot;
+        const uint32_t landed = full0 + C::kLandedOff + 8 * ring.slot;
         if (lane == 0) {
           arm(landed, unit_w * units);
           if (rank == 0) mbar_arrive(full0 + 8 * ring.slot);
@@ -441,6 +439,9 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
         ring.next<C::S>();
       }
     }
+    if (!looked) have_next = walk.step<C>(p, g, tn);
+    t = tn;
+    have = have_next;
   }
   if (!ok) {
     // Let the copies already issued land before the shared memory goes away:
@@ -452,7 +453,7 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
       else
         wait_drain(empty0 + 8 * (i % C::S), (i / C::S) & 1u, 100000000ull);
     }
-    // Adapter copies complete on barriers that only the placing warps follow.
+    // Adapter weights complete on barriers that only the placing warps follow.
     if constexpr (C::KIND == kLora) {
       const uint64_t t0 = global_timer_ns();
       while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
@@ -538,6 +539,105 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
   }
 }
 
+// Gathered rows. TMA's four-row gathers cost about 30 ns each, whatever their
+// size, 32 of them per k-block at 256 tokens: four times the MMAs' time. So four
+// warps copy the rows, 16 bytes per thread and copy, eight threads to a row's 128
+// bytes of a k-block, into the 128-byte swizzle that TMA would write.
+template <class C>
+__device__ void gather_rows(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
+                            uint32_t rank, const Ctl& ctl) {
+  constexpr int kPasses = (C::TOK / 2 + 15) / 16;   // 16 rows a pass
+  const int tid = static_cast<int>(threadIdx.x) - 64 - kEpi;
+  const int chunk = tid & 7, row0 = tid >> 3;
+  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::S;
+  const uint32_t dst0 = static_cast<uint32_t>(row0 * 128 + ((chunk ^ (row0 & 7)) << 4));
+  const int K = p.K;
+  Ring ring;
+  bool ok = true;
+  Walk walk;
+  walk.begin(p, tiles);
+  Tile t, tn;
+  // This CTA's rows of a tile; the MMA's rows past them hold whatever is there
+  // (columns that are never stored).
+  auto rows_of = [&](const Tile& q) {
+    return min(q.n / 2, q.rows - static_cast<int>(rank) * (q.n / 2));
+  };
+  // Rows of X that this thread copies.
+  int at[kPasses], next[kPasses];
+  auto look = [&](const Tile& q, int (&r)[kPasses]) {
+    const int first = q.row0 + static_cast<int>(rank) * (q.n / 2), rows = rows_of(q);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      r[i] = row0 + 16 * i < rows ? __ldg(p.rows + first + row0 + 16 * i) : -1;
+  };
+  bool have = walk.step<C>(p, g, t);
+  if (have) look(t, at);
+  while (ok && have) {
+    const int rows = rows_of(t);
+    const uint16_t* src[kPasses];
+    uint32_t real = 0;   // an index outside X: zeros
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const bool in = at[i] >= 0 && at[i] < p.T;
+      real |= in ? 1u << i : 0u;
+      src[i] = p.x + static_cast<size_t>(in ? at[i] : 0) * K + 8 * chunk;
+    }
+    bool looked = false, have_next = false;
+    for (int st = t.st; st < t.st_end; ++st) {
+      ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRolePlacer << 8) | 3);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t sx = base + ring.slot * C::kStage + C::KZ * C::kW + dst0;
+#pragma unroll
+      for (int j = 0; j < C::KZ; ++j) {
+        const int k0 = (st * C::KZ + j) * BK;
+        const bool in_k = k0 + 8 * chunk < K;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+          if (row0 + 16 * i < rows)
+            copy_16(sx + j * C::kX + i * 2048, src[i] + (in_k ? k0 : 0), in_k && ((real >> i) & 1u));
+      }
+      sign_copies(full0 + C::kLandedOff + 8 * ring.slot);
+      ring.next<C::S>();
+      if (!looked) {
+        have_next = walk.step<C>(p, g, tn);
+        if (have_next) look(tn, next);
+        looked = true;
+      }
+    }
+    if (!ok) break;
+    t = tn;
+    have = have_next;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) at[i] = next[i];
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Signs the gathered rows on the leader's full barrier: when the copies of a
+// stage have landed, they are made visible to the tensor cores' reads.
+template <class C>
+__device__ void sign_rows(const RoutedParams& p, int tiles, uint32_t base, const Ctl& ctl) {
+  const uint32_t full0 = base + C::kBarsOff, landed0 = full0 + C::kLandedOff;
+  const uint32_t lead0 = map_shared_to_rank(full0, 0);
+  Ring ring;
+  Walk walk;
+  walk.begin(p, tiles);
+  uint32_t stages = walk.it_end - walk.it;
+  for (int id = walk.next; id < walk.whole; id += walk.G) stages += walk.S;
+  for (; stages > 0; --stages) {
+    bool ok = wait_bounded(landed0 + 8 * ring.slot, ring.phase, ctl, (kRolePlacer << 8) | 4);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    if ((threadIdx.x & 31) == 0) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      sign_pair(lead0 + 8 * ring.slot);
+    }
+    __syncwarp();
+    ring.next<C::S>();
+  }
+}
+
 // The low-rank rows of the ring's adapter stages: warp `pw` of 4 places rows pw *
 // 32 .. + 32 of this CTA's tokens, one per lane, and signs every stage on the
 // leader's full barrier (also those without rows to place, which keeps it in
@@ -560,7 +660,7 @@ __device__ void place_rows(const RoutedParams& p, const Groups& g, int tiles, ui
       ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRolePlacer << 8) | 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_cluster(lead0 + 8 * ring.slot);
+      if (lane == 0) sign_pair(lead0 + 8 * ring.slot);
       ring.next<C::S>();
     }
     if (!ok) break;
@@ -618,7 +718,7 @@ __device__ void place_rows(const RoutedParams& p, const Groups& g, int tiles, ui
       // A masked row times an infinite or NaN weight would be NaN: an adapter's
       // weights that are not finite become 0 here, and the epilogue adds their
       // products to the rows that have the adapter.
-      ok = wait_bounded(full0 + C::kAdapterBarOff + 8 * ring.slot, (landed_phase >> ring.slot) & 1u, ctl,
+      ok = wait_bounded(full0 + C::kLandedOff + 8 * ring.slot, (landed_phase >> ring.slot) & 1u, ctl,
                         (kRolePlacer << 8) | 2);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -649,7 +749,7 @@ __device__ void place_rows(const RoutedParams& p, const Groups& g, int tiles, ui
       if (marked) marks[local % kMarks] = 1;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(lead0 + 8 * ring.slot);
+      if (lane == 0) sign_pair(lead0 + 8 * ring.slot);
       ring.next<C::S>();
     }
   }
@@ -722,8 +822,11 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
   uint32_t local = 0;
   Walk walk;
   walk.begin(p, tiles);
-  Tile t;
-  for (; walk.step<C>(p, g, t); ++local) {
+  Tile t, tn;
+  bool have = walk.step<C>(p, g, tn);
+  for (; have; ++local) {
+    t = tn;
+    have = walk.step<C>(p, g, tn);   // while this tile's accumulator fills
     const uint32_t acc = local & 1u;
     const bool ok = wait_bounded(tfull0 + 8 * acc, (local >> 1) & 1u, ctl, (kRoleEpilogue << 8) | 1);
     if (!epilogue_bar_and(ok)) break;
@@ -752,7 +855,7 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
     auto release = [&]() {
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(lead_tempty + 8 * acc);
+      if (lane == 0) sign_pair(lead_tempty + 8 * acc);
     };
     // 32 tokens of the tile from token 32 * c on: this lane's column.
     auto emit = [&](int c, const float (&v)[32]) {
@@ -842,8 +945,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::S; ++i) {
-      // full: the leader's expect_tx (and, kLora, both CTAs' placing warps)
-      mbar_init(bars + 8 * i, C::KIND == kLora ? 1 + 2 * kPlacers : 1);
+      mbar_init(bars + 8 * i, C::kSigns);
       mbar_init(bars + 8 * (C::S + i), 1);                   // empty: the MMAs' commit
     }
     for (int i = 0; i < 2; ++i) {
@@ -851,8 +953,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
       mbar_init(bars + 16 * C::S + 16 + 8 * i, 8);           // empty: the pair's epilogue warps
     }
     mbar_init(bars + 16 * C::S + 32, 1);
-    if constexpr (C::KIND == kLora)
-      for (int i = 0; i < C::S; ++i) mbar_init(bars + C::kAdapterBarOff + 8 * i, 1);
+    if constexpr (C::KIND == kLora || C::GATHER)
+      for (int i = 0; i < C::S; ++i)
+        mbar_init(bars + C::kLandedOff + 8 * i, C::GATHER ? 32 * kPlacers : 1);
     for (int i = 0; i < kMarks; ++i) marks[i] = 0;
     *abort_flag = 0;
     *last_flag = 0;
@@ -895,6 +998,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
     finish<C>(p, g, tiles, base, base_ptr, tmem, rank, last_flag, marks, ctl);
   } else if constexpr (C::KIND == kLora) {
     place_rows<C>(p, g, tiles, base, rank, marks, ctl);
+  } else if constexpr (C::GATHER) {
+    if (warp < 6 + kPlacers)
+      gather_rows<C>(p, g, tiles, base, rank, ctl);
+    else
+      sign_rows<C>(p, tiles, base, ctl);
   }
   __syncwarp();
   if constexpr (C::KIND == kLora) {

@@ -33,14 +33,14 @@ struct RoutedParams {  // 128-byte aligned through its CUtensorMap members
   // Weights. Grouped: tmap_w[0] = W as {K, rows, E}, boxes of 64 x 128 rows (64
   // rows when gated). Lora: tmap_w[r] = W_r, boxes of 64 x 128.
   CUtensorMap tmap_w[kMaxShards];
-  // Tokens. Grouped: tmap_x[i] = X in boxes of 64 x (128 >> i) rows, i < 5, or,
-  // gathered, tmap_x[0] in boxes of one row. Lora: tmap_x[r] = X_r in boxes of
-  // 64 x tile_tokens / 2.
+  // Tokens. Grouped: tmap_x[i] = X in boxes of 64 x 8 (i + 1) rows (none when the
+  // rows are gathered). Lora: tmap_x[r] = X_r in boxes of 64 x tile_tokens / 2.
   CUtensorMap tmap_x[kMaxShards];
   CUtensorMap tmap_b;               // lora: B as {rank, N, L}, boxes of unit_cols x 128
 
   const int32_t* offsets;           // grouped: E + 1 row offsets
   const int32_t* rows;              // grouped: row of X of each row of Y (gathered)
+  const uint16_t* x;                // gathered: X, T x K
   const int32_t* adapter;           // lora: the adapter of each row
   const int32_t* lists;             // lora: adapter lists of the token tiles
   const uint16_t* low;              // lora: M x rank_pad, the scaled low-rank rows
@@ -51,7 +51,7 @@ struct RoutedParams {  // 128-byte aligned through its CUtensorMap members
   float* partials;
   uint64_t timeout_ns;
 
-  int E, M, N, T, R, L, rank;       // T: rows of X (grouped)
+  int E, M, N, K, T, R, L, rank;       // T: rows of X (grouped)
   int n_tiles;                      // tiles of output columns
   int stages_per_tile;              // ring stages of a whole tile (the base product)
   int m_tiles, tile_tokens;         // lora: token tiles and their width
@@ -99,7 +99,8 @@ struct CombineParams {
 
 // Token capacities of the routed product's instances.
 constexpr int kRoutedSmall = 64, kRoutedMid = 128, kRoutedWide = 256;
-// k-blocks of 64 in one ring stage.
+// k-blocks of 64 in one ring stage: a stage costs its barrier's fixed time, so one
+// k-block per stage is 10 to 20 % slower at 256 tokens.
 constexpr int kRoutedKblocks = 2;
 
 cudaError_t prepare_routed_kernels();

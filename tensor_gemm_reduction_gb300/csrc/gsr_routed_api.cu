@@ -169,6 +169,8 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
   fill_routed(p, P, M, N, static_cast<int>(cdiv(K, kStageK)), tokens, ws);
   p.E = E;
   p.T = static_cast<int>(T);
+  p.K = static_cast<int>(K);
+  p.x = static_cast<const uint16_t*>(X);
   p.offsets = offsets;
   p.rows = rows;
   p.y = static_cast<uint16_t*>(Y);
@@ -177,11 +179,9 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
   p.policy_x = tokens == gsr::kRoutedWide ? gsr::kPolicyNormal : gsr::kPolicyEvictLast;
   CUresult cr = encode_stack(&p.tmap_w[0], W, E, wide, K, BK, kind == gsr::kGated ? 64 : 128);
   if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding the W descriptor failed (%d)", (int)cr);
-  if (rows) {
-    cr = encode_2d(&p.tmap_x[0], X, T, K, 1);
-  } else {
-    for (int i = 0; i < 5 && cr == CUDA_SUCCESS; ++i) cr = encode_2d(&p.tmap_x[i], X, M, K, 128 >> i);
-  }
+  if (!rows)
+    for (int i = 0; i < tokens / 16 && cr == CUDA_SUCCESS; ++i)
+      cr = encode_2d(&p.tmap_x[i], X, M, K, 8 * (i + 1));
   if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding the X descriptor failed (%d)", (int)cr);
   DeviceScope scope(P->device);
   if (scope.err != cudaSuccess) return cuda_fail(scope.err, "selecting the plan's device");
