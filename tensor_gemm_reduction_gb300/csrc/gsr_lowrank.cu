@@ -100,7 +100,7 @@ __device__ void write_list(const LowRankParams& p, int tile, uint32_t* bits, int
 // NT: 8-column tiles of the padded rank. SPLIT: the warps of a CTA share k (16
 // rows per CTA) or take 16 rows each (128 rows per CTA).
 template <int NT, bool SPLIT>
-__global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __grid_constant__ LowRankParams p) {
+__global__ void __launch_bounds__(kThreadsLow, NT <= 4 ? 3 : 2) gsr_lowrank_kernel(const __grid_constant__ LowRankParams p) {
   extern __shared__ float share[];                 // [kWarps][16][8 * NT]
   __shared__ int ids[kWarps], keeps[16 * kWarps];
   constexpr int kCols = 8 * NT;
@@ -224,11 +224,11 @@ template <int NT, bool SPLIT>
 cudaError_t launch_nt(const LowRankParams& p, cudaStream_t stream) {
   const int rows = SPLIT ? 16 : 16 * kWarps, blocks = (p.M + rows - 1) / rows;
   // 16 rows have at most 16 adapters, each a turn of its own. k is cut until the
-  // CTAs are about twice the SMs (the reduction over a cluster costs more).
+  // CTAs are about four times the SMs (the reduction over a cluster costs more).
   const int turns = SPLIT ? std::min(16, std::min(p.L, p.M)) : 1;
   int cluster = kMaxCluster;
   if (SPLIT)
-    while (cluster > 1 && blocks * turns * cluster > 304) cluster /= 2;
+    while (cluster > 1 && blocks * turns * cluster > 608) cluster /= 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -41,7 +41,8 @@ namespace gsr {
 namespace {
 
 constexpr int kEpi = 128;              // epilogue threads
-constexpr int kPlacers = 4;            // kLora: warps that place low-rank rows
+constexpr int kPlacers = 4;            // warps that place (or gather) the rows of a stage
+constexpr int kTeams = 2;              // kLora: teams of them, on alternate stages
 constexpr uint32_t kRolePlacer = 4;
 // kLora: tiles in flight between the placing warps and the epilogue, at most: a
 // ring of single-stage tiles and two accumulators.
@@ -84,6 +85,9 @@ __device__ __forceinline__ void arm(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void sign_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+__device__ __forceinline__ void sign_many(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -93,15 +97,16 @@ __device__ __forceinline__ void grid_dependency_wait() {
 
 // ------------------------------------------------------------ geometry
 
-template <int KIND_, bool GATHER_, int TOK_, int STAGES_>
+template <int KIND_, bool GATHER_, bool HALF_, int TOK_, int KZ_, int STAGES_>
 struct Cfg {
-  static constexpr int KIND = KIND_, TOK = TOK_, S = STAGES_, KZ = kRoutedKblocks;
-  static constexpr bool GATHER = GATHER_;
-  static constexpr int kThreads = 64 + kEpi + (KIND == kLora ? 32 * kPlacers : GATHER ? 32 * (kPlacers + 1) : 0);
+  static constexpr int KIND = KIND_, TOK = TOK_, S = STAGES_, KZ = KZ_;
+  static constexpr bool GATHER = GATHER_, HALF = HALF_;
+  static constexpr int kRows = HALF ? 64 : 128;         // weight rows of a CTA, at most
+  static constexpr int kThreads = 64 + kEpi + (KIND == kLora ? 32 * kPlacers * kTeams : GATHER ? 32 * (kPlacers + 1) : 0);
   // Arrivals that complete a full barrier: the leader's expect_tx and, from both
   // CTAs, the placing warps or the warp that signs for the gathered rows.
   static constexpr uint32_t kSigns = 1 + (KIND == kLora ? 2 * kPlacers : GATHER ? 2 : 0);
-  static constexpr uint32_t kW = 128 * 128;             // a k-block of this CTA's weight rows
+  static constexpr uint32_t kW = kRows * 128;           // a k-block of this CTA's weight rows
   static constexpr uint32_t kX = TOK / 2 * 128;         // a k-block of this CTA's tokens
   static constexpr uint32_t kStage = KZ * (kW + kX);
   static constexpr uint32_t kRing = S * kStage;
@@ -118,7 +123,6 @@ struct Cfg {
   static constexpr uint32_t kSmem = 1024 + kGroupsOff + kGroups;
   static_assert(kSmem <= kSmallSmemLimit, "shared memory");
   static_assert(kX % 1024 == 0, "swizzle atoms");
-  static constexpr int kColsPerCta = KIND == kGated ? 64 : 128;   // output columns
   static constexpr uint32_t kTmemCols = 2 * TOK;
 };
 
@@ -177,7 +181,7 @@ __device__ __forceinline__ void place(const RoutedParams& p, const Groups& g, in
   const int gm = min(mt - sup * 16, 16);
   const int in = local - sup * span, col = quotient(in, gm);
   t.m = sup * 16 + in - col * gm;
-  t.col0 = col * (2 * C::kColsPerCta);
+  t.col0 = col * (2 * p.cta_cols);
   t.row0 += t.m * width;
   t.rows = min(width, count - t.m * width);
   t.n = C::KIND == kLora ? width : (t.rows + 15) & ~15;
@@ -296,21 +300,34 @@ __device__ int count_groups(const RoutedParams& p, const Groups& g, int* sums) {
 
 // ------------------------------------------------------------ adapters of a tile
 
-// The steps over the adapters of token tile m that belong to piece `piece`: each
-// piece of a cut tile takes an equal share. Read by whole warps, after the
-// low-rank kernel has completed.
+// The steps over the adapters of token tile m that belong to this piece: a piece
+// of a cut tile takes the share that it has of the base product. Read by whole warps, after the
+// low-rank kernel has completed; the lanes hold 32 of the tile's adapters.
 struct AdapterSteps {
-  const int32_t* ids;
+  const int32_t* list;
   int units, st, st_end, per_stage;
+  int held, first;   // this lane's adapter, and lane 0's place in the list
   template <class C>
   __device__ __forceinline__ void begin(const RoutedParams& p, const Tile& t) {
-    const int32_t* list = p.lists + static_cast<size_t>(t.m) * kAdapterListStride;
-    ids = list + 1;
+    list = p.lists + static_cast<size_t>(t.m) * kAdapterListStride;
     units = __ldcg(list) * p.units_per_adapter;
     per_stage = C::KZ * 64 / p.unit_cols;
     const int stages = (units + per_stage - 1) / per_stage;
-    st = t.piece * stages / t.npieces;
-    st_end = (t.piece + 1) * stages / t.npieces;
+    st = t.st * stages / p.stages_per_tile;
+    st_end = t.st_end * stages / p.stages_per_tile;
+    hold(st * per_stage / p.units_per_adapter);
+  }
+  // (Past the list's end: whatever the workspace holds, never used.)
+  __device__ __forceinline__ void hold(int at) {
+    first = at;
+    const int i = at + (static_cast<int>(threadIdx.x) & 31);
+    held = i < kRoutedMaxTokens ? __ldcg(list + 1 + i) : 0;
+  }
+  // The adapter of unit u (warp-uniform, ascending over the calls).
+  __device__ __forceinline__ int adapter(const RoutedParams& p, int u) {
+    const int at = p.units_per_adapter == 2 ? u >> 1 : u;
+    if (at >= first + 32) hold(at);
+    return __shfl_sync(0xffffffffu, held, at - first);
   }
   __device__ __forceinline__ int units_in(int s) const { return min(per_stage, units - s * per_stage); }
 };
@@ -359,11 +376,13 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
   while (ok && have) {
     bool looked = false, have_next = false;
     const int half = t.n / 2;
-    const int w_row = t.col0 + static_cast<int>(rank) * C::kColsPerCta;
+    const int w_row = t.col0 + static_cast<int>(rank) * p.cta_cols;
     const int x_row = t.row0 + static_cast<int>(rank) * half;
-    const uint32_t bytes = 2 * C::KZ * (C::kW + (C::GATHER ? 0u : static_cast<uint32_t>(half) * 128));
+    const uint32_t bytes = 2 * C::KZ * (128u * p.w_rows + (C::GATHER ? 0u : static_cast<uint32_t>(half) * 128));
     int shard = 0, shard_begin = 0, shard_end = 0;
+    AdapterSteps a{};
     if constexpr (C::KIND == kLora) {
+      if (waited) a.template begin<C>(p, t);   // its reads come back during the base product
       shard_end = __shfl_sync(0xffffffffu, begins, 1);
       while (shard_end <= t.st) shard_end = __shfl_sync(0xffffffffu, begins, ++shard + 1);
       shard_begin = __shfl_sync(0xffffffffu, begins, shard);
@@ -382,7 +401,10 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
       }
       const int kx = (st - shard_begin) * (C::KZ * BK);
       if (lane == 0) {
-        if (rank == 0) arm(full0 + 8 * ring.slot, bytes);
+        if (rank == 0) {
+          arm(full0 + 8 * ring.slot, bytes);
+          if constexpr (C::KIND == kLora) sign_many(full0 + 8 * ring.slot, 2 * kPlacers);   // nothing to place
+        }
 #pragma unroll
         for (int j = 0; j < C::KZ; ++j) {
           const uint32_t dw = sw + j * C::kW;
@@ -412,10 +434,9 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
       if (!waited) {
         grid_dependency_wait();
         waited = true;
+        a.template begin<C>(p, t);
       }
-      AdapterSteps a{};
-      a.template begin<C>(p, t);
-      const uint32_t unit_w = 256u * p.unit_cols;
+      const uint32_t unit_w = 2u * C::kRows * p.unit_cols, unit_bytes = 2u * p.w_rows * p.unit_cols;
       for (int st = a.st; st < a.st_end; ++st) {
         ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRoleProducer << 8) | 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -423,16 +444,17 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
         const int units = a.units_in(st), u0 = st * a.per_stage;
         const uint32_t landed = full0 + C::kLandedOff + 8 * ring.slot;
         if (lane == 0) {
-          arm(landed, unit_w * units);
+          arm(landed, unit_bytes * units);
           if (rank == 0) mbar_arrive(full0 + 8 * ring.slot);
         }
         __syncwarp();
-        // One lane per unit (at most 8): its adapter's columns of B. They complete
-        // on this CTA's own barrier: the placing warps look them over first.
-        if (lane < units) {
-          const int u = u0 + lane, i = u / p.units_per_adapter;
-          copy_3d(base + ring.slot * C::kStage + lane * unit_w, &p.tmap_b, landed,
-                  (u - i * p.units_per_adapter) * p.unit_cols, w_row, __ldcg(a.ids + i), pol_w);
+        // Each unit's columns of its adapter's B. They complete on this CTA's own
+        // barrier, which tells the placing warps that the slot is theirs.
+        for (int u = 0; u < units; ++u) {
+          const int id = a.adapter(p, u0 + u);
+          if (lane == 0)
+            copy_3d(base + ring.slot * C::kStage + u * unit_w, &p.tmap_b, landed,
+                    p.units_per_adapter == 2 ? ((u0 + u) & 1) * p.unit_cols : 0, w_row, id, pol_w);
         }
         __syncwarp();
         ++issued;
@@ -481,8 +503,11 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
     if (!ok) break;
     tc_fence_after_sync();
     const uint32_t d = tmem + acc * C::TOK;
-    const uint32_t idesc = make_idesc(256, static_cast<uint32_t>(t.n));
+    const uint32_t idesc = make_idesc(2 * C::kRows, static_cast<uint32_t>(t.n));
     bool looked = false, have_next = false;
+    AdapterSteps a{};
+    if constexpr (C::KIND == kLora)
+      if (waited) a.template begin<C>(p, t);
     for (int st = t.st; st < t.st_end; ++st) {
       ok = wait_bounded(full0 + 8 * ring.slot, ring.phase, ctl, (kRoleMma << 8) | 2);
       ok = __all_sync(0xffffffffu, ok);
@@ -506,11 +531,10 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
       if (!waited) {
         grid_dependency_wait();
         waited = true;
+        a.template begin<C>(p, t);
       }
-      AdapterSteps a{};
-      a.template begin<C>(p, t);
       const int cols = p.unit_cols;
-      const uint32_t unit_w = 256u * cols, unit_x = static_cast<uint32_t>(C::TOK) * cols;
+      const uint32_t unit_w = 2u * C::kRows * cols, unit_x = static_cast<uint32_t>(C::TOK) * cols;
       for (int st = a.st; st < a.st_end; ++st) {
         ok = wait_bounded(full0 + 8 * ring.slot, ring.phase, ctl, (kRoleMma << 8) | 2);
         ok = __all_sync(0xffffffffu, ok);
@@ -638,128 +662,144 @@ __device__ void sign_rows(const RoutedParams& p, int tiles, uint32_t base, const
   }
 }
 
-// The low-rank rows of the ring's adapter stages: warp `pw` of 4 places rows pw *
-// 32 .. + 32 of this CTA's tokens, one per lane, and signs every stage on the
-// leader's full barrier (also those without rows to place, which keeps it in
-// step with the ring).
+// One adapter stage: this lane's row `v` (COLS columns, the adapter `id`) in the
+// units of that adapter, zeros in the others; and the stage's adapter weights
+// looked over. True if one of them was not finite.
+//
+// A masked row times an infinite or NaN weight would be NaN: such weights become
+// 0 here, and the epilogue adds their products to the rows that have the adapter.
+template <int COLS, class C>
+__device__ __forceinline__ bool place_stage(const RoutedParams& p, AdapterSteps& a, uint32_t sw, int st,
+                                            int id, int who, int row, int ways, int half,
+                                            const uint4 (&v)[kMaxRank / 8]) {
+  constexpr uint32_t kUnitX = C::TOK * COLS, kUnitW = 2 * C::kRows * COLS;
+  constexpr uint32_t kMask = COLS == 64 ? 7 : COLS == 32 ? 3 : 1;
+  const uint32_t sx = sw + C::KZ * C::kW;
+  const int units = a.units_in(st), u0 = st * a.per_stage;
+  const uint32_t at_row = static_cast<uint32_t>(row) * COLS * 2;
+#pragma unroll 2
+  for (int u = who * ways / (32 * kPlacers); u < units; u += ways) {
+    const bool hit = a.adapter(p, u0 + u) == id;
+    const bool upper = COLS == 64 && p.units_per_adapter == 2 && ((u0 + u) & 1);   // columns 64..127
+    if (row < half) {
+      const uint32_t dst = sx + u * kUnitX;
+#pragma unroll
+      for (int c = 0; c < COLS / 8; ++c) {
+        const uint4 w = COLS == 64 && upper ? v[8 + c] : v[c];
+        uint32_t off = at_row + 16u * c;
+        off ^= ((off >> 7) & kMask) << 4;   // the copies' swizzle over 2 * COLS bytes
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + off), "r"(hit ? w.x : 0u),
+                     "r"(hit ? w.y : 0u), "r"(hit ? w.z : 0u), "r"(hit ? w.w : 0u)
+                     : "memory");
+      }
+    }
+  }
+  // The weights: each warp looks over every fourth unit.
+  const int lane = who & 31;
+  const uint32_t bytes = 2u * p.w_rows * COLS;   // of a unit, a multiple of 256
+  bool marked = false;
+  for (int u = who >> 5; u < units; u += kPlacers) {
+    const uint32_t unit = sw + u * kUnitW;
+    for (uint32_t at = 16u * lane; at < bytes; at += 4 * 512) {
+      uint32_t w[4][4], any = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        w[q][0] = w[q][1] = w[q][2] = w[q][3] = 0;
+        if (at + q * 512 < bytes)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3])
+                       : "r"(unit + at + q * 512)
+                       : "memory");
+      }
+      // Bits 15 and 31 of (w & exponents) + 1 exponent step: an exponent of all ones.
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) any |= (w[q][j] & 0x7f807f80u) + 0x00800080u;
+      if (any & 0x80008000u) {
+        marked = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (at + q * 512 >= bytes) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t odd = ((w[q][j] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+            w[q][j] &= ~((odd >> 15) * 0xffffu);
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(unit + at + q * 512), "r"(w[q][0]),
+                       "r"(w[q][1]), "r"(w[q][2]), "r"(w[q][3])
+                       : "memory");
+        }
+      }
+    }
+  }
+  return marked;
+}
+
+// The low-rank rows of the ring's adapter stages. Two teams of four warps take
+// alternate stages. A team's threads are the rows of this CTA's tokens, or, with
+// at most 64 or 32 rows, two or four times the rows, on alternate adapters. Every
+// warp signs the stage on the leader's full barrier. A stage is theirs once its adapter weights have landed (the producer had waited for the
+// slot); the base product's stages pass them by.
 template <class C>
 __device__ void place_rows(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
                            uint32_t rank, volatile int* marks, const Ctl& ctl) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
-  const int i = static_cast<int>(threadIdx.x) - 64 - kEpi;   // row of this CTA's tokens
-  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::S;
+  const int who = static_cast<int>(threadIdx.x) - 64 - kEpi;
+  const int team = who / (32 * kPlacers), i = who % (32 * kPlacers);
+  const uint32_t full0 = base + C::kBarsOff;
   const uint32_t lead0 = map_shared_to_rank(full0, 0);
   Ring ring;
-  bool ok = true, waited = false;
-  uint32_t landed_phase = 0, local = 0;   // bit s: phase of slot s's adapter barrier
+  bool ok = true;
+  uint32_t landed_phase = 0, local = 0;   // bit s: phase of slot s's landed barrier
   Walk walk;
   walk.begin(p, tiles);
   Tile t;
+  grid_dependency_wait();
   for (; ok && walk.step<C>(p, g, t); ++local) {
-    for (int st = t.st; st < t.st_end; ++st) {
-      ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRolePlacer << 8) | 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0) sign_pair(lead0 + 8 * ring.slot);
-      ring.next<C::S>();
-    }
-    if (!ok) break;
-    if (!waited) {
-      grid_dependency_wait();
-      waited = true;
-    }
+    ring.slot = (ring.slot + static_cast<uint32_t>(t.st_end - t.st)) % C::S;
     AdapterSteps a{};
     a.template begin<C>(p, t);
     if (a.st >= a.st_end) continue;
-    const int half = t.n / 2, m = t.row0 + static_cast<int>(rank) * half + i;
-    const bool mine = i < half;
+    const int half = t.n / 2, ways = half <= 32 ? 4 : half <= 64 ? 2 : 1;
+    const int row = i & (32 * kPlacers / ways - 1), m = t.row0 + static_cast<int>(rank) * half + row;
     int id = -1;
     uint4 v[kMaxRank / 8];
-    if (mine && m < p.M) id = p.adapter[m];
-    const bool live = id >= 0 && id < p.L;
+    if (row < half && m < p.M) id = p.adapter[m];
+    if (id >= p.L) id = -1;   // no adapter of the list is negative
 #pragma unroll
     for (int c = 0; c < kMaxRank / 8; ++c)
-      v[c] = live && 8 * c < p.rank_pad
+      v[c] = id >= 0 && 8 * c < p.rank_pad
                  ? __ldcg(reinterpret_cast<const uint4*>(p.low + static_cast<size_t>(m) * p.rank_pad) + c)
                  : make_uint4(0, 0, 0, 0);
-    const int cols = p.unit_cols;
-    const uint32_t unit_x = static_cast<uint32_t>(C::TOK) * cols;
-    const uint32_t mask = cols == 64 ? 7u : cols == 32 ? 3u : 1u;
-    const uint32_t row_off = static_cast<uint32_t>(i) * cols * 2;
     for (int st = a.st; st < a.st_end; ++st) {
-      ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRolePlacer << 8) | 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t sx = base + ring.slot * C::kStage + C::KZ * C::kW;
-      const int units = a.units_in(st), u0 = st * a.per_stage;
-      // The stage's adapters in the warp's lanes.
-      const int at = (u0 + (lane < units ? lane : 0)) / p.units_per_adapter;
-      const int ids = __ldcg(a.ids + at);
-      for (int u = 0; u < units; ++u) {
-        const int adapter = __shfl_sync(0xffffffffu, ids, u);
-        const bool hit = live && adapter == id;
-        const bool upper = p.units_per_adapter == 2 && ((u0 + u) & 1);   // columns 64..127
-        if (mine) {
-          const uint32_t dst = sx + u * unit_x;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (8 * c < cols) {
-              const uint4 w = upper ? v[8 + c] : v[c];
-              uint32_t off = row_off + 16u * c;
-              off ^= ((off >> 7) & mask) << 4;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + off),
-                           "r"(hit ? w.x : 0u), "r"(hit ? w.y : 0u), "r"(hit ? w.z : 0u),
-                           "r"(hit ? w.w : 0u)
-                           : "memory");
-            }
-          }
-        }
-      }
-      // A masked row times an infinite or NaN weight would be NaN: an adapter's
-      // weights that are not finite become 0 here, and the epilogue adds their
-      // products to the rows that have the adapter.
+      // Both teams follow every stage, so that neither takes a slot's next phase
+      // for the one that it waits for.
       ok = wait_bounded(full0 + C::kLandedOff + 8 * ring.slot, (landed_phase >> ring.slot) & 1u, ctl,
                         (kRolePlacer << 8) | 2);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       landed_phase ^= 1u << ring.slot;
-      const uint32_t sw = base + ring.slot * C::kStage, bytes = 256u * cols * units;
-      bool marked = false;
-      for (uint32_t at = 16u * i; at < bytes; at += 16u * 32 * kPlacers) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(sw + at)
-                     : "memory");
-        uint32_t odd[4], any = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          odd[j] = ((w[j] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;   // exponent all ones
-          any |= odd[j];
-        }
-        if (any) {
-          marked = true;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] &= ~((odd[j] >> 15) * 0xffffu);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sw + at), "r"(w[0]), "r"(w[1]),
-                       "r"(w[2]), "r"(w[3])
-                       : "memory");
-        }
+      if (((st - a.st) & 1) == team) {
+        const uint32_t sw = base + ring.slot * C::kStage;
+        const bool marked = p.unit_cols == 16   ? place_stage<16, C>(p, a, sw, st, id, i, row, ways, half, v)
+                            : p.unit_cols == 32 ? place_stage<32, C>(p, a, sw, st, id, i, row, ways, half, v)
+                                                : place_stage<64, C>(p, a, sw, st, id, i, row, ways, half, v);
+        if (marked) marks[local % kMarks] = 1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) sign_pair(lead0 + 8 * ring.slot);
       }
-      if (marked) marks[local % kMarks] = 1;
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) sign_pair(lead0 + 8 * ring.slot);
       ring.next<C::S>();
     }
   }
 }
 
 // The products of adapter weights that are not finite, which the placing warps
-// took out of the tile: column `col` of 32 tokens from token 32 * c on, for the
-// adapters of this piece.
+// took out of the tile: column `col` of `valid` (or 32) rows from row0 on, for
+// the adapters of this piece.
 template <class C>
-__device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t, int c, int col,
+__device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t, int row0, int valid, int col,
                                            float (&v)[32]) {
   AdapterSteps a{};
   a.template begin<C>(p, t);
@@ -767,12 +807,12 @@ __device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t,
   if (col >= p.N) return;
 #pragma unroll 1
   for (int j = 0; j < 32; ++j) {
-    const int m = t.row0 + 32 * c + j;
-    if (32 * c + j >= t.rows) break;
+    const int m = row0 + j;
+    if (j >= valid) break;
     const int id = p.adapter[m];
     if (id < 0 || id >= p.L) continue;
     int at = 0;
-    while (__ldcg(a.ids + at) != id) ++at;   // the tile's list has every row's adapter
+    while (__ldcg(a.list + 1 + at) != id) ++at;   // the tile's list has every row's adapter
     float sum = 0.f;
     bool any = false;
     for (int k = 0; k < p.rank; ++k) {
@@ -791,9 +831,10 @@ __device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t,
 }
 
 // Stores two columns (this lane's and its neighbour's) of the chunk's tokens:
-// v[j] is token j, this lane's column. COUNT tokens, the first at `row`.
+// v[j] is token j, this lane's column (stored if below `end`). COUNT tokens, the
+// first at `row`.
 template <int COUNT>
-__device__ __forceinline__ void store_tokens(uint16_t* y, int N, int row, int valid, int col,
+__device__ __forceinline__ void store_tokens(uint16_t* y, int N, int row, int valid, int col, int end,
                                              const float* v) {
   const bool odd = threadIdx.x & 1;
   uint16_t* at = y + static_cast<size_t>(row) * N + (col & ~1);
@@ -803,7 +844,7 @@ __device__ __forceinline__ void store_tokens(uint16_t* y, int N, int row, int va
     const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
     const uint32_t out = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
     const int token = j + (odd ? 1 : 0);
-    if (token < valid && col < N)
+    if (token < valid && col < end)
       *reinterpret_cast<uint32_t*>(at + static_cast<size_t>(token) * N) = out;
   }
 }
@@ -816,7 +857,9 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
   const int et = static_cast<int>(threadIdx.x) - 64;
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int quad = (static_cast<int>(threadIdx.x) >> 5) & 3;   // TMEM lanes this warp may read
-  const int wrow = quad * 32 + lane;                            // weight row of this CTA
+  // This thread's weight row. The accumulator of a pair MMA with 128 rows holds a
+  // CTA's 64 rows twice over: lanes 64..127 hold the second half of the tokens.
+  const int wrow = C::HALF ? (quad & 1) * 32 + lane : quad * 32 + lane;
   const uint32_t lead_tempty = map_shared_to_rank(tempty0, 0);
   float* swap = reinterpret_cast<float*>(base_ptr + C::kSwapOff);
   uint32_t local = 0;
@@ -832,8 +875,11 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
     if (!epilogue_bar_and(ok)) break;
     tc_fence_after_sync();
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::TOK;
-    const int chunks = (t.rows + 31) >> 5;
-    const int col0 = t.col0 + static_cast<int>(rank) * C::kColsPerCta;
+    const int tok0 = C::HALF ? (quad >> 1) * (t.n / 2) : 0;   // this thread's first token
+    const int mine = C::HALF ? max(min(t.rows - tok0, t.n / 2), 0) : t.rows;
+    const int chunks = (mine + 31) >> 5;
+    const int col0 = t.col0 + static_cast<int>(rank) * p.cta_cols;
+    const int col_end = min(p.N, col0 + p.cta_cols);
     bool marked = false;
     if constexpr (C::KIND == kLora) {
       marked = marks[local % kMarks] != 0;
@@ -849,7 +895,7 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
       if constexpr (C::KIND == kLora) {
-        if (marked) add_unbounded<C>(p, t, c, col0 + wrow, v);
+        if (marked) add_unbounded<C>(p, t, t.row0 + tok0 + 32 * c, mine - 32 * c, col0 + wrow, v);
       }
     };
     auto release = [&]() {
@@ -859,9 +905,9 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
     };
     // 32 tokens of the tile from token 32 * c on: this lane's column.
     auto emit = [&](int c, const float (&v)[32]) {
-      const int row = t.row0 + 32 * c, valid = t.rows - 32 * c;
+      const int row = t.row0 + tok0 + 32 * c, valid = mine - 32 * c;
       if constexpr (C::KIND != kGated) {
-        store_tokens<32>(p.y, p.N, row, valid, col0 + wrow, v);
+        store_tokens<32>(p.y, p.N, row, valid, col0 + wrow, col_end, v);
       } else {
         // Quads 0 and 1 hold the gates, 2 and 3 the ups, of the same columns.
         // Each pair of warps swaps halves: the gate's warp finishes tokens
@@ -879,7 +925,7 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
           out[j] = gate / (1.f + __expf(-gate)) * mul;
         }
         named_sync(2 + pair, 64);   // read before the next chunk's halves come
-        store_tokens<16>(p.y, p.N, row + 16 * up, valid - 16 * up, col0 + pair * 32 + lane, out);
+        store_tokens<16>(p.y, p.N, row + 16 * up, valid - 16 * up, col0 + pair * 32 + lane, col_end, out);
       }
     };
 
@@ -893,15 +939,18 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
       continue;
     }
 
-    // A piece of a cut tile: publish the fp32 partial ([token][weight row]) and
+    // A piece of a cut tile: publish the fp32 partial ([token / 4][weight row][4]) and
     // count it; the piece that finds all others counted sums them in k order.
-    constexpr size_t kSlot = static_cast<size_t>(C::TOK) * 128;
+    constexpr size_t kSlot = static_cast<size_t>(C::TOK) * C::kRows;
+    const int place0 = C::HALF ? (quad >> 1) * (C::TOK / 8) * C::kRows + wrow : wrow;   // in float4
     float* slot = p.partials + (static_cast<size_t>(t.slot + t.piece) * 2 + rank) * kSlot;
     for (int c = 0; c < chunks; ++c) {
       float v[32];
       load(c, v);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) __stcg(slot + (32 * c + j) * 128 + wrow, v[j]);
+      for (int j = 0; j < 8; ++j)
+        __stcg(reinterpret_cast<float4*>(slot) + (8 * c + j) * C::kRows + place0,
+               make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
     }
     release();
     __threadfence();
@@ -913,15 +962,37 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
     epilogue_bar_sync();   // read by all before the next tile writes it
     if (!last) continue;
     __threadfence();
-    const float* first = p.partials + (static_cast<size_t>(t.slot) * 2 + rank) * kSlot;
+    const float4* first = reinterpret_cast<const float4*>(p.partials + (static_cast<size_t>(t.slot) * 2 + rank) * kSlot);
     for (int c = 0; c < chunks; ++c) {
-      float v[32];
+      float v[32] = {};
+      auto add = [&](const float4 (&f)[8]) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __ldcg(first + (32 * c + j) * 128 + wrow);
-      for (int s = 1; s < t.npieces; ++s) {
-        const float* src = first + static_cast<size_t>(s) * 2 * kSlot;
+        for (int j = 0; j < 8; ++j) {
+          v[4 * j] += f[j].x;
+          v[4 * j + 1] += f[j].y;
+          v[4 * j + 2] += f[j].z;
+          v[4 * j + 3] += f[j].w;
+        }
+      };
+      auto read = [&](int s, float4 (&f)[8]) {
+        const float4* src = first + static_cast<size_t>(s) * (2 * kSlot / 4);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += __ldcg(src + (32 * c + j) * 128 + wrow);
+        for (int j = 0; j < 8; ++j) f[j] = __ldcg(src + (8 * c + j) * C::kRows + place0);
+      };
+      // Two pieces' reads in flight; added in k order (0 + x is x, but for the
+      // sign of a zero).
+      int s = 0;
+      for (; s + 1 < t.npieces; s += 2) {
+        float4 f[8], h[8];
+        read(s, f);
+        read(s + 1, h);
+        add(f);
+        add(h);
+      }
+      if (s < t.npieces) {
+        float4 f[8];
+        read(s, f);
+        add(f);
       }
       emit(c, v);
     }
@@ -942,6 +1013,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
   const int warp = static_cast<int>(threadIdx.x) >> 5;
   const uint32_t rank = cluster_rank();
   const uint32_t bars = base + C::kBarsOff;
+  if (warp == 1) {
+    prefetch_tensormap(&p.tmap_w[0]);
+    if constexpr (!C::GATHER) prefetch_tensormap(&p.tmap_x[0]);
+    if constexpr (C::KIND == kLora) prefetch_tensormap(&p.tmap_b);
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::S; ++i) {
@@ -1021,7 +1097,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
 
 // Ring depths that fill shared memory.
 template <int KIND, bool GATHER, int TOK>
-using Instance = Cfg<KIND, GATHER, TOK, TOK == kRoutedSmall ? 5 : TOK == kRoutedMid ? 4 : 3>;
+using Instance = Cfg<KIND, GATHER, false, TOK, routed_kblocks(false, TOK),
+                     TOK == kRoutedSmall ? 5 : TOK == kRoutedMid ? 4 : 3>;
+// Few tokens: tiles of at most 128 weight rows.
+template <int TOK>
+using HalfInstance = Cfg<kLora, false, true, TOK, routed_kblocks(true, TOK),
+                         TOK == kRoutedMid ? 3 : 4>;
 
 template <class C>
 cudaError_t set_limit() {
@@ -1070,13 +1151,20 @@ cudaError_t prepare_routed_kernels() {
   if (e == cudaSuccess) e = set_limits<kGrouped, true>();
   if (e == cudaSuccess) e = set_limits<kGated, false>();
   if (e == cudaSuccess) e = set_limits<kGated, true>();
-  if (e == cudaSuccess) e = set_limits<kLora, false>();
+  if (e == cudaSuccess) e = set_limit<Instance<kLora, false, kRoutedWide>>();
+  if (e == cudaSuccess) e = set_limit<HalfInstance<kRoutedSmall>>();
+  if (e == cudaSuccess) e = set_limit<HalfInstance<kRoutedMid>>();
+  if (e == cudaSuccess) e = set_limit<HalfInstance<kRoutedWide>>();
   return e;
 }
 
-cudaError_t launch_routed(const RoutedParams& p, int kind, bool gather, int tokens, int ctas,
+cudaError_t launch_routed(const RoutedParams& p, int kind, bool gather, bool half, int tokens, int ctas,
                           cudaStream_t stream) {
-  if (kind == kLora) return launch_kind<kLora, false>(p, tokens, ctas, stream);
+  if (kind == kLora && !half) return launch_one<Instance<kLora, false, kRoutedWide>>(p, ctas, stream);
+  if (kind == kLora)
+    return tokens == kRoutedSmall ? launch_one<HalfInstance<kRoutedSmall>>(p, ctas, stream)
+           : tokens == kRoutedMid ? launch_one<HalfInstance<kRoutedMid>>(p, ctas, stream)
+                                  : launch_one<HalfInstance<kRoutedWide>>(p, ctas, stream);
   if (kind == kGated)
     return gather ? launch_kind<kGated, true>(p, tokens, ctas, stream)
                   : launch_kind<kGated, false>(p, tokens, ctas, stream);

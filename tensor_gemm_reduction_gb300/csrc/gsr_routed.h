@@ -31,12 +31,12 @@ constexpr int kAdapterListStride = kRoutedMaxTokens + 8;
 
 struct RoutedParams {  // 128-byte aligned through its CUtensorMap members
   // Weights. Grouped: tmap_w[0] = W as {K, rows, E}, boxes of 64 x 128 rows (64
-  // rows when gated). Lora: tmap_w[r] = W_r, boxes of 64 x 128.
+  // rows when gated). Lora: tmap_w[r] = W_r, boxes of 64 x w_rows.
   CUtensorMap tmap_w[kMaxShards];
   // Tokens. Grouped: tmap_x[i] = X in boxes of 64 x 8 (i + 1) rows (none when the
   // rows are gathered). Lora: tmap_x[r] = X_r in boxes of 64 x tile_tokens / 2.
   CUtensorMap tmap_x[kMaxShards];
-  CUtensorMap tmap_b;               // lora: B as {rank, N, L}, boxes of unit_cols x 128
+  CUtensorMap tmap_b;               // lora: B as {rank, N, L}, boxes of unit_cols x w_rows
 
   const int32_t* offsets;           // grouped: E + 1 row offsets
   const int32_t* rows;              // grouped: row of X of each row of Y (gathered)
@@ -53,6 +53,7 @@ struct RoutedParams {  // 128-byte aligned through its CUtensorMap members
 
   int E, M, N, K, T, R, L, rank;       // T: rows of X (grouped)
   int n_tiles;                      // tiles of output columns
+  int cta_cols, w_rows;             // output columns and weight rows of a CTA's part of a tile
   int stages_per_tile;              // ring stages of a whole tile (the base product)
   int m_tiles, tile_tokens;         // lora: token tiles and their width
   int max_pieces, min_piece;        // of a cut tile: pieces at most, stages at least
@@ -99,14 +100,16 @@ struct CombineParams {
 
 // Token capacities of the routed product's instances.
 constexpr int kRoutedSmall = 64, kRoutedMid = 128, kRoutedWide = 256;
-// k-blocks of 64 in one ring stage: a stage costs its barrier's fixed time, so one
-// k-block per stage is 10 to 20 % slower at 256 tokens.
-constexpr int kRoutedKblocks = 2;
+// k-blocks of 64 in one ring stage. A stage costs its barriers' fixed time (about
+// 200 ns), so it should carry many bytes: with one k-block per stage the 256-token
+// tiles are 10 to 20 % slower. The half tiles carry few weight rows, so four.
+constexpr int routed_kblocks(bool half, int tokens) { return half && tokens <= kRoutedMid ? 4 : 2; }
 
 cudaError_t prepare_routed_kernels();
 cudaError_t prepare_lowrank_kernels();
 cudaError_t prepare_route_kernels();
-cudaError_t launch_routed(const RoutedParams& p, int kind, bool gather, int tokens, int ctas,
+// half: tiles of at most 128 weight rows (kLora).
+cudaError_t launch_routed(const RoutedParams& p, int kind, bool gather, bool half, int tokens, int ctas,
                           cudaStream_t stream);
 cudaError_t launch_low_rank(const LowRankParams& p, cudaStream_t stream);
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);

@@ -25,7 +25,8 @@ using gsr::round256;
 
 namespace {
 
-constexpr int kStageK = gsr::kRoutedKblocks * BK;   // k of one ring stage
+// k of one ring stage.
+int stage_k(bool half, int tokens) { return gsr::routed_kblocks(half, tokens) * BK; }
 
 // CTA pairs a launch may use.
 int64_t pairs_of(const gemm_shard_plan* P) {
@@ -156,7 +157,7 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
                      : mean <= gsr::kRoutedMid ? gsr::kRoutedMid
                                                : gsr::kRoutedWide;
   const int64_t ctas = 2 * std::min<int64_t>(pairs_of(P), (cdiv(M, tokens) + E) * n_tiles *
-                                                              cdiv(K, 2 * kStageK));
+                                                              cdiv(K, 2 * stage_k(false, tokens)));
   if (gsr::log_config_enabled())
     std::fprintf(stderr, "gsr: %s M=%lld N=%lld K=%lld E=%d gather=%d kernel=routed tokens=%d ctas=%lld\n",
                  kind == gsr::kGated ? "grouped_gated" : "grouped", (long long)M, (long long)N,
@@ -166,7 +167,7 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
 
   gsr::RoutedParams p;
   std::memset(&p, 0, sizeof p);
-  fill_routed(p, P, M, N, static_cast<int>(cdiv(K, kStageK)), tokens, ws);
+  fill_routed(p, P, M, N, static_cast<int>(cdiv(K, stage_k(false, tokens))), tokens, ws);
   p.E = E;
   p.T = static_cast<int>(T);
   p.K = static_cast<int>(K);
@@ -175,6 +176,8 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
   p.rows = rows;
   p.y = static_cast<uint16_t*>(Y);
   p.n_tiles = static_cast<int>(n_tiles);
+  p.cta_cols = kind == gsr::kGated ? 64 : 128;
+  p.w_rows = 128;
   p.policy_w = tokens == gsr::kRoutedWide ? gsr::kPolicyNormal : gsr::kPolicyEvictFirst;
   p.policy_x = tokens == gsr::kRoutedWide ? gsr::kPolicyNormal : gsr::kPolicyEvictLast;
   CUresult cr = encode_stack(&p.tmap_w[0], W, E, wide, K, BK, kind == gsr::kGated ? 64 : 128);
@@ -185,7 +188,7 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
   if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding the X descriptor failed (%d)", (int)cr);
   DeviceScope scope(P->device);
   if (scope.err != cudaSuccess) return cuda_fail(scope.err, "selecting the plan's device");
-  cudaError_t e = gsr::launch_routed(p, kind, rows != nullptr, tokens, static_cast<int>(ctas),
+  cudaError_t e = gsr::launch_routed(p, kind, rows != nullptr, false, tokens, static_cast<int>(ctas),
                                      reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
   return ok();
@@ -327,14 +330,25 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
   if (s) return s;
   if (M == 0) return ok();
 
-  // The instance by the rows of a token tile: up to 256 rows run as one.
+  // Up to 256 rows run as one token tile, a stream of weights: tiles of at most
+  // 128 weight rows, as few as spread N over the pairs in the fewest waves (N = 7168
+  // on 76 pairs: 96 rows, 75 tiles, none cut; at M = 128, cutting 256-row tiles
+  // instead spent 10 us of 40 on the partials). Fewer than 64 rows make the copies
+  // too small: then tiles are cut.
+  const bool half = M <= gsr::kRoutedWide;
   const int tokens = M <= gsr::kRoutedSmall ? gsr::kRoutedSmall
                      : M <= gsr::kRoutedMid ? gsr::kRoutedMid
                                             : gsr::kRoutedWide;
   const int64_t m_tiles = cdiv(M, tokens);
   const int64_t width = cdiv(cdiv(M, m_tiles), 16) * 16;
-  const int64_t n_tiles = cdiv(N, gsr::kRoutedTileRows);
+  int64_t tile_rows = gsr::kRoutedTileRows;
+  if (half) {
+    const int64_t waves = cdiv(N, 128 * pairs_of(P));
+    tile_rows = std::min<int64_t>(128, std::max<int64_t>(64, cdiv(cdiv(N, waves * pairs_of(P)), 16) * 16));
+  }
+  const int64_t n_tiles = cdiv(N, tile_rows);
   if (m_tiles * n_tiles > INT32_MAX / 2) return fail(GSR_ERR_INVALID_VALUE, "M and N give too many tiles");
+  const int kStageK = stage_k(half, tokens);
   int64_t stages = 0;
   for (int r = 0; r < R; ++r) stages += cdiv(K_r[r], kStageK);
   const int64_t ctas = 2 * std::min(pairs_of(P), m_tiles * n_tiles * cdiv(stages, 2));
@@ -360,6 +374,8 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
   p.lists = lists;
   p.y = static_cast<uint16_t*>(Y);
   p.n_tiles = static_cast<int>(n_tiles);
+  p.cta_cols = p.w_rows = static_cast<int>(tile_rows / 2);
+  if (half) p.whole_from = static_cast<int>(cdiv(3 * pairs_of(P), 5));
   p.m_tiles = static_cast<int>(m_tiles);
   p.tile_tokens = static_cast<int>(width);
   p.unit_cols = rank <= 16 ? 16 : rank <= 32 ? 32 : 64;
@@ -378,7 +394,7 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
     q.x[r] = static_cast<const uint16_t*>(X_r[r]);
     q.a[r] = static_cast<const uint16_t*>(A_r[r]);
     q.k[r] = K_r[r];
-    CUresult cr = encode_2d(&p.tmap_w[r], W_r[r], N, K_r[r], 128);
+    CUresult cr = encode_2d(&p.tmap_w[r], W_r[r], N, K_r[r], p.w_rows);
     if (cr == CUDA_SUCCESS) cr = encode_2d(&p.tmap_x[r], X_r[r], M, K_r[r], static_cast<int>(width / 2));
     if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding shard %d's descriptors failed (%d)", r, (int)cr);
   }
@@ -386,7 +402,7 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
     p.shard_st_begin[r] = st;
     q.unit_begin[r] = unit;
   }
-  CUresult cr = encode_stack(&p.tmap_b, B, L, N, rank, p.unit_cols, 128);
+  CUresult cr = encode_stack(&p.tmap_b, B, L, N, rank, p.unit_cols, p.w_rows);
   if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding the B descriptor failed (%d)", (int)cr);
   q.adapter = adapter;
   q.scale = scale;
@@ -405,7 +421,7 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
   if (scope.err != cudaSuccess) return cuda_fail(scope.err, "selecting the plan's device");
   cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = gsr::launch_low_rank(q, st_);
-  if (e == cudaSuccess) e = gsr::launch_routed(p, gsr::kLora, false, tokens, static_cast<int>(ctas), st_);
+  if (e == cudaSuccess) e = gsr::launch_routed(p, gsr::kLora, false, half, tokens, static_cast<int>(ctas), st_);
   if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
   return ok();
 }
