@@ -97,21 +97,32 @@ __device__ void write_list(const LowRankParams& p, int tile, uint32_t* bits, int
     for (uint32_t b = bits[w]; b; b &= b - 1u) list[1 + at++] = 32 * w + __ffs(b) - 1;
 }
 
-// NT: 8-column tiles of the padded rank. SPLIT: the warps of a CTA share k (16
-// rows per CTA) or take 16 rows each (128 rows per CTA).
+// NT: 8-column tiles of a pass over the padded rank (128 columns take two passes of
+// 64). SPLIT: the warps of a CTA share k (16 rows per CTA) or take 16 rows each
+// (128 rows per CTA).
+//
+// The shares go through shared memory 32 columns at a time.
+constexpr int kShareCols = 32;
+constexpr int kSmemBytes = kWarps * 16 * kShareCols * 4;
+static_assert(kSmemBytes >= kMaxAdapters / 8, "a bit per adapter");
+
 template <int NT, bool SPLIT>
 __global__ void __launch_bounds__(kThreadsLow, NT <= 4 ? 3 : 2) gsr_lowrank_kernel(const __grid_constant__ LowRankParams p) {
-  extern __shared__ float share[];                 // [kWarps][16][8 * NT]
+  extern __shared__ float share[];                 // [kWarps][16][columns of a turn]
   __shared__ int ids[kWarps], keeps[16 * kWarps];
-  constexpr int kCols = 8 * NT;
+  constexpr int kCols = 8 * NT < kShareCols ? 8 * NT : kShareCols, kTurnTiles = kCols / 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int z = static_cast<int>(blockIdx.z), ctas = static_cast<int>(gridDim.z);
   const int blocks = (p.M + (SPLIT ? 16 : 16 * kWarps) - 1) / (SPLIT ? 16 : 16 * kWarps);
   if (static_cast<int>(blockIdx.x) >= blocks) {   // whole clusters
-    if (blockIdx.y == 0 && z == 0)
-      write_list(p, static_cast<int>(blockIdx.x) - blocks, reinterpret_cast<uint32_t*>(share), ids);
+    if (blockIdx.y == 0)
+      for (int tile = (static_cast<int>(blockIdx.x) - blocks) * ctas + z; tile < p.m_tiles;
+           tile += (static_cast<int>(gridDim.x) - blocks) * ctas) {
+        write_list(p, tile, reinterpret_cast<uint32_t*>(share), ids);
+        __syncthreads();
+      }
     return;
   }
 
@@ -143,92 +154,94 @@ __global__ void __launch_bounds__(kThreadsLow, NT <= 4 ? 3 : 2) gsr_lowrank_kern
     uint32_t left = leaders;
     for (int i = 0; i < turn; ++i) left &= left - 1u;
     const int a = left ? __shfl_sync(0xffffffffu, id, __ffs(left) - 1) : -1;
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    if (a >= 0) {
-      for (int r = 0; r < p.R; ++r) {
-        const int lo = max(u0, p.unit_begin[r]), hi = min(u1, p.unit_begin[r + 1]);
-        if (lo >= hi) continue;
-        const int64_t K = p.k[r];
-        int k = (lo - p.unit_begin[r]) * kUnit + quad * 8;
-        const int k_end = min(static_cast<int>(K), (hi - p.unit_begin[r]) * kUnit);
-        const uint16_t* xa = p.x[r] + static_cast<int64_t>(row0 + group) * K;
-        const uint16_t* xb = xa + 8 * K;
-        const uint16_t* aa = p.a[r] + (static_cast<int64_t>(a) * p.rank + group) * K;
-#pragma unroll 2
-        for (; k - quad * 8 < k_end; k += 32) {
-          const bool in = k < k_end;
-          const uint4 f = load16(xa + k, in && row_a);
-          const uint4 s = load16(xb + k, in && row_b);
-          uint4 b[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            b[n] = load16(aa + static_cast<int64_t>(8 * n) * K + k, in && 8 * n + group < p.rank);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_16816(acc[n], f.x, s.x, f.y, s.y, b[n].x, b[n].y);
-            mma_16816(acc[n], f.z, s.z, f.w, s.w, b[n].z, b[n].w);
-          }
-        }
-      }
-    }
-    float* mine = share + warp * (16 * kCols);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      mine[group * kCols + 8 * n + 2 * quad] = acc[n][0];
-      mine[group * kCols + 8 * n + 2 * quad + 1] = acc[n][1];
-      mine[(group + 8) * kCols + 8 * n + 2 * quad] = acc[n][2];
-      mine[(group + 8) * kCols + 8 * n + 2 * quad + 1] = acc[n][3];
-    }
     if constexpr (!SPLIT) {
       if (lane < 16) keeps[warp * 16 + lane] = a >= 0 && id == a ? a : -1;   // rows to keep
     } else {
       if (warp == 0 && lane < 16) keeps[lane] = id == a ? a : -1;
     }
-    cluster_sync_all();
-    // Each CTA of the cluster adds up a share of the elements, in k order.
-    constexpr int kElems = (SPLIT ? 16 : 16 * kWarps) * kCols;
-    for (int e = z * kThreadsLow + tid; e < kElems; e += ctas * kThreadsLow) {
-      const int row = e / kCols, col = e - row * kCols;
-      const int keep = keeps[row];
-      if (keep < 0) continue;
-      float sum = 0.f;
-      for (int c = 0; c < ctas; ++c) {
-        const uint32_t at = cluster_shared_addr(share, static_cast<uint32_t>(c));
+    for (int pass = 0; pass < p.rank_pad; pass += 8 * NT) {
+      float acc[NT][4];
 #pragma unroll
-        for (int w = 0; w < (SPLIT ? kWarps : 1); ++w) {
-          float v;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                       : "=f"(v)
-                       : "r"(at + 4u * static_cast<uint32_t>(SPLIT ? w * kElems + e : e)));
-          sum += v;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+      if (a >= 0) {
+        for (int r = 0; r < p.R; ++r) {
+          const int lo = max(u0, p.unit_begin[r]), hi = min(u1, p.unit_begin[r + 1]);
+          if (lo >= hi) continue;
+          const int64_t K = p.k[r];
+          int k = (lo - p.unit_begin[r]) * kUnit + quad * 8;
+          const int k_end = min(static_cast<int>(K), (hi - p.unit_begin[r]) * kUnit);
+          const uint16_t* xa = p.x[r] + static_cast<int64_t>(row0 + group) * K;
+          const uint16_t* xb = xa + 8 * K;
+          const uint16_t* aa = p.a[r] + (static_cast<int64_t>(a) * p.rank + pass + group) * K;
+#pragma unroll 2
+          for (; k - quad * 8 < k_end; k += 32) {
+            const bool in = k < k_end;
+            const uint4 f = load16(xa + k, in && row_a);
+            const uint4 s = load16(xb + k, in && row_b);
+            uint4 b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              b[n] = load16(aa + static_cast<int64_t>(8 * n) * K + k, in && pass + 8 * n + group < p.rank);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_16816(acc[n], f.x, s.x, f.y, s.y, b[n].x, b[n].y);
+              mma_16816(acc[n], f.z, s.z, f.w, s.w, b[n].z, b[n].w);
+            }
+          }
         }
       }
-      const float s = p.scale ? __ldg(p.scale + keep) : 1.f;
-      const int m = static_cast<int>(blockIdx.x) * (SPLIT ? 16 : 16 * kWarps) + row;
-      p.low[static_cast<size_t>(m) * p.rank_pad + col] =
-          __bfloat16_as_ushort(__float2bfloat16(sum * s));
+#pragma unroll
+      for (int n0 = 0; n0 < NT; n0 += kTurnTiles) {
+        float* mine = share + warp * (16 * kCols);
+#pragma unroll
+        for (int n = 0; n < kTurnTiles; ++n) {
+          const float* c = acc[n0 + n];
+          *reinterpret_cast<float2*>(mine + group * kCols + 8 * n + 2 * quad) = make_float2(c[0], c[1]);
+          *reinterpret_cast<float2*>(mine + (group + 8) * kCols + 8 * n + 2 * quad) = make_float2(c[2], c[3]);
+        }
+        cluster_sync_all();
+        // Each CTA of the cluster adds up a share of the elements, in k order.
+        constexpr int kElems = (SPLIT ? 16 : 16 * kWarps) * kCols;
+        for (int e = z * kThreadsLow + tid; e < kElems; e += ctas * kThreadsLow) {
+          const int row = e / kCols, col = pass + 8 * n0 + e - row * kCols;
+          const int keep = keeps[row];
+          if (keep < 0) continue;
+          float sum = 0.f;
+          for (int c = 0; c < ctas; ++c) {
+            const uint32_t at = cluster_shared_addr(share, static_cast<uint32_t>(c));
+#pragma unroll
+            for (int w = 0; w < (SPLIT ? kWarps : 1); ++w) {
+              float v;
+              asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                           : "=f"(v)
+                           : "r"(at + 4u * static_cast<uint32_t>(SPLIT ? w * kElems + e : e)));
+              sum += v;
+            }
+          }
+          const float s = p.scale ? __ldg(p.scale + keep) : 1.f;
+          const int m = static_cast<int>(blockIdx.x) * (SPLIT ? 16 : 16 * kWarps) + row;
+          p.low[static_cast<size_t>(m) * p.rank_pad + col] =
+              __bfloat16_as_ushort(__float2bfloat16(sum * s));
+        }
+        cluster_sync_all();   // read by all before the next share is written
+      }
     }
-    cluster_sync_all();   // read by all before the next turn writes
   }
 }
-
-// The warps' shares, or a bit per adapter.
-template <int NT>
-constexpr int smem_bytes() { return kWarps * 16 * 8 * NT * 4 > kMaxAdapters / 8 ? kWarps * 16 * 8 * NT * 4 : kMaxAdapters / 8; }
 
 template <int NT, bool SPLIT>
 cudaError_t launch_nt(const LowRankParams& p, cudaStream_t stream) {
   const int rows = SPLIT ? 16 : 16 * kWarps, blocks = (p.M + rows - 1) / rows;
-  // 16 rows have at most 16 adapters, each a turn of its own. k is cut until the
-  // CTAs are about four times the SMs (the reduction over a cluster costs more).
+  // 16 rows have at most 16 adapters, each a turn of its own. k is cut among the
+  // CTAs of a cluster until they are about four times the SMs (the reduction over a
+  // cluster costs more).
   const int turns = SPLIT ? std::min(16, std::min(p.L, p.M)) : 1;
   int cluster = kMaxCluster;
   if (SPLIT)
     while (cluster > 1 && blocks * turns * cluster > 608) cluster /= 2;
+  const int list_blocks = (std::min(p.m_tiles, 16) + cluster - 1) / cluster;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -237,43 +250,23 @@ cudaError_t launch_nt(const LowRankParams& p, cudaStream_t stream) {
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = cluster;
-  cfg.gridDim = dim3(blocks + p.m_tiles, turns, cluster);
+  cfg.gridDim = dim3(blocks + list_blocks, turns, cluster);
   cfg.blockDim = dim3(kThreadsLow, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes<NT>();
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, gsr_lowrank_kernel<NT, SPLIT>, p);
 }
 
-template <int NT>
-cudaError_t set_limit() {
-  cudaError_t e = cudaFuncSetAttribute(gsr_lowrank_kernel<NT, true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_bytes<NT>());
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(gsr_lowrank_kernel<NT, false>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smem_bytes<NT>());
-}
-
 }  // namespace
-
-cudaError_t prepare_lowrank_kernels() {
-  cudaError_t e = set_limit<2>();
-  if (e == cudaSuccess) e = set_limit<4>();
-  if (e == cudaSuccess) e = set_limit<8>();
-  if (e == cudaSuccess) e = set_limit<16>();
-  return e;
-}
 
 cudaError_t launch_low_rank(const LowRankParams& p, cudaStream_t stream) {
   const bool split = p.rows_per_cta == 16;
   switch (p.rank_pad) {
     case 16: return split ? launch_nt<2, true>(p, stream) : launch_nt<2, false>(p, stream);
     case 32: return split ? launch_nt<4, true>(p, stream) : launch_nt<4, false>(p, stream);
-    case 64: return split ? launch_nt<8, true>(p, stream) : launch_nt<8, false>(p, stream);
-    default: return split ? launch_nt<16, true>(p, stream) : launch_nt<16, false>(p, stream);
+    default: return split ? launch_nt<8, true>(p, stream) : launch_nt<8, false>(p, stream);
   }
 }
 

@@ -26,9 +26,11 @@
 // sum stays in the same fp32 accumulator. Those masked rows exist in shared
 // memory alone.
 //
-// Epilogue: a thread holds one output column of 32 tokens; neighbouring lanes
-// exchange halves so that each store writes two columns of one row (64-byte
-// segments per row and warp).
+// Epilogue: a warp takes 32 output columns of 32 tokens at a time from TMEM in
+// the fragment layout of 8 x 8 matrices, writes them transposed to 2 KB of shared
+// memory of its own (stmatrix) and stores them as 16-byte vectors, 64 bytes per
+// row. (Stores of two columns straight from registers took 6.3 us for 256 tokens
+// x 128 columns, more than the MMAs of a tile at K = 896.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,7 +44,6 @@ namespace {
 
 constexpr int kEpi = 128;              // epilogue threads
 constexpr int kPlacers = 4;            // warps that place (or gather) the rows of a stage
-constexpr int kTeams = 2;              // kLora: teams of them, on alternate stages
 constexpr uint32_t kRolePlacer = 4;
 // kLora: tiles in flight between the placing warps and the epilogue, at most: a
 // ring of single-stage tiles and two accumulators.
@@ -74,6 +75,25 @@ __device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool real
 __device__ __forceinline__ void sign_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+// 32 TMEM columns of 16 lanes: v[4 g + e] is column 8 g + 2 (lane % 4) + e % 2 of
+// lane (lane / 4) + 8 (e / 2).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit elements, transposed: lane l gives the address of
+// row l % 8 of matrix l / 8.
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                 uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 __device__ __forceinline__ void arm(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
@@ -101,8 +121,9 @@ template <int KIND_, bool GATHER_, bool HALF_, int TOK_, int KZ_, int STAGES_>
 struct Cfg {
   static constexpr int KIND = KIND_, TOK = TOK_, S = STAGES_, KZ = KZ_;
   static constexpr bool GATHER = GATHER_, HALF = HALF_;
+  static constexpr int kTeams = HALF ? 2 : 1;           // kLora: of four warps that place rows
   static constexpr int kRows = HALF ? 64 : 128;         // weight rows of a CTA, at most
-  static constexpr int kThreads = 64 + kEpi + (KIND == kLora ? 32 * kPlacers * kTeams : GATHER ? 32 * (kPlacers + 1) : 0);
+  static constexpr int kThreads = 64 + kEpi + (KIND == kLora ? 32 * kPlacers : GATHER ? 32 * (kPlacers + 1) : 0);
   // Arrivals that complete a full barrier: the leader's expect_tx and, from both
   // CTAs, the placing warps or the warp that signs for the gathered rows.
   static constexpr uint32_t kSigns = 1 + (KIND == kLora ? 2 * kPlacers : GATHER ? 2 : 0);
@@ -115,11 +136,11 @@ struct Cfg {
   static constexpr uint32_t kBars = (2 * S + 5 + (KIND == kLora || GATHER ? S : 0)) * 8;
   static constexpr uint32_t kLandedOff = (2 * S + 5) * 8;
   static constexpr uint32_t kGroups = KIND == kLora ? 0 : 4 * (3 * kMaxGroups + 1 + 32);
-  static constexpr uint32_t kSwap = KIND == kGated ? 2 * 2 * 16 * 32 * 4 : 0;
+  static constexpr uint32_t kStaging = 4 * 2048;        // 2 KB per epilogue warp
   static constexpr uint32_t kBarsOff = kRing;
   static constexpr uint32_t kMiscOff = kBarsOff + kBars;
-  static constexpr uint32_t kSwapOff = (kMiscOff + 16 + 4 * kMarks + 127) / 128 * 128;
-  static constexpr uint32_t kGroupsOff = kSwapOff + kSwap;
+  static constexpr uint32_t kStagingOff = (kMiscOff + 16 + 4 * kMarks + 127) / 128 * 128;
+  static constexpr uint32_t kGroupsOff = kStagingOff + kStaging;
   static constexpr uint32_t kSmem = 1024 + kGroupsOff + kGroups;
   static_assert(kSmem <= kSmallSmemLimit, "shared memory");
   static_assert(kX % 1024 == 0, "swizzle atoms");
@@ -701,7 +722,7 @@ __device__ __forceinline__ bool place_stage(const RoutedParams& p, AdapterSteps&
   for (int u = who >> 5; u < units; u += kPlacers) {
     const uint32_t unit = sw + u * kUnitW;
     for (uint32_t at = 16u * lane; at < bytes; at += 4 * 512) {
-      uint32_t w[4][4], any = 0;
+      uint32_t w[4][4], sum[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         w[q][0] = w[q][1] = w[q][2] = w[q][3] = 0;
@@ -711,12 +732,13 @@ __device__ __forceinline__ bool place_stage(const RoutedParams& p, AdapterSteps&
                        : "r"(unit + at + q * 512)
                        : "memory");
       }
-      // Bits 15 and 31 of (w & exponents) + 1 exponent step: an exponent of all ones.
+      // x * 0 + sum is 0 for finite x, NaN for the others.
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) any |= (w[q][j] & 0x7f807f80u) + 0x00800080u;
-      if (any & 0x80008000u) {
+        for (int j = 0; j < 4; ++j)
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[q]) : "r"(w[q][j]), "r"(0u));
+      if (((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0) {
         marked = true;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -736,80 +758,111 @@ __device__ __forceinline__ bool place_stage(const RoutedParams& p, AdapterSteps&
   return marked;
 }
 
-// The low-rank rows of the ring's adapter stages. Two teams of four warps take
-// alternate stages. A team's threads are the rows of this CTA's tokens, or, with
-// at most 64 or 32 rows, two or four times the rows, on alternate adapters. Every
-// warp signs the stage on the leader's full barrier. A stage is theirs once its adapter weights have landed (the producer had waited for the
-// slot); the base product's stages pass them by.
+// The adapter stages of one tile, for one team of four warps (thread `i` of
+// them). The threads are the rows of this CTA's tokens, or, with at most 64 or 32
+// rows, two or four times the rows, on alternate adapters. Every warp signs the
+// stage on the leader's full barrier. A stage is the teams' once its adapter
+// weights have landed (the producer had waited for the slot); the base product's
+// stages pass them by. Teams take alternate stages, but follow every one, so that
+// none takes a slot's next phase for the one that it waits for.
+struct Placing {
+  Ring ring;
+  uint32_t phases = 0;   // bit s: phase of slot s's landed barrier
+};
+template <int TEAM, class C>
+__device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local, Placing& q, int i,
+                           uint32_t base, uint32_t rank, volatile int* marks, const Ctl& ctl) {
+  const int lane = i & 31;
+  const uint32_t full0 = base + C::kBarsOff;
+  const uint32_t lead0 = map_shared_to_rank(full0, 0);
+  q.ring.slot = (q.ring.slot + static_cast<uint32_t>(t.st_end - t.st)) % C::S;
+  AdapterSteps a{};
+  a.template begin<C>(p, t);
+  if (a.st >= a.st_end) return true;
+  const int half = t.n / 2, ways = half <= 32 ? 4 : half <= 64 ? 2 : 1;
+  const int row = i & (32 * kPlacers / ways - 1), m = t.row0 + static_cast<int>(rank) * half + row;
+  int id = -1;
+  uint4 v[kMaxRank / 8];
+  if (row < half && m < p.M) id = p.adapter[m];
+  if (id >= p.L) id = -1;   // no adapter of the list is negative
+#pragma unroll
+  for (int c = 0; c < kMaxRank / 8; ++c)
+    v[c] = id >= 0 && 8 * c < p.rank_pad
+               ? __ldcg(reinterpret_cast<const uint4*>(p.low + static_cast<size_t>(m) * p.rank_pad) + c)
+               : make_uint4(0, 0, 0, 0);
+  for (int st = a.st; st < a.st_end; ++st) {
+    bool ok = wait_bounded(full0 + C::kLandedOff + 8 * q.ring.slot, (q.phases >> q.ring.slot) & 1u, ctl,
+                           (kRolePlacer << 8) | 2);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    q.phases ^= 1u << q.ring.slot;
+    if ((st - a.st) % C::kTeams == TEAM) {
+      const uint32_t sw = base + q.ring.slot * C::kStage;
+      const bool marked = p.unit_cols == 16   ? place_stage<16, C>(p, a, sw, st, id, i, row, ways, half, v)
+                          : p.unit_cols == 32 ? place_stage<32, C>(p, a, sw, st, id, i, row, ways, half, v)
+                                              : place_stage<64, C>(p, a, sw, st, id, i, row, ways, half, v);
+      if (marked) marks[local % kMarks] = 1;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) sign_pair(lead0 + 8 * q.ring.slot);
+    }
+    q.ring.template next<C::S>();
+  }
+  return true;
+}
+
+// The placing warps: team 0 of every tile. With half tiles, the epilogue's warps,
+// which then wait for the accumulator, are team 1.
 template <class C>
 __device__ void place_rows(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
                            uint32_t rank, volatile int* marks, const Ctl& ctl) {
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const int who = static_cast<int>(threadIdx.x) - 64 - kEpi;
-  const int team = who / (32 * kPlacers), i = who % (32 * kPlacers);
-  const uint32_t full0 = base + C::kBarsOff;
-  const uint32_t lead0 = map_shared_to_rank(full0, 0);
-  Ring ring;
-  bool ok = true;
-  uint32_t landed_phase = 0, local = 0;   // bit s: phase of slot s's landed barrier
+  const int i = static_cast<int>(threadIdx.x) - 64 - kEpi;
   Walk walk;
   walk.begin(p, tiles);
   Tile t;
-  grid_dependency_wait();
-  for (; ok && walk.step<C>(p, g, t); ++local) {
-    ring.slot = (ring.slot + static_cast<uint32_t>(t.st_end - t.st)) % C::S;
-    AdapterSteps a{};
-    a.template begin<C>(p, t);
-    if (a.st >= a.st_end) continue;
-    const int half = t.n / 2, ways = half <= 32 ? 4 : half <= 64 ? 2 : 1;
-    const int row = i & (32 * kPlacers / ways - 1), m = t.row0 + static_cast<int>(rank) * half + row;
-    int id = -1;
-    uint4 v[kMaxRank / 8];
-    if (row < half && m < p.M) id = p.adapter[m];
-    if (id >= p.L) id = -1;   // no adapter of the list is negative
-#pragma unroll
-    for (int c = 0; c < kMaxRank / 8; ++c)
-      v[c] = id >= 0 && 8 * c < p.rank_pad
-                 ? __ldcg(reinterpret_cast<const uint4*>(p.low + static_cast<size_t>(m) * p.rank_pad) + c)
-                 : make_uint4(0, 0, 0, 0);
-    for (int st = a.st; st < a.st_end; ++st) {
-      // Both teams follow every stage, so that neither takes a slot's next phase
-      // for the one that it waits for.
-      ok = wait_bounded(full0 + C::kLandedOff + 8 * ring.slot, (landed_phase >> ring.slot) & 1u, ctl,
-                        (kRolePlacer << 8) | 2);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      landed_phase ^= 1u << ring.slot;
-      if (((st - a.st) & 1) == team) {
-        const uint32_t sw = base + ring.slot * C::kStage;
-        const bool marked = p.unit_cols == 16   ? place_stage<16, C>(p, a, sw, st, id, i, row, ways, half, v)
-                            : p.unit_cols == 32 ? place_stage<32, C>(p, a, sw, st, id, i, row, ways, half, v)
-                                                : place_stage<64, C>(p, a, sw, st, id, i, row, ways, half, v);
-        if (marked) marks[local % kMarks] = 1;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) sign_pair(lead0 + 8 * ring.slot);
+  if constexpr (C::HALF) {
+    // The adapters' weights for the first tile's columns, into L2 while the base
+    // product streams: read at its end, each would wait for memory. The ids are
+    // the caller's, so they may be read at once; repeats are found per warp.
+    if (walk.step<C>(p, g, t)) {
+      const int col = t.col0 + static_cast<int>(rank) * p.cta_cols;
+      const uint32_t bytes = 2u * static_cast<uint32_t>(max(min(p.cta_cols, p.N - col), 0)) * p.rank;
+      for (int m = i; m < p.M && bytes; m += 32 * kPlacers) {
+        const int id = p.adapter[m];
+        const uint32_t same = __match_any_sync(__activemask(), id);
+        if (id >= 0 && id < p.L && (i & 31) == __ffs(same) - 1)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                           p.b + (static_cast<size_t>(id) * p.N + col) * p.rank),
+                       "r"(bytes)
+                       : "memory");
       }
-      ring.next<C::S>();
+      __syncwarp();
     }
+    walk.begin(p, tiles);
   }
+  grid_dependency_wait();
+  Placing q;
+  for (uint32_t local = 0; walk.step<C>(p, g, t); ++local)
+    if (!place_tile<0, C>(p, t, local, q, i, base, rank, marks, ctl)) break;
 }
 
 // The products of adapter weights that are not finite, which the placing warps
-// took out of the tile: column `col` of `valid` (or 32) rows from row0 on, for
-// the adapters of this piece.
+// took out of the tile, added to a warp's fragments v of 32 tokens x 32 columns
+// (`valid` rows from `row` on, columns from `col` to `end`), for the adapters of
+// this piece.
 template <class C>
-__device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t, int row0, int valid, int col,
-                                           float (&v)[32]) {
+__device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t, int row, int valid, int col,
+                                           int end, float (&v)[32]) {
   AdapterSteps a{};
   a.template begin<C>(p, t);
   const int u0 = a.st * a.per_stage, u1 = min(a.st_end * a.per_stage, a.units);
-  if (col >= p.N) return;
+  const int lane = static_cast<int>(threadIdx.x) & 31;
 #pragma unroll 1
-  for (int j = 0; j < 32; ++j) {
-    const int m = row0 + j;
-    if (j >= valid) break;
-    const int id = p.adapter[m];
+  for (int i = 0; i < 32; ++i) {
+    const int token = 8 * ((i >> 2) & 3) + 2 * (lane & 3) + (i & 1);
+    const int n = col + 16 * (i >> 4) + 8 * ((i >> 1) & 1) + (lane >> 2);
+    const int m = row + token;
+    const int id = token < valid && n < end ? p.adapter[m] : -1;
     if (id < 0 || id >= p.L) continue;
     int at = 0;
     while (__ldcg(a.list + 1 + at) != id) ++at;   // the tile's list has every row's adapter
@@ -818,35 +871,42 @@ __device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t,
     for (int k = 0; k < p.rank; ++k) {
       const int u = at * p.units_per_adapter + k / p.unit_cols;
       if (u < u0 || u >= u1) continue;
-      const uint32_t w = p.b[(static_cast<size_t>(id) * p.N + col) * p.rank + k];
+      const uint32_t w = p.b[(static_cast<size_t>(id) * p.N + n) * p.rank + k];
       if ((w & 0x7f80u) != 0x7f80u) continue;
       const uint32_t x = __ldcg(p.low + static_cast<size_t>(m) * p.rank_pad + k);
       sum += __uint_as_float(w << 16) * __uint_as_float(x << 16);
       any = true;
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (any && i == j) v[i] += sum;
+    if (any) v[i] += sum;
   }
 }
 
-// Stores two columns (this lane's and its neighbour's) of the chunk's tokens:
-// v[j] is token j, this lane's column (stored if below `end`). COUNT tokens, the
-// first at `row`.
-template <int COUNT>
+// Stores GROUPS x 8 tokens x 32 columns, packed as 8 x 8 matrices (w[g][b]: tokens
+// 8 g .., columns 8 b ..), through the warp's 2 KB of staging: a token's 64 bytes
+// are four 16-byte chunks, turned by the token so that neither the transposed
+// stores nor the reads meet in a bank.
+template <int GROUPS>
 __device__ __forceinline__ void store_tokens(uint16_t* y, int N, int row, int valid, int col, int end,
-                                             const float* v) {
-  const bool odd = threadIdx.x & 1;
-  uint16_t* at = y + static_cast<size_t>(row) * N + (col & ~1);
+                                             uint32_t staging, const uint32_t (&w)[GROUPS][4]) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const uint32_t in = staging + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
 #pragma unroll
-  for (int j = 0; j < COUNT; j += 2) {
-    const uint32_t own = pack_bf16x2(__float_as_uint(v[j]), __float_as_uint(v[j + 1]));
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-    const uint32_t out = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-    const int token = j + (odd ? 1 : 0);
-    if (token < valid && col < end)
-      *reinterpret_cast<uint32_t*>(at + static_cast<size_t>(token) * N) = out;
+  for (int g = 0; g < GROUPS; ++g) store_transposed(in + g * 512, w[g][0], w[g][1], w[g][2], w[g][3]);
+  __syncwarp();
+  const int r = lane >> 2, c = lane & 3;
+  const uint32_t out = staging + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  uint16_t* at = y + static_cast<size_t>(row + r) * N + col + 8 * c;
+  const bool in_cols = col + 8 * c < end;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(out + g * 512)
+                 : "memory");
+    if (in_cols && r + 8 * g < valid) *reinterpret_cast<uint4*>(at + static_cast<size_t>(8 * g) * N) = v;
   }
+  __syncwarp();   // read before the next chunk is written
 }
 
 template <class C>
@@ -857,12 +917,14 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
   const int et = static_cast<int>(threadIdx.x) - 64;
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int quad = (static_cast<int>(threadIdx.x) >> 5) & 3;   // TMEM lanes this warp may read
-  // This thread's weight row. The accumulator of a pair MMA with 128 rows holds a
-  // CTA's 64 rows twice over: lanes 64..127 hold the second half of the tokens.
-  const int wrow = C::HALF ? (quad & 1) * 32 + lane : quad * 32 + lane;
+  // This warp's first weight row. The accumulator of a pair MMA with 128 rows holds
+  // a CTA's 64 rows twice over: lanes 64..127 hold the second half of the tokens.
+  const int wrow = (C::HALF ? quad & 1 : quad) * 32;
   const uint32_t lead_tempty = map_shared_to_rank(tempty0, 0);
-  float* swap = reinterpret_cast<float*>(base_ptr + C::kSwapOff);
+  float* swap = reinterpret_cast<float*>(base_ptr + C::kStagingOff);
+  const uint32_t staging = base + C::kStagingOff + quad * 2048;
   uint32_t local = 0;
+  Placing placing;
   Walk walk;
   walk.begin(p, tiles);
   Tile t, tn;
@@ -871,7 +933,12 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
     t = tn;
     have = walk.step<C>(p, g, tn);   // while this tile's accumulator fills
     const uint32_t acc = local & 1u;
-    const bool ok = wait_bounded(tfull0 + 8 * acc, (local >> 1) & 1u, ctl, (kRoleEpilogue << 8) | 1);
+    bool placed = true;
+    if constexpr (C::KIND == kLora && C::HALF) {
+      if (local == 0) grid_dependency_wait();
+      placed = place_tile<1, C>(p, t, local, placing, et, base, rank, marks, ctl);
+    }
+    const bool ok = placed && wait_bounded(tfull0 + 8 * acc, (local >> 1) & 1u, ctl, (kRoleEpilogue << 8) | 1);
     if (!epilogue_bar_and(ok)) break;
     tc_fence_after_sync();
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::TOK;
@@ -887,15 +954,17 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
       if (marked && et == 0) marks[local % kMarks] = 0;
     }
 
-    // 32 columns of the accumulator, fp32.
+    // This warp's fragments of 32 tokens from token 32 * c on: v[16 h + 4 g + e] is
+    // token 8 g + 2 (lane % 4) + e % 2, column 16 h + 8 (e / 2) + lane / 4.
     auto load = [&](int c, float (&v)[32]) {
       uint32_t r[32];
-      tmem_ld_32cols(taddr + 32 * c, r);
+      tmem_ld_16x32(taddr + 32 * c, r);
+      tmem_ld_16x32(taddr + (16u << 16) + 32 * c, r + 16);
       tmem_ld_wait(r);
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
       if constexpr (C::KIND == kLora) {
-        if (marked) add_unbounded<C>(p, t, t.row0 + tok0 + 32 * c, mine - 32 * c, col0 + wrow, v);
+        if (marked) add_unbounded<C>(p, t, t.row0 + tok0 + 32 * c, mine - 32 * c, col0 + wrow, col_end, v);
       }
     };
     auto release = [&]() {
@@ -903,29 +972,48 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
       __syncwarp();
       if (lane == 0) sign_pair(lead_tempty + 8 * acc);
     };
-    // 32 tokens of the tile from token 32 * c on: this lane's column.
     auto emit = [&](int c, const float (&v)[32]) {
       const int row = t.row0 + tok0 + 32 * c, valid = mine - 32 * c;
       if constexpr (C::KIND != kGated) {
-        store_tokens<32>(p.y, p.N, row, valid, col0 + wrow, col_end, v);
-      } else {
-        // Quads 0 and 1 hold the gates, 2 and 3 the ups, of the same columns.
-        // Each pair of warps swaps halves: the gate's warp finishes tokens
-        // 0..15, the up's warp 16..31.
-        const int pair = quad & 1, up = quad >> 1;
-        float* buf = swap + pair * (2 * 16 * 32);
+        uint32_t w[4][4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) buf[up * 512 + j * 32 + lane] = up ? v[j] : v[16 + j];
-        named_sync(2 + pair, 64);
-        float out[16];
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int j = 16 * (b >> 1) + 4 * g + 2 * (b & 1);
+            w[g][b] = pack_bf16x2(__float_as_uint(v[j]), __float_as_uint(v[j + 1]));
+          }
+        store_tokens<4>(p.y, p.N, row, valid, col0 + wrow, col_end, staging, w);
+      } else {
+        // Quads 0 and 1 hold the gates, 2 and 3 the ups, of the same columns, in
+        // the same layout. Each pair of warps swaps halves through their staging:
+        // the gate's warp finishes tokens 0..15, the up's warp 16..31.
+        const int pair = quad & 1, up = quad >> 1;
+        float* own = swap + quad * 512;
+        const float* theirs = swap + (quad ^ 2) * 512;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float other = buf[(1 - up) * 512 + j * 32 + lane];
-          const float gate = up ? other : v[j], mul = up ? v[16 + j] : other;
-          out[j] = gate / (1.f + __expf(-gate)) * mul;
+          const int i = 16 * (j >> 3) + (j & 7);   // of the first two token groups
+          own[j * 32 + lane] = up ? v[i] : v[i + 8];
         }
-        named_sync(2 + pair, 64);   // read before the next chunk's halves come
-        store_tokens<16>(p.y, p.N, row + 16 * up, valid - 16 * up, col0 + pair * 32 + lane, col_end, out);
+        named_sync(2 + pair, 64);
+        uint32_t w[2][4];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            float out[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = 8 * (b >> 1) + 4 * g + 2 * (b & 1) + e, i = 16 * (j >> 3) + (j & 7);
+              const float other = theirs[j * 32 + lane];
+              const float gate = up ? other : v[i], mul = up ? v[i + 8] : other;
+              out[e] = gate / (1.f + __expf(-gate)) * mul;
+            }
+            w[g][b] = pack_bf16x2(__float_as_uint(out[0]), __float_as_uint(out[1]));
+          }
+        named_sync(2 + pair, 64);   // read by the other warp: the staging is free
+        store_tokens<2>(p.y, p.N, row + 16 * up, valid - 16 * up, col0 + pair * 32, col_end, staging, w);
       }
     };
 
@@ -939,17 +1027,16 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
       continue;
     }
 
-    // A piece of a cut tile: publish the fp32 partial ([token / 4][weight row][4]) and
+    // A piece of a cut tile: publish the fp32 partial (each thread its fragments) and
     // count it; the piece that finds all others counted sums them in k order.
     constexpr size_t kSlot = static_cast<size_t>(C::TOK) * C::kRows;
-    const int place0 = C::HALF ? (quad >> 1) * (C::TOK / 8) * C::kRows + wrow : wrow;   // in float4
-    float* slot = p.partials + (static_cast<size_t>(t.slot + t.piece) * 2 + rank) * kSlot;
+    float4* slot = reinterpret_cast<float4*>(p.partials + (static_cast<size_t>(t.slot + t.piece) * 2 + rank) * kSlot);
     for (int c = 0; c < chunks; ++c) {
       float v[32];
       load(c, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        __stcg(reinterpret_cast<float4*>(slot) + (8 * c + j) * C::kRows + place0,
+        __stcg(slot + (8 * c + j) * kEpi + et,
                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
     }
     release();
@@ -977,19 +1064,21 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
       auto read = [&](int s, float4 (&f)[8]) {
         const float4* src = first + static_cast<size_t>(s) * (2 * kSlot / 4);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __ldcg(src + (8 * c + j) * C::kRows + place0);
+        for (int j = 0; j < 8; ++j) f[j] = __ldcg(src + (8 * c + j) * kEpi + et);
       };
-      // Two pieces' reads in flight; added in k order (0 + x is x, but for the
-      // sign of a zero).
+      // In k order (0 + x is x, but for the sign of a zero); two pieces' reads in
+      // flight where there are registers for them.
       int s = 0;
-      for (; s + 1 < t.npieces; s += 2) {
-        float4 f[8], h[8];
-        read(s, f);
-        read(s + 1, h);
-        add(f);
-        add(h);
+      if constexpr (C::KIND != kLora) {
+        for (; s + 1 < t.npieces; s += 2) {
+          float4 f[8], h[8];
+          read(s, f);
+          read(s + 1, h);
+          add(f);
+          add(h);
+        }
       }
-      if (s < t.npieces) {
+      for (; s < t.npieces; ++s) {
         float4 f[8];
         read(s, f);
         add(f);

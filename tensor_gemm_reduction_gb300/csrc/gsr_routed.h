@@ -106,7 +106,6 @@ constexpr int kRoutedSmall = 64, kRoutedMid = 128, kRoutedWide = 256;
 constexpr int routed_kblocks(bool half, int tokens) { return half && tokens <= kRoutedMid ? 4 : 2; }
 
 cudaError_t prepare_routed_kernels();
-cudaError_t prepare_lowrank_kernels();
 cudaError_t prepare_route_kernels();
 // half: tiles of at most 128 weight rows (kLora).
 cudaError_t launch_routed(const RoutedParams& p, int kind, bool gather, bool half, int tokens, int ctas,
