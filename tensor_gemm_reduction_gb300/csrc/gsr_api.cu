@@ -748,6 +748,7 @@ gsr_status gemm_shard_plan_create(gemm_shard_plan** out, int device, int64_t max
     if (e == cudaSuccess) e = gsr::prepare_small_kernel();
     if (e == cudaSuccess) e = gsr::prepare_pack_kernel();
     if (e == cudaSuccess) e = gsr::prepare_routed_kernels();
+    if (e == cudaSuccess) e = gsr::prepare_lowrank_kernels();
     if (e == cudaSuccess) e = gsr::prepare_route_kernels();
     if (e != cudaSuccess) return cuda_fail(e, "configuring the kernels");
   }

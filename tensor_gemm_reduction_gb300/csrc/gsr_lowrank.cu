@@ -7,20 +7,19 @@
 // adapter's own part of Y, as rounding Y itself does).
 //
 // The rank is small (8 to 128), so the work is reading X and the adapters that
-// some row has: a few hundred flops per row and byte at most, which warp-level
-// mma.sync (m16n8k16) covers. One warp takes 16 rows and a share of k and reads
-// both operands straight into the fragments, 16 bytes per lane: a lane's eight
-// consecutive k are its two fragments' k (the sum does not mind the order, and X
-// and A use the same), so no shared memory and no transpose is needed.
+// some row has: a few hundred flops per byte at most, which warp-level mma.sync
+// (m16n8k16) covers. Both operands stream through a ring in shared memory, 16
+// bytes per asynchronous copy, eight copies to a 128-byte line, swizzled for
+// ldmatrix. (Loads straight into the fragments ask for 64 bytes of a line at a
+// time: at 64 adapters and 128 rows the requests in flight held the kernel to
+// 2.6 TB/s from memory.)
 //
-// 16 rows may have up to 16 adapters. Blocks take them in turn (blockIdx.y);
-// each computes all 16 rows against its adapter and keeps those that have it.
-// k is cut over the CTAs of a cluster (and, for few rows, over the warps of the
-// CTA too); the fp32 shares meet in distributed shared memory and are added in
-// a fixed order.
-//
-// Blocks past the rows write the adapter lists of the token tiles of the product
-// that follows (ascending, without repeats).
+// With few rows a block takes an adapter and gathers the rows that have it, 16 at a
+// time, and its warps share k; with many, a block takes 128 consecutive rows, 16
+// per warp, and goes through their adapters. k is also cut over the CTAs of a
+// cluster; the fp32 shares meet in distributed shared memory and are added in a
+// fixed order. The adapter lists of the token tiles of the product that follows
+// (ascending, without repeats) are written on the side.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -35,25 +34,42 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreadsLow = 32 * kWarps;
 constexpr int kMaxCluster = 8;       // CTAs that share the reduction, at most
-constexpr int kUnit = 64;            // k per step of a warp (128 bytes of a row)
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 load16(const uint16_t* p, bool ok) {
-  return ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// 16 bytes to shared memory, or 16 zeros; asynchronous.
+__device__ __forceinline__ void copy_16(uint32_t dst, const uint16_t* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_shared_addr(const void* p, uint32_t rank) {
   uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), out;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(a), "r"(rank));
   return out;
+}
+
+// For reads of the cluster's shared memory that are done (their values used): no
+// release, which would wait for global stores.
+__device__ __forceinline__ void cluster_sync_reads() {
+  __syncwarp();
+  asm volatile(
+      "barrier.cluster.arrive.relaxed.aligned;\n\t"
+      "barrier.cluster.wait.aligned;" ::
+          : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync_all() {
@@ -97,151 +113,336 @@ __device__ void write_list(const LowRankParams& p, int tile, uint32_t* bits, int
     for (uint32_t b = bits[w]; b; b &= b - 1u) list[1 + at++] = 32 * w + __ffs(b) - 1;
 }
 
-// NT: 8-column tiles of a pass over the padded rank (128 columns take two passes of
-// 64). SPLIT: the warps of a CTA share k (16 rows per CTA) or take 16 rows each
-// (128 rows per CTA).
-//
-// The shares go through shared memory 32 columns at a time.
-constexpr int kShareCols = 32;
-constexpr int kSmemBytes = kWarps * 16 * kShareCols * 4;
-static_assert(kSmemBytes >= kMaxAdapters / 8, "a bit per adapter");
+// The shards' table in shared memory, filled before the kernel waits for its
+// predecessor: the first reads of the parameters come from memory, and one by one,
+// where they are used, took longer than the products.
+struct Shards {
+  const uint16_t *x[kMaxShards], *a[kMaxShards];
+  int k[kMaxShards];
+  __device__ __forceinline__ void fill(const LowRankParams& p) {
+    const int r = static_cast<int>(threadIdx.x);
+    if (r < kMaxShards) {
+      x[r] = p.x[r];
+      a[r] = p.a[r];
+      k[r] = r < p.R ? static_cast<int>(p.k[r]) : 0;
+    }
+  }
+};
 
-template <int NT, bool SPLIT>
-__global__ void __launch_bounds__(kThreadsLow, NT <= 4 ? 3 : 2) gsr_lowrank_kernel(const __grid_constant__ LowRankParams p) {
-  extern __shared__ float share[];                 // [kWarps][16][columns of a turn]
-  __shared__ int ids[kWarps], keeps[16 * kWarps];
-  constexpr int kCols = 8 * NT < kShareCols ? 8 * NT : kShareCols, kTurnTiles = kCols / 8;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// A block's stream: ROWS rows (their indices in `rows`, < 0: zeros) against columns
+// pass .. pass + 8 NT of adapter a, over this CTA's share of k, in stages of KSTEP.
+// 128 rows: warp w has rows 16 w ..; 16 rows: the warps share a stage's k.
+template <int ROWS, int NT>
+struct Stream {
+  static constexpr int KSTEP = ROWS == 16 ? 128 : 64, kPitch = 2 * KSTEP, kChunks = KSTEP / 8;
+  static constexpr int kLines = ROWS + 8 * NT, kStage = kLines * kPitch;
+  static constexpr int S = ROWS == 16 ? (NT == 8 ? 5 : 6) : 4;
+  static constexpr int kBytes = S * kStage;
+
+  static __device__ __forceinline__ void run(const LowRankParams& p, const Shards& sh, uint32_t ring,
+                                             const int* rows, int a, int pass, int z, int ctas,
+                                             float (&acc)[NT][4]) {
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    int total = 0;
+    for (int r = 0; r < p.R; ++r) total += (sh.k[r] + KSTEP - 1) / KSTEP;
+    const int first = static_cast<int>(static_cast<long long>(z) * total / ctas);
+    const int count = static_cast<int>(static_cast<long long>(z + 1) * total / ctas) - first;
+    int shard = 0, k0 = 0;   // of the next stage to copy
+    for (int left = first; left > 0;) {
+      const int here = (sh.k[shard] - k0 + KSTEP - 1) / KSTEP, n = min(left, here);
+      left -= n;
+      k0 += n * KSTEP;
+      if (n == here) {
+        ++shard;
+        k0 = 0;
+      }
+    }
+    const int chunk = tid % kChunks;
+    auto copy = [&](int slot) {
+      const int K = sh.k[shard], k = k0 + 8 * chunk;
+      const uint16_t* x = sh.x[shard];
+      const uint16_t* aa = sh.a[shard] + (static_cast<int64_t>(a) * p.rank + pass) * K;
+      const bool in = k < K;
+      const uint32_t base = ring + slot * kStage;
+#pragma unroll
+      for (int line = tid / kChunks; line < kLines; line += kThreadsLow / kChunks) {
+        const int j = line - ROWS, row = line < ROWS ? rows[line] : j;
+        const bool real = in && (line < ROWS ? row >= 0 : pass + j < p.rank);
+        const uint16_t* src = (line < ROWS ? x : aa) + (real ? static_cast<int64_t>(row) * K + k : 0);
+        copy_16(base + line * kPitch + ((chunk ^ (line & 7)) << 4), src, real);
+      }
+      k0 += KSTEP;
+      if (k0 >= K) {
+        ++shard;
+        k0 = 0;
+      }
+    };
+    __syncthreads();   // rows[] written, the ring no longer read
+    int copied = 0;
+#pragma unroll
+    for (; copied < S - 1; ++copied) {
+      if (copied < count) copy(copied);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    const int x_row = (ROWS == 16 ? 0 : 16 * warp) + (lane & 15), x_chunk = lane >> 4;
+    const int a_line = ROWS + (lane & 7) + ((lane >> 4) << 3), a_chunk = (lane >> 3) & 1;
+    int slot = 0, next = S - 1;
+    for (int i = 0; i < count; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+      __syncthreads();   // stage i has landed, stage i - 1 is read
+      if (copied < count) copy(next);
+      ++copied;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      const uint32_t base = ring + slot * kStage;
+#pragma unroll
+      for (int q = 0; q < (ROWS == 16 ? 1 : KSTEP / 16); ++q) {
+        const int ks = ROWS == 16 ? warp : q;
+        uint32_t x[4];
+        load_matrices(base + x_row * kPitch + (((2 * ks + x_chunk) ^ (x_row & 7)) << 4), x);
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t w[4];
+          const int line = a_line + 8 * n;
+          load_matrices(base + line * kPitch + (((2 * ks + a_chunk) ^ (line & 7)) << 4), w);
+          mma_16816(acc[n], x[0], x[1], x[2], x[3], w[0], w[1]);
+          mma_16816(acc[n + 1], x[0], x[1], x[2], x[3], w[2], w[3]);
+        }
+      }
+      slot = slot + 1 == S ? 0 : slot + 1;
+      next = next + 1 == S ? 0 : next + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();   // the ring may hold the shares now
+  }
+};
+
+// The shares use the ring's memory, 32 columns at a time; the adapter lists too, a
+// bit per adapter.
+constexpr int kShareCols = 32;
+static_assert(Stream<16, 2>::kBytes >= kWarps * 16 * kShareCols * 4, "shares");
+static_assert(Stream<16, 2>::kBytes >= kMaxAdapters / 8, "a bit per adapter");
+
+// Adds up the shares share[warp][16][columns] in k order, over the warps of the CTA
+// (KW of them share a row group) and then over the cluster, and writes them,
+// scaled, to columns `first` .. of the rows at[] (< 0: none) that have the adapters
+// keeps[].
+template <int COLS, int KW>
+__device__ __forceinline__ void write_rows(const LowRankParams& p, float* share, const int* at,
+                                           const int* keeps, int first, int z, int ctas) {
+  constexpr int kElems = 16 * (kWarps / KW) * COLS;
+  const int tid = static_cast<int>(threadIdx.x);
+  if constexpr (KW > 1) {
+    __syncthreads();
+    for (int e = tid; e < kElems; e += kThreadsLow) {
+      float sum = share[e];
+#pragma unroll
+      for (int w = 1; w < KW; ++w) sum += share[w * kElems + e];
+      share[e] = sum;   // read by this thread alone
+    }
+  }
+  cluster_sync_all();
+  for (int e = z * kThreadsLow + tid; e < kElems; e += ctas * kThreadsLow) {
+    const int row = e / COLS;
+    if (at[row] < 0) continue;
+    float v[kMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      v[c] = 0.f;
+      if (c < ctas)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                     : "=f"(v[c])
+                     : "r"(cluster_shared_addr(share + e, static_cast<uint32_t>(c))));
+    }
+    float sum = v[0];
+#pragma unroll
+    for (int c = 1; c < kMaxCluster; ++c) sum += v[c];
+    const float s = p.scale ? __ldg(p.scale + keeps[row]) : 1.f;
+    p.low[static_cast<size_t>(at[row]) * p.rank_pad + first + e - row * COLS] =
+        __bfloat16_as_ushort(__float2bfloat16(sum * s));
+  }
+  cluster_sync_reads();   // read by all before the next share is written
+}
+
+// The product that follows may start once every block has read its operands (or
+// has left): started earlier, its stream of weights held this kernel's reads back
+// (64 adapters, 128 rows: 20 us in place of 9).
+__device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <int NT>
+__device__ __forceinline__ void put_share(float* share, const float (*acc)[4], int cols) {
+  const int lane = static_cast<int>(threadIdx.x) & 31, group = lane >> 2, quad = lane & 3;
+  float* mine = share + (static_cast<int>(threadIdx.x) >> 5) * (16 * cols);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    *reinterpret_cast<float2*>(mine + group * cols + 8 * n + 2 * quad) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(mine + (group + 8) * cols + 8 * n + 2 * quad) = make_float2(acc[n][2], acc[n][3]);
+  }
+}
+
+// Few rows (at most kFewRows): block (x, y) takes the y-th adapter that a row has
+// and, of its rows, every gridDim.x-th group of 16, so that an adapter is read
+// about once however its rows are spread. k is cut over the cluster and the warps.
+// NT: 8-column tiles of a pass over the padded rank.
+constexpr int kFewRows = 1024;
+
+template <int NT>
+__global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_few_kernel(const __grid_constant__ LowRankParams p) {
+  extern __shared__ float share[];                 // the ring; [kWarps][16][columns of a turn]
+  __shared__ int sums[kWarps], members[kFewRows], group_rows[16], group_ids[16], found;
+  __shared__ Shards shards;
+  constexpr int kCols = 8 * NT < kShareCols ? 8 * NT : kShareCols, kTurnTiles = kCols / 8;
+  shards.fill(p);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int z = static_cast<int>(blockIdx.z), ctas = static_cast<int>(gridDim.z);
-  const int blocks = (p.M + (SPLIT ? 16 : 16 * kWarps) - 1) / (SPLIT ? 16 : 16 * kWarps);
-  if (static_cast<int>(blockIdx.x) >= blocks) {   // whole clusters
-    if (blockIdx.y == 0)
-      for (int tile = (static_cast<int>(blockIdx.x) - blocks) * ctas + z; tile < p.m_tiles;
-           tile += (static_cast<int>(gridDim.x) - blocks) * ctas) {
-        write_list(p, tile, reinterpret_cast<uint32_t*>(share), ids);
-        __syncthreads();
-      }
-    return;
-  }
+  const int nth = static_cast<int>(blockIdx.y);
 
-  const int row0 = static_cast<int>(blockIdx.x) * (SPLIT ? 16 : 16 * kWarps) + (SPLIT ? 0 : 16 * warp);
-  const int group = lane >> 2, quad = lane & 3;
-  // The distinct adapters of this warp's 16 rows: lane i (< 16) holds row i's;
-  // `leaders` marks the first row of each.
-  int id = lane < 16 && row0 + lane < p.M ? p.adapter[row0 + lane] : -1;
-  if (id < 0 || id >= p.L) id = -1;
-  const uint32_t same = __match_any_sync(0xffffffffu, id);
-  const uint32_t leaders =
-      __ballot_sync(0xffffffffu, id >= 0 && (same & ((1u << lane) - 1u)) == 0);
-  int most = __popc(leaders);
-  if constexpr (!SPLIT) {
-    // The CTA's warps go through their adapters together.
-    if (lane == 0) ids[warp] = most;
-    __syncthreads();
-    for (int i = 0; i < kWarps; ++i) most = max(most, ids[i]);
+  // The list of token tile `tile`, by one block of each column of the grid; the
+  // whole call's distinct adapters likewise (a bit per adapter).
+  uint32_t* bits = reinterpret_cast<uint32_t*>(share);
+  if (nth == 0 && z == 0)
+    for (int tile = static_cast<int>(blockIdx.x); tile < p.m_tiles; tile += static_cast<int>(gridDim.x)) {
+      write_list(p, tile, bits, sums);
+      __syncthreads();
+    }
+  constexpr int kPer = kFewRows / kThreadsLow;
+  int id[kPer];
+  const int words = (p.L + 31) / 32, per = (words + kThreadsLow - 1) / kThreadsLow;
+  const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
+  for (int w = w0; w < w1; ++w) bits[w] = 0;
+  if (tid == 0) found = -1;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    // Rows in order over warps, then lanes.
+    const int m = (warp * kPer + i) * 32 + lane;
+    id[i] = m < p.M ? p.adapter[m] : -1;
+    if (id[i] < 0 || id[i] >= p.L) id[i] = -1;
+    if (id[i] >= 0) atomicOr(&bits[id[i] >> 5], 1u << (id[i] & 31));
   }
-  const int units = p.unit_begin[p.R];
-  const int parts = SPLIT ? ctas * kWarps : ctas;
-  const int part = SPLIT ? z * kWarps + warp : z;
-  const int u0 = static_cast<int>(static_cast<long long>(part) * units / parts);
-  const int u1 = static_cast<int>(static_cast<long long>(part + 1) * units / parts);
-  const bool row_a = row0 + group < p.M, row_b = row0 + group + 8 < p.M;
+  __syncthreads();
+  int mine = 0;
+  for (int w = w0; w < w1; ++w) mine += __popc(bits[w]);
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int before = incl - mine;
+  for (int i = 0; i < warp; ++i) before += sums[i];
+  if (nth >= before && nth < before + mine) {
+    int left = nth - before, w = w0;
+    while (__popc(bits[w]) <= left) left -= __popc(bits[w++]);
+    uint32_t b = bits[w];
+    for (; left > 0; --left) b &= b - 1u;
+    found = 32 * w + __ffs(b) - 1;
+  }
+  __syncthreads();
+  const int a = found;
+  if (a < 0) return;   // fewer adapters (the whole cluster)
+  // Its rows, in order.
+  uint32_t has[kPer];
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    has[i] = __ballot_sync(0xffffffffu, id[i] == a);
+    count += __popc(has[i]);
+  }
+  __syncthreads();
+  if (lane == 0) sums[warp] = count;
+  __syncthreads();
+  int at = 0, total = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) at += sums[i];
+    total += sums[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (id[i] == a) members[at + __popc(has[i] & ((1u << lane) - 1u))] = (warp * kPer + i) * 32 + lane;
+    at += __popc(has[i]);
+  }
+  __syncthreads();
 
-  for (int turn = static_cast<int>(blockIdx.y); turn < most; turn += static_cast<int>(gridDim.y)) {
-    // The turn-th distinct adapter of this warp's rows (none: nothing to add).
-    uint32_t left = leaders;
-    for (int i = 0; i < turn; ++i) left &= left - 1u;
-    const int a = left ? __shfl_sync(0xffffffffu, id, __ffs(left) - 1) : -1;
-    if constexpr (!SPLIT) {
-      if (lane < 16) keeps[warp * 16 + lane] = a >= 0 && id == a ? a : -1;   // rows to keep
-    } else {
-      if (warp == 0 && lane < 16) keeps[lane] = id == a ? a : -1;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(share));
+  for (int g = 16 * static_cast<int>(blockIdx.x); g < total; g += 16 * static_cast<int>(gridDim.x)) {
+    if (tid < 16) {
+      group_rows[tid] = g + tid < total ? members[g + tid] : -1;
+      group_ids[tid] = a;
     }
     for (int pass = 0; pass < p.rank_pad; pass += 8 * NT) {
-      float acc[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-      if (a >= 0) {
-        for (int r = 0; r < p.R; ++r) {
-          const int lo = max(u0, p.unit_begin[r]), hi = min(u1, p.unit_begin[r + 1]);
-          if (lo >= hi) continue;
-          const int64_t K = p.k[r];
-          int k = (lo - p.unit_begin[r]) * kUnit + quad * 8;
-          const int k_end = min(static_cast<int>(K), (hi - p.unit_begin[r]) * kUnit);
-          const uint16_t* xa = p.x[r] + static_cast<int64_t>(row0 + group) * K;
-          const uint16_t* xb = xa + 8 * K;
-          const uint16_t* aa = p.a[r] + (static_cast<int64_t>(a) * p.rank + pass + group) * K;
-#pragma unroll 2
-          for (; k - quad * 8 < k_end; k += 32) {
-            const bool in = k < k_end;
-            const uint4 f = load16(xa + k, in && row_a);
-            const uint4 s = load16(xb + k, in && row_b);
-            uint4 b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              b[n] = load16(aa + static_cast<int64_t>(8 * n) * K + k, in && pass + 8 * n + group < p.rank);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_16816(acc[n], f.x, s.x, f.y, s.y, b[n].x, b[n].y);
-              mma_16816(acc[n], f.z, s.z, f.w, s.w, b[n].z, b[n].w);
-            }
-          }
-        }
-      }
+      float acc[NT][4] = {};
+      Stream<16, NT>::run(p, shards, ring, group_rows, a, pass, z, ctas, acc);
+      let_next_start();
 #pragma unroll
       for (int n0 = 0; n0 < NT; n0 += kTurnTiles) {
-        float* mine = share + warp * (16 * kCols);
-#pragma unroll
-        for (int n = 0; n < kTurnTiles; ++n) {
-          const float* c = acc[n0 + n];
-          *reinterpret_cast<float2*>(mine + group * kCols + 8 * n + 2 * quad) = make_float2(c[0], c[1]);
-          *reinterpret_cast<float2*>(mine + (group + 8) * kCols + 8 * n + 2 * quad) = make_float2(c[2], c[3]);
-        }
-        cluster_sync_all();
-        // Each CTA of the cluster adds up a share of the elements, in k order.
-        constexpr int kElems = (SPLIT ? 16 : 16 * kWarps) * kCols;
-        for (int e = z * kThreadsLow + tid; e < kElems; e += ctas * kThreadsLow) {
-          const int row = e / kCols, col = pass + 8 * n0 + e - row * kCols;
-          const int keep = keeps[row];
-          if (keep < 0) continue;
-          float sum = 0.f;
-          for (int c = 0; c < ctas; ++c) {
-            const uint32_t at = cluster_shared_addr(share, static_cast<uint32_t>(c));
-#pragma unroll
-            for (int w = 0; w < (SPLIT ? kWarps : 1); ++w) {
-              float v;
-              asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                           : "=f"(v)
-                           : "r"(at + 4u * static_cast<uint32_t>(SPLIT ? w * kElems + e : e)));
-              sum += v;
-            }
-          }
-          const float s = p.scale ? __ldg(p.scale + keep) : 1.f;
-          const int m = static_cast<int>(blockIdx.x) * (SPLIT ? 16 : 16 * kWarps) + row;
-          p.low[static_cast<size_t>(m) * p.rank_pad + col] =
-              __bfloat16_as_ushort(__float2bfloat16(sum * s));
-        }
-        cluster_sync_all();   // read by all before the next share is written
+        put_share<kTurnTiles>(share, acc + n0, kCols);
+        write_rows<kCols, kWarps>(p, share, group_rows, group_ids, pass + 8 * n0, z, ctas);
       }
     }
   }
 }
 
-template <int NT, bool SPLIT>
-cudaError_t launch_nt(const LowRankParams& p, cudaStream_t stream) {
-  const int rows = SPLIT ? 16 : 16 * kWarps, blocks = (p.M + rows - 1) / rows;
-  // 16 rows have at most 16 adapters, each a turn of its own. k is cut among the
-  // CTAs of a cluster until they are about four times the SMs (the reduction over a
-  // cluster costs more).
-  const int turns = SPLIT ? std::min(16, std::min(p.L, p.M)) : 1;
-  int cluster = kMaxCluster;
-  if (SPLIT)
-    while (cluster > 1 && blocks * turns * cluster > 608) cluster /= 2;
-  const int list_blocks = (std::min(p.m_tiles, 16) + cluster - 1) / cluster;
+// Many rows: block x takes 128 rows, 16 per warp, and their adapters one after the
+// other, ascending.
+template <int NT>
+__global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __grid_constant__ LowRankParams p) {
+  extern __shared__ float share[];                 // the ring; [kWarps][16][columns of a turn]
+  __shared__ int sums[kWarps], keeps[16 * kWarps], at[16 * kWarps], rows[16 * kWarps];
+  __shared__ Shards shards;
+  constexpr int kCols = 8 * NT < kShareCols ? 8 * NT : kShareCols, kTurnTiles = kCols / 8;
+  shards.fill(p);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();   // the product's blocks fit only when these leave
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int z = static_cast<int>(blockIdx.z), ctas = static_cast<int>(gridDim.z);
+  const int blocks = (p.M + 16 * kWarps - 1) / (16 * kWarps);
+  if (static_cast<int>(blockIdx.x) >= blocks) {   // whole clusters: the token tiles' lists
+    for (int tile = (static_cast<int>(blockIdx.x) - blocks) * ctas + z; tile < p.m_tiles;
+         tile += (static_cast<int>(gridDim.x) - blocks) * ctas) {
+      write_list(p, tile, reinterpret_cast<uint32_t*>(share), sums);
+      __syncthreads();
+    }
+    return;
+  }
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(share));
+  const int m = static_cast<int>(blockIdx.x) * 16 * kWarps + tid;   // thread i < 128 has row i
+  int id = tid < 16 * kWarps && m < p.M ? p.adapter[m] : -1;
+  if (id < 0 || id >= p.L) id = -1;
+  if (tid < 16 * kWarps) rows[tid] = m < p.M ? m : -1;
+  for (int last = -1;;) {
+    // The smallest adapter above the last one.
+    const int mine = id > last ? id : INT32_MAX;
+    const int least = __reduce_min_sync(0xffffffffu, mine);
+    __syncthreads();   // the last turn's reads
+    if (lane == 0) sums[warp] = least;
+    __syncthreads();
+    int a = INT32_MAX;
+    for (int i = 0; i < kWarps; ++i) a = min(a, sums[i]);
+    if (a == INT32_MAX) break;
+    last = a;
+    if (tid < 16 * kWarps) {
+      at[tid] = id == a ? m : -1;
+      keeps[tid] = a;
+    }
+    for (int pass = 0; pass < p.rank_pad; pass += 8 * NT) {
+      float acc[NT][4] = {};
+      Stream<128, NT>::run(p, shards, ring, rows, a, pass, z, ctas, acc);
+#pragma unroll
+      for (int n0 = 0; n0 < NT; n0 += kTurnTiles) {
+        put_share<kTurnTiles>(share, acc + n0, kCols);
+        write_rows<kCols, 1>(p, share, at, keeps, pass + 8 * n0, z, ctas);
+      }
+    }
+  }
+}
+
+template <class K>
+cudaError_t launch_clusters(K kernel, const LowRankParams& p, dim3 grid, int smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -249,24 +450,58 @@ cudaError_t launch_nt(const LowRankParams& p, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = cluster;
-  cfg.gridDim = dim3(blocks + list_blocks, turns, cluster);
+  attr[1].val.clusterDim.z = grid.z;
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreadsLow, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gsr_lowrank_kernel<NT, SPLIT>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int NT>
+cudaError_t launch_nt(const LowRankParams& p, cudaStream_t stream) {
+  if (p.M <= kFewRows) {
+    // About two CTAs per SM: k cut over up to eight of a cluster, then, where there
+    // are few adapters, their rows over blocks. (Blocks that find no adapter or rows
+    // leave at once, but the others are not spread over the SMs anew.)
+    const int adapters = std::min(p.L, p.M);
+    int cluster = kMaxCluster;
+    while (cluster > 1 && adapters * cluster > 304) cluster /= 2;
+    const int groups = std::min((p.M + 15) / 16, std::max(1, 304 / (adapters * cluster)));
+    return launch_clusters(gsr_lowrank_few_kernel<NT>, p, dim3(groups, adapters, cluster),
+                           Stream<16, NT>::kBytes, stream);
+  }
+  const int blocks = (p.M + 16 * kWarps - 1) / (16 * kWarps);
+  const int list_blocks = (std::min(p.m_tiles, 16) + kMaxCluster - 1) / kMaxCluster;
+  return launch_clusters(gsr_lowrank_kernel<NT>, p, dim3(blocks + list_blocks, 1, kMaxCluster),
+                         Stream<128, NT>::kBytes, stream);
 }
 
 }  // namespace
 
+template <int NT>
+cudaError_t set_limits() {
+  cudaError_t e = cudaFuncSetAttribute(gsr_lowrank_few_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Stream<16, NT>::kBytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(gsr_lowrank_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Stream<128, NT>::kBytes);
+}
+
+cudaError_t prepare_lowrank_kernels() {
+  cudaError_t e = set_limits<2>();
+  if (e == cudaSuccess) e = set_limits<4>();
+  if (e == cudaSuccess) e = set_limits<8>();
+  return e;
+}
+
 cudaError_t launch_low_rank(const LowRankParams& p, cudaStream_t stream) {
-  const bool split = p.rows_per_cta == 16;
   switch (p.rank_pad) {
-    case 16: return split ? launch_nt<2, true>(p, stream) : launch_nt<2, false>(p, stream);
-    case 32: return split ? launch_nt<4, true>(p, stream) : launch_nt<4, false>(p, stream);
-    default: return split ? launch_nt<8, true>(p, stream) : launch_nt<8, false>(p, stream);
+    case 16: return launch_nt<2>(p, stream);
+    case 32: return launch_nt<4>(p, stream);
+    default: return launch_nt<8>(p, stream);
   }
 }
 

@@ -111,6 +111,16 @@ __device__ __forceinline__ void sign_many(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// The lane that every election of a whole warp picks.
+__device__ __forceinline__ bool elected() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -132,14 +142,16 @@ struct Cfg {
   static constexpr uint32_t kStage = KZ * (kW + kX);
   static constexpr uint32_t kRing = S * kStage;
   // full[S], empty[S], tmem_full[2], tmem_empty[2], drain; landed[S]: this CTA's
-  // adapter weights (kLora) or gathered rows
-  static constexpr uint32_t kBars = (2 * S + 5 + (KIND == kLora || GATHER ? S : 0)) * 8;
-  static constexpr uint32_t kLandedOff = (2 * S + 5) * 8;
+  // adapter weights (kLora) or gathered rows; granted[S] (kLora): the slot is free
+  // for an adapter stage; looked (kLora): the tile's adapters are looked over
+  static constexpr uint32_t kBars = (2 * S + 5 + (KIND == kLora ? 2 * S + 1 : GATHER ? S : 0)) * 8;
+  static constexpr uint32_t kLandedOff = (2 * S + 5) * 8, kGrantedOff = kLandedOff + S * 8;
+  static constexpr uint32_t kLookedOff = kGrantedOff + S * 8;
   static constexpr uint32_t kGroups = KIND == kLora ? 0 : 4 * (3 * kMaxGroups + 1 + 32);
   static constexpr uint32_t kStaging = 4 * 2048;        // 2 KB per epilogue warp
   static constexpr uint32_t kBarsOff = kRing;
   static constexpr uint32_t kMiscOff = kBarsOff + kBars;
-  static constexpr uint32_t kStagingOff = (kMiscOff + 16 + 4 * kMarks + 127) / 128 * 128;
+  static constexpr uint32_t kStagingOff = (kMiscOff + 16 + 4 * (kMarks + 3) + 127) / 128 * 128;
   static constexpr uint32_t kGroupsOff = kStagingOff + kStaging;
   static constexpr uint32_t kSmem = 1024 + kGroupsOff + kGroups;
   static_assert(kSmem <= kSmallSmemLimit, "shared memory");
@@ -365,6 +377,25 @@ __device__ __forceinline__ uint64_t unit_desc(uint32_t saddr, int cols) {
   return d;
 }
 
+// The MMAs of one adapter stage, by one thread: an election and fresh descriptors
+// per MMA took 75 ns of its issue, three times the tensor cores' own time.
+template <int COLS, class C>
+__device__ __forceinline__ void multiply_units(uint32_t d, uint32_t sw, uint32_t sx, uint32_t idesc, int units) {
+  uint64_t w = unit_desc(sw, COLS), x = unit_desc(sx, COLS);
+  for (int u = 0; u < units; ++u) {
+#pragma unroll
+    for (int k = 0; k < COLS / 16; ++k)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "setp.eq.b32 p, 0, 0;\n\t"
+          "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+          "l"(w + 2 * k), "l"(x + 2 * k), "r"(idesc)
+          : "memory");
+    w += 2 * C::kRows * COLS / 16;   // addresses are in units of 16 bytes
+    x += C::TOK * COLS / 16;
+  }
+}
+
 // ------------------------------------------------------------ roles
 
 struct Ring {
@@ -466,11 +497,12 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
         const uint32_t landed = full0 + C::kLandedOff + 8 * ring.slot;
         if (lane == 0) {
           arm(landed, unit_bytes * units);
+          mbar_arrive(full0 + C::kGrantedOff + 8 * ring.slot);
           if (rank == 0) mbar_arrive(full0 + 8 * ring.slot);
         }
         __syncwarp();
         // Each unit's columns of its adapter's B. They complete on this CTA's own
-        // barrier, which tells the placing warps that the slot is theirs.
+        // barrier, which the placing warps follow.
         for (int u = 0; u < units; ++u) {
           const int id = a.adapter(p, u0 + u);
           if (lane == 0)
@@ -554,8 +586,6 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
         waited = true;
         a.template begin<C>(p, t);
       }
-      const int cols = p.unit_cols;
-      const uint32_t unit_w = 2u * C::kRows * cols, unit_x = static_cast<uint32_t>(C::TOK) * cols;
       for (int st = a.st; st < a.st_end; ++st) {
         ok = wait_bounded(full0 + 8 * ring.slot, ring.phase, ctl, (kRoleMma << 8) | 2);
         ok = __all_sync(0xffffffffu, ok);
@@ -563,10 +593,16 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
         tc_fence_after_sync();
         const uint32_t sw = base + ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
         const int units = a.units_in(st);
-        for (int u = 0; u < units; ++u) {
-          const uint64_t dw = unit_desc(sw + u * unit_w, cols), dx = unit_desc(sx + u * unit_x, cols);
-          for (int k = 0; k < cols / 16; ++k) mma_bf16_ss_pair(d, dw + 2 * k, dx + 2 * k, idesc, 1u);
+        // The commit below is by the same thread.
+        if (elected()) {
+          if (p.unit_cols == 16)
+            multiply_units<16, C>(d, sw, sx, idesc, units);
+          else if (p.unit_cols == 32)
+            multiply_units<32, C>(d, sw, sx, idesc, units);
+          else
+            multiply_units<64, C>(d, sw, sx, idesc, units);
         }
+        __syncwarp();
         issued = true;
         mma_commit_pair(empty0 + 8 * ring.slot, 0x3);
         ring.next<C::S>();
@@ -683,19 +719,14 @@ __device__ void sign_rows(const RoutedParams& p, int tiles, uint32_t base, const
   }
 }
 
-// One adapter stage: this lane's row `v` (COLS columns, the adapter `id`) in the
-// units of that adapter, zeros in the others; and the stage's adapter weights
-// looked over. True if one of them was not finite.
-//
-// A masked row times an infinite or NaN weight would be NaN: such weights become
-// 0 here, and the epilogue adds their products to the rows that have the adapter.
+// One adapter stage's rows: this lane's row `v` (COLS columns, the adapter `id`)
+// in the units of that adapter, zeros in the others.
 template <int COLS, class C>
-__device__ __forceinline__ bool place_stage(const RoutedParams& p, AdapterSteps& a, uint32_t sw, int st,
+__device__ __forceinline__ void place_stage(const RoutedParams& p, AdapterSteps& a, uint32_t sx, int st,
                                             int id, int who, int row, int ways, int half,
                                             const uint4 (&v)[kMaxRank / 8]) {
-  constexpr uint32_t kUnitX = C::TOK * COLS, kUnitW = 2 * C::kRows * COLS;
+  constexpr uint32_t kUnitX = C::TOK * COLS;
   constexpr uint32_t kMask = COLS == 64 ? 7 : COLS == 32 ? 3 : 1;
-  const uint32_t sx = sw + C::KZ * C::kW;
   const int units = a.units_in(st), u0 = st * a.per_stage;
   const uint32_t at_row = static_cast<uint32_t>(row) * COLS * 2;
 #pragma unroll 2
@@ -715,59 +746,79 @@ __device__ __forceinline__ bool place_stage(const RoutedParams& p, AdapterSteps&
       }
     }
   }
-  // The weights: each warp looks over every fourth unit.
-  const int lane = who & 31;
-  const uint32_t bytes = 2u * p.w_rows * COLS;   // of a unit, a multiple of 256
-  bool marked = false;
-  for (int u = who >> 5; u < units; u += kPlacers) {
-    const uint32_t unit = sw + u * kUnitW;
-    for (uint32_t at = 16u * lane; at < bytes; at += 4 * 512) {
-      uint32_t w[4][4], sum[4] = {0, 0, 0, 0};
+}
+
+// bf16 pairs: x * 0 + sum stays 0 for finite x and turns NaN for the others.
+__device__ __forceinline__ void add_zeros(uint32_t& sum, const uint4& w) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w.x), "r"(0u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w.y), "r"(0u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w.z), "r"(0u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w.w), "r"(0u));
+}
+
+// A masked row times an infinite or NaN weight would be NaN, so the tile's
+// adapters (this CTA's weight rows of them) are looked over while the base
+// product streams. That also brings them into L2 for the copies to come. Thread
+// `who` of `threads`; true if a weight that it read is not finite.
+__device__ __forceinline__ bool look_over(const RoutedParams& p, const Tile& t, uint32_t rank, int who,
+                                          int threads) {
+  const int32_t* list = p.lists + static_cast<size_t>(t.m) * kAdapterListStride;
+  const int count = __ldcg(list), lane = who & 31;
+  const int col = t.col0 + static_cast<int>(rank) * p.cta_cols;
+  const int vecs = max(min(p.cta_cols, p.N - col), 0) * p.rank / 8;   // 16-byte vectors, contiguous
+  uint32_t sum[4] = {0, 0, 0, 0};
+  for (int i = who >> 5; i < count; i += threads >> 5) {
+    const uint4* w = reinterpret_cast<const uint4*>(
+        p.b + (static_cast<size_t>(__ldcg(list + 1 + i)) * p.N + col) * p.rank);
+    for (int at = lane; at < vecs; at += 4 * 32) {
+      uint4 x[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        w[q][0] = w[q][1] = w[q][2] = w[q][3] = 0;
-        if (at + q * 512 < bytes)
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3])
-                       : "r"(unit + at + q * 512)
-                       : "memory");
-      }
-      // x * 0 + sum is 0 for finite x, NaN for the others.
+      for (int q = 0; q < 4; ++q) x[q] = at + 32 * q < vecs ? __ldcg(w + at + 32 * q) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[q]) : "r"(w[q][j]), "r"(0u));
-      if (((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0) {
-        marked = true;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (at + q * 512 >= bytes) break;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t odd = ((w[q][j] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-            w[q][j] &= ~((odd >> 15) * 0xffffu);
-          }
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(unit + at + q * 512), "r"(w[q][0]),
-                       "r"(w[q][1]), "r"(w[q][2]), "r"(w[q][3])
-                       : "memory");
-        }
-      }
+      for (int q = 0; q < 4; ++q) add_zeros(sum[q], x[q]);
     }
   }
-  return marked;
+  return ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0;
+}
+
+// The weights of a marked tile's stage that are not finite become 0 (the epilogue
+// adds their products to the rows that have the adapter).
+template <class C>
+__device__ __noinline__ void take_out(const RoutedParams& p, uint32_t sw, int units, int who) {
+  const uint32_t unit = 2u * C::kRows * p.unit_cols, bytes = 2u * p.w_rows * p.unit_cols;
+  for (int u = 0; u < units; ++u)
+    for (uint32_t at = 16u * who; at < bytes; at += 16 * 32 * kPlacers) {
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(sw + u * unit + at)
+                   : "memory");
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // Bits 15 and 31: an exponent of all ones in the half below.
+        const uint32_t odd = ((w[j] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        w[j] &= ~((odd >> 15) * 0xffffu);
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sw + u * unit + at), "r"(w[0]),
+                   "r"(w[1]), "r"(w[2]), "r"(w[3])
+                   : "memory");
+    }
 }
 
 // The adapter stages of one tile, for one team of four warps (thread `i` of
 // them). The threads are the rows of this CTA's tokens, or, with at most 64 or 32
-// rows, two or four times the rows, on alternate adapters. Every warp signs the
-// stage on the leader's full barrier. A stage is the teams' once its adapter
-// weights have landed (the producer had waited for the slot); the base product's
-// stages pass them by. Teams take alternate stages, but follow every one, so that
-// none takes a slot's next phase for the one that it waits for.
+// rows, two or four times the rows, on alternate adapters. The rows are placed
+// once the producer grants the slot, while its adapter weights are on their way;
+// every warp signs the stage on the leader's full barrier when they have landed.
+// The base product's stages pass by, and with two teams every other stage: a wait
+// by parity is safe all the same. A slot is not granted again before its stage is
+// signed, so the wait is never late; the producer grants in order, at least the
+// stage S before this one before the team's last one (S >= 3), so it is never a
+// phase early; and a granted slot's earlier weights have landed.
 struct Placing {
   Ring ring;
-  uint32_t phases = 0;   // bit s: phase of slot s's landed barrier
+  uint32_t phases = 0;   // bit s: phase of slot s's granted and landed barriers
+  uint32_t count = 0;    // adapter stages so far: the teams take turns
 };
 template <int TEAM, class C>
 __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local, Placing& q, int i,
@@ -778,7 +829,6 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
   q.ring.slot = (q.ring.slot + static_cast<uint32_t>(t.st_end - t.st)) % C::S;
   AdapterSteps a{};
   a.template begin<C>(p, t);
-  if (a.st >= a.st_end) return true;
   const int half = t.n / 2, ways = half <= 32 ? 4 : half <= 64 ? 2 : 1;
   const int row = i & (32 * kPlacers / ways - 1), m = t.row0 + static_cast<int>(rank) * half + row;
   int id = -1;
@@ -790,22 +840,38 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
     v[c] = id >= 0 && 8 * c < p.rank_pad
                ? __ldcg(reinterpret_cast<const uint4*>(p.low + static_cast<size_t>(m) * p.rank_pad) + c)
                : make_uint4(0, 0, 0, 0);
-  for (int st = a.st; st < a.st_end; ++st) {
-    bool ok = wait_bounded(full0 + C::kLandedOff + 8 * q.ring.slot, (q.phases >> q.ring.slot) & 1u, ctl,
-                           (kRolePlacer << 8) | 2);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return false;
-    q.phases ^= 1u << q.ring.slot;
-    if ((st - a.st) % C::kTeams == TEAM) {
-      const uint32_t sw = base + q.ring.slot * C::kStage;
-      const bool marked = p.unit_cols == 16   ? place_stage<16, C>(p, a, sw, st, id, i, row, ways, half, v)
-                          : p.unit_cols == 32 ? place_stage<32, C>(p, a, sw, st, id, i, row, ways, half, v)
-                                              : place_stage<64, C>(p, a, sw, st, id, i, row, ways, half, v);
-      if (marked) marks[local % kMarks] = 1;
+  // What the teams' warps saw, of this tile and the next two.
+  volatile int* seen = marks + kMarks;
+  const bool odd = look_over(p, t, rank, i + TEAM * 32 * kPlacers, 32 * kPlacers * C::kTeams);
+  if (odd) seen[local % 3] = 1;
+  if (TEAM == 0 && i == 0) seen[(local + 1) % 3] = 0;   // read by all two tiles ago
+  __syncwarp();
+  if (lane == 0) mbar_arrive(full0 + C::kLookedOff);
+  bool all = wait_bounded(full0 + C::kLookedOff, local & 1u, ctl, (kRolePlacer << 8) | 5);
+  if (!__all_sync(0xffffffffu, all)) return false;
+  const bool marked = seen[local % 3] != 0;
+  for (int st = a.st; st < a.st_end; ++st, ++q.count) {
+    if (q.count % C::kTeams == TEAM) {
+      const uint32_t phase = (q.phases >> q.ring.slot) & 1u;
+      bool ok = wait_bounded(full0 + C::kGrantedOff + 8 * q.ring.slot, phase, ctl, (kRolePlacer << 8) | 1);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      // (The producer is few tiles past the epilogue here: kMarks are enough.)
+      if (marked && i == 0) marks[local % kMarks] = 1;
+      const uint32_t sw = base + q.ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
+      if (p.unit_cols == 16)
+        place_stage<16, C>(p, a, sx, st, id, i, row, ways, half, v);
+      else if (p.unit_cols == 32)
+        place_stage<32, C>(p, a, sx, st, id, i, row, ways, half, v);
+      else
+        place_stage<64, C>(p, a, sx, st, id, i, row, ways, half, v);
+      ok = wait_bounded(full0 + C::kLandedOff + 8 * q.ring.slot, phase, ctl, (kRolePlacer << 8) | 2);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (marked) take_out<C>(p, sw, a.units_in(st), i);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) sign_pair(lead0 + 8 * q.ring.slot);
     }
+    q.phases ^= 1u << q.ring.slot;
     q.ring.template next<C::S>();
   }
   return true;
@@ -820,26 +886,6 @@ __device__ void place_rows(const RoutedParams& p, const Groups& g, int tiles, ui
   Walk walk;
   walk.begin(p, tiles);
   Tile t;
-  if constexpr (C::HALF) {
-    // The adapters' weights for the first tile's columns, into L2 while the base
-    // product streams: read at its end, each would wait for memory. The ids are
-    // the caller's, so they may be read at once; repeats are found per warp.
-    if (walk.step<C>(p, g, t)) {
-      const int col = t.col0 + static_cast<int>(rank) * p.cta_cols;
-      const uint32_t bytes = 2u * static_cast<uint32_t>(max(min(p.cta_cols, p.N - col), 0)) * p.rank;
-      for (int m = i; m < p.M && bytes; m += 32 * kPlacers) {
-        const int id = p.adapter[m];
-        const uint32_t same = __match_any_sync(__activemask(), id);
-        if (id >= 0 && id < p.L && (i & 31) == __ffs(same) - 1)
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                           p.b + (static_cast<size_t>(id) * p.N + col) * p.rank),
-                       "r"(bytes)
-                       : "memory");
-      }
-      __syncwarp();
-    }
-    walk.begin(p, tiles);
-  }
   grid_dependency_wait();
   Placing q;
   for (uint32_t local = 0; walk.step<C>(p, g, t); ++local)
@@ -1121,7 +1167,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
     if constexpr (C::KIND == kLora || C::GATHER)
       for (int i = 0; i < C::S; ++i)
         mbar_init(bars + C::kLandedOff + 8 * i, C::GATHER ? 32 * kPlacers : 1);
-    for (int i = 0; i < kMarks; ++i) marks[i] = 0;
+    if constexpr (C::KIND == kLora)
+      for (int i = 0; i < C::S; ++i) mbar_init(bars + C::kGrantedOff + 8 * i, 1);
+    if constexpr (C::KIND == kLora) {
+      mbar_init(bars + C::kLookedOff, kPlacers * C::kTeams);
+      for (int i = 0; i < kMarks + 3; ++i) marks[i] = 0;
+    }
     *abort_flag = 0;
     *last_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1142,11 +1193,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
   // and the roles wait before they read what the low-rank kernel writes.
   Groups g{};
   int tiles;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (C::KIND == kLora) {
     tiles = p.m_tiles * p.n_tiles;
   } else {
     grid_dependency_wait();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int* mem = reinterpret_cast<int*>(base_ptr + C::kGroupsOff);
     g.row = mem;
     g.count = mem + kMaxGroups;
@@ -1174,7 +1225,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
     // Every thread, also one without a tile: this grid must not complete before
     // the low-rank kernel has.
     grid_dependency_wait();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
   tc_fence_before_sync();
   cluster_barrier();   // no CTA leaves while its peer may still signal it

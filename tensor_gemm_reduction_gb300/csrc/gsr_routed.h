@@ -70,14 +70,12 @@ struct LowRankParams {
   const uint16_t* x[kMaxShards];    // M x K_r
   const uint16_t* a[kMaxShards];    // L x rank x K_r
   int64_t k[kMaxShards];
-  int unit_begin[kMaxShards + 1];   // first 64-column unit of shard r
   const int32_t* adapter;
   const float* scale;               // NULL: 1
   uint16_t* low;
   int32_t* lists;
   int M, R, L, rank, rank_pad;
   int tile_tokens, m_tiles;         // of the product that reads the lists
-  int rows_per_cta;                 // 16 (the warps share the reduction) or 128
 };
 
 struct RouteParams {
@@ -106,6 +104,7 @@ constexpr int kRoutedSmall = 64, kRoutedMid = 128, kRoutedWide = 256;
 constexpr int routed_kblocks(bool half, int tokens) { return half && tokens <= kRoutedMid ? 4 : 2; }
 
 cudaError_t prepare_routed_kernels();
+cudaError_t prepare_lowrank_kernels();
 cudaError_t prepare_route_kernels();
 // half: tiles of at most 128 weight rows (kLora).
 cudaError_t launch_routed(const RoutedParams& p, int kind, bool gather, bool half, int tokens, int ctas,

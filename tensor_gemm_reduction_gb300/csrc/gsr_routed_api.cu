@@ -385,12 +385,10 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
   p.policy_x = m_tiles == 1 ? gsr::kPolicyEvictLast : gsr::kPolicyNormal;
   gsr::LowRankParams q;
   std::memset(&q, 0, sizeof q);
-  int st = 0, unit = 0;
+  int st = 0;
   for (int r = 0; r < R; ++r) {
     p.shard_st_begin[r] = st;
     st += static_cast<int>(cdiv(K_r[r], kStageK));
-    q.unit_begin[r] = unit;
-    unit += static_cast<int>(cdiv(K_r[r], 64));
     q.x[r] = static_cast<const uint16_t*>(X_r[r]);
     q.a[r] = static_cast<const uint16_t*>(A_r[r]);
     q.k[r] = K_r[r];
@@ -398,10 +396,7 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
     if (cr == CUDA_SUCCESS) cr = encode_2d(&p.tmap_x[r], X_r[r], M, K_r[r], static_cast<int>(width / 2));
     if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding shard %d's descriptors failed (%d)", r, (int)cr);
   }
-  for (int r = R; r <= gsr::kMaxShards; ++r) {
-    p.shard_st_begin[r] = st;
-    q.unit_begin[r] = unit;
-  }
+  for (int r = R; r <= gsr::kMaxShards; ++r) p.shard_st_begin[r] = st;
   CUresult cr = encode_stack(&p.tmap_b, B, L, N, rank, p.unit_cols, p.w_rows);
   if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding the B descriptor failed (%d)", (int)cr);
   q.adapter = adapter;
@@ -415,8 +410,6 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
   q.rank_pad = p.rank_pad;
   q.tile_tokens = p.tile_tokens;
   q.m_tiles = p.m_tiles;
-  // Few rows: the warps of a CTA share the reduction of 16; many: 16 rows each.
-  q.rows_per_cta = M <= 256 ? 16 : 128;
   DeviceScope scope(P->device);
   if (scope.err != cudaSuccess) return cuda_fail(scope.err, "selecting the plan's device");
   cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
