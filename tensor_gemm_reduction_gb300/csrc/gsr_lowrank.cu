@@ -263,9 +263,8 @@ __device__ __forceinline__ void write_rows(const LowRankParams& p, float* share,
   cluster_sync_reads();   // read by all before the next share is written
 }
 
-// The product that follows may start once every block has read its operands (or
-// has left): started earlier, its stream of weights held this kernel's reads back
-// (64 adapters, 128 rows: 20 us in place of 9).
+// The product that follows may start its blocks where these leave room, and its
+// base product with them: everything before this kernel has completed by now.
 __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -295,6 +294,7 @@ __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_few_kernel(const _
   constexpr int kCols = 8 * NT < kShareCols ? 8 * NT : kShareCols, kTurnTiles = kCols / 8;
   shards.fill(p);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int z = static_cast<int>(blockIdx.z), ctas = static_cast<int>(gridDim.z);
   const int nth = static_cast<int>(blockIdx.y);
@@ -377,7 +377,6 @@ __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_few_kernel(const _
     for (int pass = 0; pass < p.rank_pad; pass += 8 * NT) {
       float acc[NT][4] = {};
       Stream<16, NT>::run(p, shards, ring, group_rows, a, pass, z, ctas, acc);
-      let_next_start();
 #pragma unroll
       for (int n0 = 0; n0 < NT; n0 += kTurnTiles) {
         put_share<kTurnTiles>(share, acc + n0, kCols);
@@ -397,7 +396,7 @@ __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __gri
   constexpr int kCols = 8 * NT < kShareCols ? 8 * NT : kShareCols, kTurnTiles = kCols / 8;
   shards.fill(p);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  let_next_start();   // the product's blocks fit only when these leave
+  let_next_start();
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int z = static_cast<int>(blockIdx.z), ctas = static_cast<int>(gridDim.z);
   const int blocks = (p.M + 16 * kWarps - 1) / (16 * kWarps);

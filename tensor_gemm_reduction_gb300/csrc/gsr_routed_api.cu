@@ -223,7 +223,7 @@ gsr_status gemm_group_route(const gemm_shard_plan* P, int64_t T, int topk, int E
     return fail(GSR_ERR_INVALID_VALUE, "E=%d outside 1..%d", E, gsr::kMaxGroups);
   if (topk < 1 || topk > gsr::kMaxTopk)
     return fail(GSR_ERR_INVALID_VALUE, "topk=%d outside 1..%d", topk, gsr::kMaxTopk);
-  if (T < 0 || T * topk > P->max_M || T > P->max_M)
+  if (T < 0 || T > P->max_M || T * topk > P->max_M)
     return fail(GSR_ERR_INVALID_VALUE, "T=%lld: T * topk outside 0..%lld (the plan's max_M)",
                 (long long)T, (long long)P->max_M);
   if (T * topk > (int64_t(1) << 30))

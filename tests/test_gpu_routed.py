@@ -56,6 +56,25 @@ def test_route_of_no_tokens_and_of_dropped_ones(setup):
     assert not offsets.any() and (source == -1).all() and (position == -1).all()
 
 
+@pytest.mark.parametrize("T,topk,E", [(32768, 8, 3), (140000, 2, 1024)])
+def test_route_of_many_entries(T, topk, E):
+    """The largest number of entries that stays in registers, and more than that."""
+    plan = B.gemm_shard_plan_create(0, T * topk, 64, 64, 1)
+    ids = torch.randint(-1, E, (T, topk), generator=U.gen(E), device=U.DEV)
+    i32 = dict(dtype=torch.int32, device=U.DEV)
+    offsets, source, position = torch.empty(E + 1, **i32), torch.empty(T * topk, **i32), torch.empty(T, topk, **i32)
+    B.gemm_group_route(plan, ids, E, offsets, source, position)
+    flat = ids.reshape(-1)
+    order = torch.argsort(torch.where(flat < 0, E, flat), stable=True)
+    kept = int((flat >= 0).sum())
+    assert torch.equal(offsets[1:].long(), torch.bincount(flat[flat >= 0], minlength=E).cumsum(0))
+    assert int(offsets[0]) == 0 and (source[kept:] == -1).all()
+    assert torch.equal(source[:kept].long(), order[:kept] // topk)
+    back = torch.full_like(flat, -1)
+    back[order[:kept]] = torch.arange(kept, device=U.DEV)
+    assert torch.equal(position.reshape(-1).long(), back)
+
+
 # ---------------------------------------------------------------- grouped
 
 GROUPS = [
@@ -322,3 +341,14 @@ def test_calls_on_another_stream_and_in_a_graph(setup):
     status_ok(setup)
     # Other rows share a tile now, but a row's sum over k has the same order.
     assert torch.equal(Y, first.flip(0))
+
+
+@pytest.mark.parametrize("tokens,graph", [(1, False), (33, False), (300, True)])
+def test_the_example_runs_them_together(tokens, graph):
+    import importlib.util
+    import os
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer", at)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    assert mod.main(["--tokens", str(tokens)] + (["--graph"] if graph else [])) == 0
