@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_few_kernel(const _
 template <int NT>
 __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __grid_constant__ LowRankParams p) {
   extern __shared__ float share[];                 // the ring; [kWarps][16][columns of a turn]
-  __shared__ int sums[kWarps], keeps[16 * kWarps], at[16 * kWarps], rows[16 * kWarps];
+  __shared__ int sums[kWarps], keeps[16 * kWarps], rows[16 * kWarps];
   __shared__ Shards shards;
   constexpr int kCols = 8 * NT < kShareCols ? 8 * NT : kShareCols, kTurnTiles = kCols / 8;
   shards.fill(p);
@@ -412,7 +412,6 @@ __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __gri
   const int m = static_cast<int>(blockIdx.x) * 16 * kWarps + tid;   // thread i < 128 has row i
   int id = tid < 16 * kWarps && m < p.M ? p.adapter[m] : -1;
   if (id < 0 || id >= p.L) id = -1;
-  if (tid < 16 * kWarps) rows[tid] = m < p.M ? m : -1;
   for (int last = -1;;) {
     // The smallest adapter above the last one.
     const int mine = id > last ? id : INT32_MAX;
@@ -425,7 +424,7 @@ __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __gri
     if (a == INT32_MAX) break;
     last = a;
     if (tid < 16 * kWarps) {
-      at[tid] = id == a ? m : -1;
+      rows[tid] = id == a ? m : -1;   // the others are not read (zeros)
       keeps[tid] = a;
     }
     for (int pass = 0; pass < p.rank_pad; pass += 8 * NT) {
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __gri
 #pragma unroll
       for (int n0 = 0; n0 < NT; n0 += kTurnTiles) {
         put_share<kTurnTiles>(share, acc + n0, kCols);
-        write_rows<kCols, 1>(p, share, at, keeps, pass + 8 * n0, z, ctas);
+        write_rows<kCols, 1>(p, share, rows, keeps, pass + 8 * n0, z, ctas);
       }
     }
   }

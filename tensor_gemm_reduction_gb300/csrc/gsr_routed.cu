@@ -127,11 +127,19 @@ __device__ __forceinline__ void grid_dependency_wait() {
 
 // ------------------------------------------------------------ geometry
 
+// The shards of X and A, read from the parameters at the kernel's start (cold
+// parameters cost a memory access each where they are used).
+struct SelfTable {
+  const uint16_t *x[kMaxShards], *a[kMaxShards];
+  int k[kMaxShards];
+};
+
 template <int KIND_, bool GATHER_, bool HALF_, int TOK_, int KZ_, int STAGES_>
 struct Cfg {
   static constexpr int KIND = KIND_, TOK = TOK_, S = STAGES_, KZ = KZ_;
   static constexpr bool GATHER = GATHER_, HALF = HALF_;
   static constexpr int kTeams = HALF ? 2 : 1;           // kLora: of four warps that place rows
+  static constexpr bool SELF = HALF && TOK == kRoutedSmall;   // may compute the low-rank rows itself
   static constexpr int kRows = HALF ? 64 : 128;         // weight rows of a CTA, at most
   static constexpr int kThreads = 64 + kEpi + (KIND == kLora ? 32 * kPlacers : GATHER ? 32 * (kPlacers + 1) : 0);
   // Arrivals that complete a full barrier: the leader's expect_tx and, from both
@@ -153,10 +161,15 @@ struct Cfg {
   static constexpr uint32_t kMiscOff = kBarsOff + kBars;
   static constexpr uint32_t kStagingOff = (kMiscOff + 16 + 4 * (kMarks + 3) + 127) / 128 * 128;
   static constexpr uint32_t kGroupsOff = kStagingOff + kStaging;
-  static constexpr uint32_t kSmem = 1024 + kGroupsOff + kGroups;
+  static constexpr uint32_t kSelf = SELF ? sizeof(SelfTable) + 8 * 4 * kSelfElements : 0;
+  static constexpr uint32_t kSmem = 1024 + kGroupsOff + kGroups + kSelf;
   static_assert(kSmem <= kSmallSmemLimit, "shared memory");
   static_assert(kX % 1024 == 0, "swizzle atoms");
-  static constexpr uint32_t kTmemCols = 2 * TOK;
+  static_assert(!GATHER || TOK <= 256, "gathered rows: one MMA's tokens");
+  // Accumulators: two, so that a tile's epilogue runs beside the next tile's
+  // MMAs, or one of 512 tokens.
+  static constexpr uint32_t kAccs = TOK == 512 ? 1 : 2;
+  static constexpr uint32_t kTmemCols = kAccs * TOK;
 };
 
 // The groups as every CTA counts them (shared memory).
@@ -165,7 +178,8 @@ struct Groups {
 };
 
 struct Tile {
-  int row0, rows, n;          // first row of Y, rows, MMA columns (a multiple of 16)
+  int row0, rows, n;          // first row of Y, rows, MMA columns (a multiple of 16; above
+                              // 256 in two MMAs, see halves)
   int col0;                   // first output column of the pair
   int group, m;               // group; lora: token tile
   int piece, npieces, slot, cut;    // cut: index among the cut tiles
@@ -219,6 +233,16 @@ __device__ __forceinline__ void place(const RoutedParams& p, const Groups& g, in
   t.rows = min(width, count - t.m * width);
   t.n = C::KIND == kLora ? width : (t.rows + 15) & ~15;
 }
+
+// A CTA's rows of the tokens [0, n) of a tile: with n <= 256, h[0] = n / 2 rows from
+// rank * h[0] on; with more, two MMAs' worth, the second from 2 h[0] + rank * h[1] on.
+struct Halves {
+  int h[2];
+  __device__ __forceinline__ explicit Halves(int n) {
+    h[0] = n <= 256 ? n / 2 : ((n / 2 + 15) / 16) * 8;
+    h[1] = n / 2 - h[0];
+  }
+};
 
 // Every role walks the same tiles: this worker's range of the cut tiles, then
 // its whole tiles.
@@ -343,12 +367,32 @@ struct AdapterSteps {
   template <class C>
   __device__ __forceinline__ void begin(const RoutedParams& p, const Tile& t) {
     list = p.lists + static_cast<size_t>(t.m) * kAdapterListStride;
-    units = __ldcg(list) * p.units_per_adapter;
+    const bool self = C::SELF && p.self_rows;
+    int count = 0, own = -1;
+    uint32_t leaders = 0;
+    if (self) {
+      // No list for so few rows: their adapters in the order of their first rows.
+      const int lane = static_cast<int>(threadIdx.x) & 31;
+      own = lane < p.M ? p.adapter[lane] : -1;
+      if (own >= p.L) own = -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, own);
+      leaders = __ballot_sync(0xffffffffu, own >= 0 && (same & ((1u << lane) - 1u)) == 0);
+      count = __popc(leaders);
+    } else {
+      count = __ldcg(list);
+    }
+    units = count * p.units_per_adapter;
     per_stage = C::KZ * 64 / p.unit_cols;
     const int stages = (units + per_stage - 1) / per_stage;
     st = t.st * stages / p.stages_per_tile;
     st_end = t.st_end * stages / p.stages_per_tile;
-    hold(st * per_stage / p.units_per_adapter);
+    if (self) {
+      first = 0;
+      const int lane = static_cast<int>(threadIdx.x) & 31;
+      held = __shfl_sync(0xffffffffu, own, lane < count ? __fns(leaders, 0, lane + 1) : 0);
+    } else {
+      hold(st * per_stage / p.units_per_adapter);
+    }
   }
   // (Past the list's end: whatever the workspace holds, never used.)
   __device__ __forceinline__ void hold(int at) {
@@ -468,8 +512,16 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
             if constexpr (C::KIND == kGated)
               copy_3d(dw + C::kW / 2, &p.tmap_w[0], lead, kx + j * BK, p.N + w_row, t.group, pol_w);
             // The map whose boxes are exactly this tile's rows.
-            if constexpr (!C::GATHER)
+            if constexpr (!C::GATHER && C::TOK <= 256)
               copy_2d(sx + j * C::kX, &p.tmap_x[half / 8 - 1], lead, kx + j * BK, x_row, pol_x);
+            if constexpr (!C::GATHER && C::TOK > 256) {
+              const Halves q(t.n);
+              copy_2d(sx + j * C::kX, &p.tmap_x[q.h[0] / 8 - 1], lead, kx + j * BK,
+                      t.row0 + static_cast<int>(rank) * q.h[0], pol_x);
+              if (q.h[1])
+                copy_2d(sx + j * C::kX + q.h[0] * 128, &p.tmap_x[q.h[1] / 8 - 1], lead, kx + j * BK,
+                        t.row0 + 2 * q.h[0] + static_cast<int>(rank) * q.h[1], pol_x);
+            }
           }
         }
       }
@@ -550,13 +602,15 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
   Tile t, tn;
   bool have = walk.step<C>(p, g, t);
   for (; ok && have; ++local) {
-    const uint32_t acc = local & 1u;
-    ok = wait_bounded(tempty0 + 8 * acc, ((local >> 1) & 1u) ^ 1u, ctl, (kRoleMma << 8) | 1);
+    const uint32_t acc = local % C::kAccs;
+    ok = wait_bounded(tempty0 + 8 * acc, ((local / C::kAccs) & 1u) ^ 1u, ctl, (kRoleMma << 8) | 1);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     tc_fence_after_sync();
     const uint32_t d = tmem + acc * C::TOK;
-    const uint32_t idesc = make_idesc(2 * C::kRows, static_cast<uint32_t>(t.n));
+    const Halves q(t.n);
+    const uint32_t idesc = make_idesc(2 * C::kRows, static_cast<uint32_t>(C::TOK > 256 ? 2 * q.h[0] : t.n));
+    const uint32_t idesc2 = make_idesc(2 * C::kRows, static_cast<uint32_t>(2 * q.h[1]));
     bool looked = false, have_next = false;
     AdapterSteps a{};
     if constexpr (C::KIND == kLora)
@@ -568,9 +622,15 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
       tc_fence_after_sync();
       const uint32_t sw = base + ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
 #pragma unroll
-      for (int j = 0; j < C::KZ; ++j)
+      for (int j = 0; j < C::KZ; ++j) {
         mma4_bf16_pair(d, smem_desc_sw128(sw + j * C::kW), smem_desc_sw128(sx + j * C::kX), idesc,
                        (st > t.st || j > 0) ? 1u : 0u);
+        if constexpr (C::TOK > 256)
+          if (q.h[1])
+            mma4_bf16_pair(d + 2 * q.h[0], smem_desc_sw128(sw + j * C::kW),
+                           smem_desc_sw128(sx + j * C::kX + q.h[0] * 128), idesc2,
+                           (st > t.st || j > 0) ? 1u : 0u);
+      }
       issued = true;
       mma_commit_pair(empty0 + 8 * ring.slot, 0x3);
       ring.next<C::S>();
@@ -760,16 +820,17 @@ __device__ __forceinline__ void add_zeros(uint32_t& sum, const uint4& w) {
 // adapters (this CTA's weight rows of them) are looked over while the base
 // product streams. That also brings them into L2 for the copies to come. Thread
 // `who` of `threads`; true if a weight that it read is not finite.
-__device__ __forceinline__ bool look_over(const RoutedParams& p, const Tile& t, uint32_t rank, int who,
-                                          int threads) {
-  const int32_t* list = p.lists + static_cast<size_t>(t.m) * kAdapterListStride;
-  const int count = __ldcg(list), lane = who & 31;
+template <class C>
+__device__ __forceinline__ bool look_over(const RoutedParams& p, const Tile& t, const AdapterSteps& steps,
+                                          uint32_t rank, int who, int threads) {
+  const int count = steps.units / p.units_per_adapter, lane = who & 31;
+  const bool self = C::SELF && p.self_rows;
   const int col = t.col0 + static_cast<int>(rank) * p.cta_cols;
   const int vecs = max(min(p.cta_cols, p.N - col), 0) * p.rank / 8;   // 16-byte vectors, contiguous
   uint32_t sum[4] = {0, 0, 0, 0};
   for (int i = who >> 5; i < count; i += threads >> 5) {
-    const uint4* w = reinterpret_cast<const uint4*>(
-        p.b + (static_cast<size_t>(__ldcg(list + 1 + i)) * p.N + col) * p.rank);
+    const int id = self ? __shfl_sync(0xffffffffu, steps.held, i) : __ldcg(steps.list + 1 + i);
+    const uint4* w = reinterpret_cast<const uint4*>(p.b + (static_cast<size_t>(id) * p.N + col) * p.rank);
     for (int at = lane; at < vecs; at += 4 * 32) {
       uint4 x[4];
 #pragma unroll
@@ -805,6 +866,67 @@ __device__ __noinline__ void take_out(const RoutedParams& p, uint32_t sw, int un
     }
 }
 
+// Up to kSelfRows rows: the two teams compute the low-rank rows themselves, in
+// every CTA that holds them, from L2 and while the weights stream, and no kernel
+// runs before the product. The 8 warps take every 8th chunk of 256 k of all columns
+// (16 rows of A in flight per warp); part[w][m][j] is warp w's sum.
+__device__ __forceinline__ void self_rows(const RoutedParams& p, const SelfTable& s, float* part, int who) {
+  const int lane = who & 31, warp = who >> 5;
+  for (int m = 0; m < p.M; ++m) {
+    const int id = p.adapter[m];
+    if (id < 0 || id >= p.L) continue;
+    for (int j0 = 0; j0 < p.rank_pad; j0 += 16) {
+      float sum[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum[j] = 0.f;
+      int at = 8 * lane + 256 * warp;   // this lane's k in shard r
+      for (int r = 0; r < p.R;) {
+        const int K = s.k[r], chunks = (K + 255) >> 8;
+        if (at >= chunks * 256) {
+          at -= chunks * 256;
+          ++r;
+          continue;
+        }
+        if (at < K) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(s.x[r] + static_cast<size_t>(m) * K + at));
+          const uint16_t* a = s.a[r] + (static_cast<size_t>(id) * p.rank + j0) * K + at;
+          uint4 v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            v[j] = j0 + j < p.rank ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<size_t>(j) * K))
+                                   : make_uint4(0, 0, 0, 0);
+          const uint32_t xw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint32_t aw[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sum[j] = fmaf(__uint_as_float(xw[i] << 16), __uint_as_float(aw[i] << 16), sum[j]);
+              sum[j] = fmaf(__uint_as_float(xw[i] & 0xffff0000u), __uint_as_float(aw[i] & 0xffff0000u), sum[j]);
+            }
+          }
+        }
+        __syncwarp();
+        at += 8 * 256;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+        if (lane == j) part[warp * kSelfElements + m * p.rank_pad + j0 + j] = sum[j];
+      }
+    }
+  }
+}
+
+// Element (m, j) of the rows that self_rows summed, as bf16 bits.
+__device__ __forceinline__ uint32_t self_low(const RoutedParams& p, const float* part, int m, int j, float scale) {
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) sum += part[w * kSelfElements + m * p.rank_pad + j];
+  return __bfloat16_as_ushort(__float2bfloat16(sum * scale));
+}
+
 // The adapter stages of one tile, for one team of four warps (thread `i` of
 // them). The threads are the rows of this CTA's tokens, or, with at most 64 or 32
 // rows, two or four times the rows, on alternate adapters. The rows are placed
@@ -819,6 +941,8 @@ struct Placing {
   Ring ring;
   uint32_t phases = 0;   // bit s: phase of slot s's granted and landed barriers
   uint32_t count = 0;    // adapter stages so far: the teams take turns
+  const SelfTable* table;   // shared memory, for self_rows
+  float* part;              // its sums
 };
 template <int TEAM, class C>
 __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local, Placing& q, int i,
@@ -835,14 +959,20 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
   uint4 v[kMaxRank / 8];
   if (row < half && m < p.M) id = p.adapter[m];
   if (id >= p.L) id = -1;   // no adapter of the list is negative
+  const bool self = C::SELF && p.self_rows;
+  if (self) {
+    // Half a tile's tokens are 8 at least, so rank 0 holds every row.
+    if (local == 0 && rank == 0) self_rows(p, *q.table, q.part, i + TEAM * 32 * kPlacers);
+  } else {
 #pragma unroll
-  for (int c = 0; c < kMaxRank / 8; ++c)
-    v[c] = id >= 0 && 8 * c < p.rank_pad
-               ? __ldcg(reinterpret_cast<const uint4*>(p.low + static_cast<size_t>(m) * p.rank_pad) + c)
-               : make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < kMaxRank / 8; ++c)
+      v[c] = id >= 0 && 8 * c < p.rank_pad
+                 ? __ldcg(reinterpret_cast<const uint4*>(p.low + static_cast<size_t>(m) * p.rank_pad) + c)
+                 : make_uint4(0, 0, 0, 0);
+  }
   // What the teams' warps saw, of this tile and the next two.
   volatile int* seen = marks + kMarks;
-  const bool odd = look_over(p, t, rank, i + TEAM * 32 * kPlacers, 32 * kPlacers * C::kTeams);
+  const bool odd = look_over<C>(p, t, a, rank, i + TEAM * 32 * kPlacers, 32 * kPlacers * C::kTeams);
   if (odd) seen[local % 3] = 1;
   if (TEAM == 0 && i == 0) seen[(local + 1) % 3] = 0;   // read by all two tiles ago
   __syncwarp();
@@ -850,6 +980,20 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
   bool all = wait_bounded(full0 + C::kLookedOff, local & 1u, ctl, (kRolePlacer << 8) | 5);
   if (!__all_sync(0xffffffffu, all)) return false;
   const bool marked = seen[local % 3] != 0;
+  if (self) {
+    const float scale = id >= 0 && p.scale ? __ldg(p.scale + id) : 1.f;
+#pragma unroll
+    for (int c = 0; c < kMaxRank / 8; ++c) {
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (8 * c < kSelfElements && id >= 0 && 8 * c < p.rank_pad) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = self_low(p, q.part, m, 8 * c + 2 * i, scale) |
+                 self_low(p, q.part, m, 8 * c + 2 * i + 1, scale) << 16;
+      }
+      v[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
   for (int st = a.st; st < a.st_end; ++st, ++q.count) {
     if (q.count % C::kTeams == TEAM) {
       const uint32_t phase = (q.phases >> q.ring.slot) & 1u;
@@ -881,13 +1025,12 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
 // which then wait for the accumulator, are team 1.
 template <class C>
 __device__ void place_rows(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
-                           uint32_t rank, volatile int* marks, const Ctl& ctl) {
+                           uint32_t rank, Placing q, volatile int* marks, const Ctl& ctl) {
   const int i = static_cast<int>(threadIdx.x) - 64 - kEpi;
   Walk walk;
   walk.begin(p, tiles);
   Tile t;
   grid_dependency_wait();
-  Placing q;
   for (uint32_t local = 0; walk.step<C>(p, g, t); ++local)
     if (!place_tile<0, C>(p, t, local, q, i, base, rank, marks, ctl)) break;
 }
@@ -897,8 +1040,8 @@ __device__ void place_rows(const RoutedParams& p, const Groups& g, int tiles, ui
 // (`valid` rows from `row` on, columns from `col` to `end`), for the adapters of
 // this piece.
 template <class C>
-__device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t, int row, int valid, int col,
-                                           int end, float (&v)[32]) {
+__device__ __noinline__ void add_unbounded(const RoutedParams& p, const float* part, const Tile& t, int row,
+                                           int valid, int col, int end, float (&v)[32]) {
   AdapterSteps a{};
   a.template begin<C>(p, t);
   const int u0 = a.st * a.per_stage, u1 = min(a.st_end * a.per_stage, a.units);
@@ -910,8 +1053,19 @@ __device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t,
     const int m = row + token;
     const int id = token < valid && n < end ? p.adapter[m] : -1;
     if (id < 0 || id >= p.L) continue;
+    // Its place in the tile's list, which has every row's adapter (computed rows:
+    // the adapters that appear first in earlier rows).
     int at = 0;
-    while (__ldcg(a.list + 1 + at) != id) ++at;   // the tile's list has every row's adapter
+    if (C::SELF && p.self_rows) {
+      for (int i0 = 0; p.adapter[i0] != id; ++i0) {
+        const int other = p.adapter[i0];
+        bool first = other >= 0 && other < p.L;
+        for (int i1 = 0; i1 < i0; ++i1) first = first && p.adapter[i1] != other;
+        at += first;
+      }
+    } else {
+      while (__ldcg(a.list + 1 + at) != id) ++at;
+    }
     float sum = 0.f;
     bool any = false;
     for (int k = 0; k < p.rank; ++k) {
@@ -919,7 +1073,9 @@ __device__ __noinline__ void add_unbounded(const RoutedParams& p, const Tile& t,
       if (u < u0 || u >= u1) continue;
       const uint32_t w = p.b[(static_cast<size_t>(id) * p.N + n) * p.rank + k];
       if ((w & 0x7f80u) != 0x7f80u) continue;
-      const uint32_t x = __ldcg(p.low + static_cast<size_t>(m) * p.rank_pad + k);
+      const uint32_t x = C::SELF && p.self_rows
+                             ? self_low(p, part, m, k, p.scale ? __ldg(p.scale + id) : 1.f)
+                             : __ldcg(p.low + static_cast<size_t>(m) * p.rank_pad + k);
       sum += __uint_as_float(w << 16) * __uint_as_float(x << 16);
       any = true;
     }
@@ -958,7 +1114,7 @@ __device__ __forceinline__ void store_tokens(uint16_t* y, int N, int row, int va
 template <class C>
 __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
                        uint8_t* base_ptr, uint32_t tmem, uint32_t rank, volatile int* last_flag,
-                       volatile int* marks, const Ctl& ctl) {
+                       Placing placing, volatile int* marks, const Ctl& ctl) {
   const uint32_t tfull0 = base + C::kBarsOff + 16 * C::S, tempty0 = tfull0 + 16;
   const int et = static_cast<int>(threadIdx.x) - 64;
   const int lane = static_cast<int>(threadIdx.x) & 31;
@@ -970,7 +1126,6 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
   float* swap = reinterpret_cast<float*>(base_ptr + C::kStagingOff);
   const uint32_t staging = base + C::kStagingOff + quad * 2048;
   uint32_t local = 0;
-  Placing placing;
   Walk walk;
   walk.begin(p, tiles);
   Tile t, tn;
@@ -978,13 +1133,13 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
   for (; have; ++local) {
     t = tn;
     have = walk.step<C>(p, g, tn);   // while this tile's accumulator fills
-    const uint32_t acc = local & 1u;
+    const uint32_t acc = local % C::kAccs;
     bool placed = true;
     if constexpr (C::KIND == kLora && C::HALF) {
       if (local == 0) grid_dependency_wait();
       placed = place_tile<1, C>(p, t, local, placing, et, base, rank, marks, ctl);
     }
-    const bool ok = placed && wait_bounded(tfull0 + 8 * acc, (local >> 1) & 1u, ctl, (kRoleEpilogue << 8) | 1);
+    const bool ok = placed && wait_bounded(tfull0 + 8 * acc, (local / C::kAccs) & 1u, ctl, (kRoleEpilogue << 8) | 1);
     if (!epilogue_bar_and(ok)) break;
     tc_fence_after_sync();
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::TOK;
@@ -1010,7 +1165,8 @@ __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
       if constexpr (C::KIND == kLora) {
-        if (marked) add_unbounded<C>(p, t, t.row0 + tok0 + 32 * c, mine - 32 * c, col0 + wrow, col_end, v);
+        if (marked)
+          add_unbounded<C>(p, placing.part, t, t.row0 + tok0 + 32 * c, mine - 32 * c, col0 + wrow, col_end, v);
       }
     };
     auto release = [&]() {
@@ -1148,6 +1304,18 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
   const int warp = static_cast<int>(threadIdx.x) >> 5;
   const uint32_t rank = cluster_rank();
   const uint32_t bars = base + C::kBarsOff;
+  Placing placing{};
+  if constexpr (C::SELF) {
+    SelfTable* table = reinterpret_cast<SelfTable*>(base_ptr + C::kGroupsOff);
+    placing.table = table;
+    placing.part = reinterpret_cast<float*>(table + 1);
+    if (p.self_rows && threadIdx.x >= 64 && threadIdx.x < 64 + kMaxShards) {
+      const int r = static_cast<int>(threadIdx.x) - 64;
+      table->x[r] = p.x_r[r];
+      table->a[r] = p.a_r[r];
+      table->k[r] = p.k_r[r];
+    }
+  }
   if (warp == 1) {
     prefetch_tensormap(&p.tmap_w[0]);
     if constexpr (!C::GATHER) prefetch_tensormap(&p.tmap_x[0]);
@@ -1188,13 +1356,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
   // Programmatic dependent launch. The grouped kinds wait here for the previous
-  // kernel. kLora follows the low-rank kernel, which lets it start only once
-  // everything before that kernel has completed: X and W may be read at once,
-  // and the roles wait before they read what the low-rank kernel writes.
+  // kernel, and kLora where it computes the low-rank rows itself. Else kLora follows
+  // the low-rank kernel, which lets it start only once everything before that kernel
+  // has completed: X and W may be read at once, and the roles wait before they read
+  // what the low-rank kernel writes.
   Groups g{};
   int tiles;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (C::KIND == kLora) {
+    if (C::SELF && p.self_rows) grid_dependency_wait();
     tiles = p.m_tiles * p.n_tiles;
   } else {
     grid_dependency_wait();
@@ -1211,9 +1381,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
   } else if (warp == 1) {
     if (rank == 0) multiply<C>(p, g, tiles, base, tmem, ctl);
   } else if (warp < 6) {
-    finish<C>(p, g, tiles, base, base_ptr, tmem, rank, last_flag, marks, ctl);
+    finish<C>(p, g, tiles, base, base_ptr, tmem, rank, last_flag, placing, marks, ctl);
   } else if constexpr (C::KIND == kLora) {
-    place_rows<C>(p, g, tiles, base, rank, marks, ctl);
+    place_rows<C>(p, g, tiles, base, rank, placing, marks, ctl);
   } else if constexpr (C::GATHER) {
     if (warp < 6 + kPlacers)
       gather_rows<C>(p, g, tiles, base, rank, ctl);
@@ -1237,7 +1407,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
 // Ring depths that fill shared memory.
 template <int KIND, bool GATHER, int TOK>
 using Instance = Cfg<KIND, GATHER, false, TOK, routed_kblocks(false, TOK),
-                     TOK == kRoutedSmall ? 5 : TOK == kRoutedMid ? 4 : 3>;
+                     TOK == kRoutedSmall ? 5 : TOK == kRoutedWide ? 3 : 4>;
 // Few tokens: tiles of at most 128 weight rows.
 template <int TOK>
 using HalfInstance = Cfg<kLora, false, true, TOK, routed_kblocks(true, TOK),
@@ -1273,6 +1443,8 @@ cudaError_t set_limits() {
   cudaError_t e = set_limit<Instance<KIND, GATHER, kRoutedSmall>>();
   if (e == cudaSuccess) e = set_limit<Instance<KIND, GATHER, kRoutedMid>>();
   if (e == cudaSuccess) e = set_limit<Instance<KIND, GATHER, kRoutedWide>>();
+  if constexpr (!GATHER)
+    if (e == cudaSuccess) e = set_limit<Instance<KIND, GATHER, kRoutedDouble>>();
   return e;
 }
 
@@ -1280,6 +1452,8 @@ template <int KIND, bool GATHER>
 cudaError_t launch_kind(const RoutedParams& p, int tokens, int ctas, cudaStream_t stream) {
   if (tokens == kRoutedSmall) return launch_one<Instance<KIND, GATHER, kRoutedSmall>>(p, ctas, stream);
   if (tokens == kRoutedMid) return launch_one<Instance<KIND, GATHER, kRoutedMid>>(p, ctas, stream);
+  if constexpr (!GATHER)
+    if (tokens == kRoutedDouble) return launch_one<Instance<KIND, GATHER, kRoutedDouble>>(p, ctas, stream);
   return launch_one<Instance<KIND, GATHER, kRoutedWide>>(p, ctas, stream);
 }
 

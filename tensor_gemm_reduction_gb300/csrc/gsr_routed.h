@@ -25,7 +25,7 @@ enum RoutedKind : int { kGrouped = 0, kGated = 1, kLora = 2 };
 // fp32 partials of cut tiles; then the adapters' low-rank rows and lists.
 constexpr size_t kRoutedCounterBytes = 8192;
 constexpr int kRoutedTileRows = 256;        // weight rows of a CTA pair's tile
-constexpr int kRoutedMaxTokens = 256;       // tokens of a tile, at most
+constexpr int kRoutedMaxTokens = 256;       // tokens of a tile, at most (kLora)
 // One adapter list per token tile: a count, then the tile's adapters ascending.
 constexpr int kAdapterListStride = kRoutedMaxTokens + 8;
 
@@ -45,6 +45,10 @@ struct RoutedParams {  // 128-byte aligned through its CUtensorMap members
   const int32_t* lists;             // lora: adapter lists of the token tiles
   const uint16_t* low;              // lora: M x rank_pad, the scaled low-rank rows
   const uint16_t* b;                // lora: L x N x rank
+  const uint16_t *x_r[kMaxShards], *a_r[kMaxShards];   // lora, self_rows: the operands of the
+  int k_r[kMaxShards];                                 // low-rank rows
+  const float* scale;
+  int self_rows;                    // lora: the product computes the low-rank rows itself
   uint16_t* y;                      // M x N
   uint32_t* status;
   uint32_t* counters;
@@ -63,6 +67,10 @@ struct RoutedParams {  // 128-byte aligned through its CUtensorMap members
   int policy_w, policy_x;
   int shard_st_begin[kMaxShards + 1];  // lora: first stage of shard r
 };
+
+// Calls of this few rows and columns (M * rank_pad) compute the low-rank rows in the
+// product.
+constexpr int kSelfRows = 4, kSelfElements = 32;
 
 // The low-rank rows: low[m, :] = scale[a] * sum_r X_r[m] . A_r[a]^T, a = adapter[m],
 // in bf16, and the adapter lists of the token tiles.
@@ -97,11 +105,13 @@ struct CombineParams {
 };
 
 // Token capacities of the routed product's instances.
-constexpr int kRoutedSmall = 64, kRoutedMid = 128, kRoutedWide = 256;
+constexpr int kRoutedSmall = 64, kRoutedMid = 128, kRoutedWide = 256, kRoutedDouble = 512;
 // k-blocks of 64 in one ring stage. A stage costs its barriers' fixed time (about
 // 200 ns), so it should carry many bytes: with one k-block per stage the 256-token
 // tiles are 10 to 20 % slower. The half tiles carry few weight rows, so four.
-constexpr int routed_kblocks(bool half, int tokens) { return half && tokens <= kRoutedMid ? 4 : 2; }
+constexpr int routed_kblocks(bool half, int tokens) {
+  return tokens == kRoutedDouble ? 1 : half && tokens <= kRoutedMid ? 4 : 2;
+}
 
 cudaError_t prepare_routed_kernels();
 cudaError_t prepare_lowrank_kernels();

@@ -39,7 +39,7 @@ size_t partial_bytes(const gemm_shard_plan* P) {
   // Cut tiles are fewer than the pairs, and each pair's range cuts at most one
   // more: two slots per pair, one half per CTA.
   const size_t pairs = static_cast<size_t>(std::max(1, P->sm_count / 2));
-  return 2 * pairs * 2 * gsr::kRoutedMaxTokens * 128 * sizeof(float);
+  return 2 * pairs * 2 * gsr::kRoutedDouble * 128 * sizeof(float);
 }
 size_t low_bytes(const gemm_shard_plan* P) {
   return round256(static_cast<size_t>(P->max_M) * gsr::kMaxRank * 2);
@@ -107,7 +107,7 @@ void fill_routed(gsr::RoutedParams& p, const gemm_shard_plan* P, int64_t M, int6
   // with small partials, wide ones pay 128 KB of partial per piece and CTA.
   p.max_pieces = tokens == gsr::kRoutedSmall ? 32 : tokens == gsr::kRoutedMid ? 8 : 4;
   p.min_piece = 2;
-  p.whole_from = static_cast<int>(tokens == gsr::kRoutedWide ? cdiv(pairs * 4, 5) : pairs);
+  p.whole_from = static_cast<int>(tokens >= gsr::kRoutedWide ? cdiv(pairs * 4, 5) : pairs);
   // The stream-K arithmetic is 32-bit.
   if (static_cast<double>(pairs) * (pairs + 1) * stages >= 4294967296.0) p.max_pieces = 1;
   p.timeout_ns = P->timeout_ns;
@@ -152,10 +152,19 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
   // The instance by the mean group: the rows of a group are few where the
   // weights are the traffic, and a capacity near them leaves shared memory for a
   // deeper ring. Any instance is right for any sizes.
+  // Large groups: tiles of 512 tokens read the weights half as often from L2, which
+  // bounds the 256-token tiles, but have one accumulator, so nothing hides the
+  // epilogue; a long k makes up for that. Rows that do not start on 128-byte lines
+  // take two lines per 128 bytes of k, so there it pays sooner. Measured at 512 rows
+  // per group, N = 3584 (256 / 512 tokens, us): K = 1024 201 / 221, 1792 299 / 309,
+  // 2688 415 / 410, 3584 546 / 521; K = 520 99 / 111, 1000 150 / 148, 2008 266 / 226.
+  // With gathered rows the copies' latency eats the gain (567 / 622, K = 7168).
   const int64_t mean = cdiv(M, E);
+  const bool long_k = K >= (K % BK ? 1000 : 2560);
   const int tokens = mean <= gsr::kRoutedSmall ? gsr::kRoutedSmall
                      : mean <= gsr::kRoutedMid ? gsr::kRoutedMid
-                                               : gsr::kRoutedWide;
+                     : mean <= gsr::kRoutedWide || !long_k || rows ? gsr::kRoutedWide
+                                                            : gsr::kRoutedDouble;
   const int64_t ctas = 2 * std::min<int64_t>(pairs_of(P), (cdiv(M, tokens) + E) * n_tiles *
                                                               cdiv(K, 2 * stage_k(false, tokens)));
   if (gsr::log_config_enabled())
@@ -178,12 +187,12 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
   p.n_tiles = static_cast<int>(n_tiles);
   p.cta_cols = kind == gsr::kGated ? 64 : 128;
   p.w_rows = 128;
-  p.policy_w = tokens == gsr::kRoutedWide ? gsr::kPolicyNormal : gsr::kPolicyEvictFirst;
-  p.policy_x = tokens == gsr::kRoutedWide ? gsr::kPolicyNormal : gsr::kPolicyEvictLast;
+  p.policy_w = tokens >= gsr::kRoutedWide ? gsr::kPolicyNormal : gsr::kPolicyEvictFirst;
+  p.policy_x = tokens >= gsr::kRoutedWide ? gsr::kPolicyNormal : gsr::kPolicyEvictLast;
   CUresult cr = encode_stack(&p.tmap_w[0], W, E, wide, K, BK, kind == gsr::kGated ? 64 : 128);
   if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding the W descriptor failed (%d)", (int)cr);
   if (!rows)
-    for (int i = 0; i < tokens / 16 && cr == CUDA_SUCCESS; ++i)
+    for (int i = 0; i < std::min(tokens, 256) / 16 && cr == CUDA_SUCCESS; ++i)
       cr = encode_2d(&p.tmap_x[i], X, M, K, 8 * (i + 1));
   if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding the X descriptor failed (%d)", (int)cr);
   DeviceScope scope(P->device);
@@ -381,6 +390,10 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
   p.unit_cols = rank <= 16 ? 16 : rank <= 32 ? 32 : 64;
   p.units_per_adapter = rank <= 64 ? 1 : 2;
   p.rank_pad = p.unit_cols * p.units_per_adapter;
+  p.scale = scale;
+  // A row or a few of low rank: the product computes their low-rank rows itself, and
+  // is the call's only kernel.
+  p.self_rows = M <= gsr::kSelfRows && M * p.rank_pad <= gsr::kSelfElements;
   p.policy_w = m_tiles == 1 ? gsr::kPolicyEvictFirst : gsr::kPolicyNormal;
   p.policy_x = m_tiles == 1 ? gsr::kPolicyEvictLast : gsr::kPolicyNormal;
   gsr::LowRankParams q;
@@ -392,6 +405,9 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
     q.x[r] = static_cast<const uint16_t*>(X_r[r]);
     q.a[r] = static_cast<const uint16_t*>(A_r[r]);
     q.k[r] = K_r[r];
+    p.x_r[r] = q.x[r];
+    p.a_r[r] = q.a[r];
+    p.k_r[r] = static_cast<int>(K_r[r]);
     CUresult cr = encode_2d(&p.tmap_w[r], W_r[r], N, K_r[r], p.w_rows);
     if (cr == CUDA_SUCCESS) cr = encode_2d(&p.tmap_x[r], X_r[r], M, K_r[r], static_cast<int>(width / 2));
     if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding shard %d's descriptors failed (%d)", r, (int)cr);
@@ -413,7 +429,7 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
   DeviceScope scope(P->device);
   if (scope.err != cudaSuccess) return cuda_fail(scope.err, "selecting the plan's device");
   cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = gsr::launch_low_rank(q, st_);
+  cudaError_t e = p.self_rows ? cudaSuccess : gsr::launch_low_rank(q, st_);
   if (e == cudaSuccess) e = gsr::launch_routed(p, gsr::kLora, false, half, tokens, static_cast<int>(ctas), st_);
   if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
   return ok();

@@ -105,6 +105,27 @@ def test_grouped(setup, counts, N, K, gated, gather):
     assert U.untouched(full, M, torch.ones(M, dtype=torch.bool, device=U.DEV))
 
 
+@pytest.mark.parametrize("counts", [[257], [512, 1, 300], [0, 1029], [600, 528, 40]], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("gather", [False, True], ids=["rows", "gathered"])
+def test_grouped_long_k(setup, counts, gated, gather):
+    """Large groups and a long k: tiles of up to 512 tokens."""
+    plan, ws = setup
+    g = U.gen(sum(counts))
+    M, E, N, K = sum(counts), len(counts), 200, 4104
+    T = M // 3 if gather else M
+    X = U.normal(g, T, K)
+    W = U.normal(g, E, 2 * N if gated else N, K, std=K ** -0.5)
+    rows = torch.randint(-1, T, (M,), generator=g, device=U.DEV, dtype=torch.int32) if gather else None
+    full, Y = U.guarded(M, N)
+    call = B.gemm_grouped_gated if gated else B.gemm_grouped
+    call(plan, X, W, U.offsets_of(counts), Y, ws, rows=rows)
+    status_ok(setup)
+    ref, bound = U.grouped_ref(X, W, counts, rows, gated)
+    U.close(Y, ref, bound)
+    assert U.untouched(full, M, torch.ones(M, dtype=torch.bool, device=U.DEV))
+
+
 @pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
 def test_rows_of_no_group_stay(setup, gated):
     """Offsets that start past 0 and end before M: the other rows are not written."""
@@ -232,7 +253,8 @@ def test_combine_into_its_base(setup):
 # ---------------------------------------------------------------- adapters
 
 LORA = [  # M, N, K_r, L, rank, run
-    (1, 264, [8], 1, 8, 1), (1, 1024, [896, 72], 3, 16, 1), (7, 512, [200, 64], 4, 32, 1),
+    (1, 264, [8], 1, 8, 1), (1, 1024, [896, 72], 3, 16, 1), (1, 520, [304] * 16, 2, 24, 1), (2, 264, [136, 8], 3, 16, 1),
+    (3, 200, [64], 2, 16, 1), (7, 512, [200, 64], 4, 32, 1),
     (64, 520, [512], 64, 16, 1), (65, 256, [128] * 4, 5, 64, 1), (128, 1000, [304, 208], 100, 24, 1),
     (129, 264, [256], 7, 128, 1), (256, 512, [136] * 3, 300, 8, 1), (257, 512, [256], 2, 48, 100),
     (600, 776, [512, 200], 40, 96, 1), (1000, 1024, [448] * 2, 3, 64, 300),
@@ -280,6 +302,34 @@ def test_lora_ids_out_of_range_and_nan_of_others(setup):
     bad = (adapter == 2) | (adapter == 4)
     assert not torch.isfinite(Y[bad]).any()
     ref, bound = U.lora_ref([X], [W], [A], Bm, adapter, None)
+    U.close(Y[~bad], ref[~bad], bound[~bad])
+
+
+@pytest.mark.parametrize("M,L,run", [(2, 2, 1), (100, 3, 1), (600, 2, 40)])
+def test_lora_weights_that_are_not_finite(setup, M, L, run):
+    """Infinite and NaN weights of an adapter's B give what its products give, in its
+    rows and their columns, and nothing in other rows of the tile."""
+    plan, ws = setup
+    g = U.gen(14 + M)
+    N, K, rank = 264, 320, 16
+    X, W = U.normal(g, M, K), U.normal(g, N, K, std=K ** -0.5)
+    A, Bm = U.normal(g, L, rank, K, std=K ** -0.5), U.normal(g, L, N, rank, std=rank ** -0.5)
+    Bm[1, 5, 3], Bm[1, 130, 0], Bm[1, 200, 9] = float("inf"), float("-inf"), float("nan")
+    adapter = (torch.arange(M, device=U.DEV) // run % L).to(torch.int32)
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device=U.DEV)
+    B.gemm_ar_lora(plan, [X], [W], [A], Bm, adapter, Y, ws)
+    status_ok(setup)
+    bad = torch.zeros(M, N, dtype=torch.bool, device=U.DEV)
+    for n in (5, 130, 200):
+        bad[adapter == 1, n] = True
+    assert torch.equal(~torch.isfinite(Y), bad)
+    assert torch.isnan(Y[adapter == 1, 200]).all() and torch.isinf(Y[adapter == 1, 5]).all()
+    low = X.double() @ A[1].double().t()
+    sign = torch.where(low[:, 3] > 0, 1.0, -1.0)[adapter == 1]
+    assert torch.equal(torch.sign(Y[adapter == 1, 5].double()), sign)
+    clean = Bm.clone()
+    clean[1, [5, 130, 200]] = 0
+    ref, bound = U.lora_ref([X], [W], [A], clean, adapter, None)
     U.close(Y[~bad], ref[~bad], bound[~bad])
 
 
