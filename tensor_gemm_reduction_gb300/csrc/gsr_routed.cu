@@ -45,9 +45,9 @@ namespace {
 constexpr int kEpi = 128;              // epilogue threads
 constexpr int kPlacers = 4;            // warps that place (or gather) the rows of a stage
 constexpr uint32_t kRolePlacer = 4;
-// kLora: tiles in flight between the placing warps and the epilogue, at most: a
-// ring of single-stage tiles and two accumulators.
-constexpr int kMarks = 8;
+// kLora: more than the tiles in flight between the placing warps and the epilogue (a
+// ring of single-stage tiles and two accumulators).
+constexpr int kMarks = 32;
 
 // Called by the lanes that issue (no election inside).
 __device__ __forceinline__ void copy_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
@@ -65,6 +65,9 @@ __device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap* map, ui
       ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(pol)
       : "memory");
+}
+__device__ __forceinline__ void fetch_descriptor(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 // 16 bytes to shared memory, or 16 zeros; asynchronous.
 __device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool real) {
@@ -149,12 +152,16 @@ struct Cfg {
   static constexpr uint32_t kX = TOK / 2 * 128;         // a k-block of this CTA's tokens
   static constexpr uint32_t kStage = KZ * (kW + kX);
   static constexpr uint32_t kRing = S * kStage;
-  // full[S], empty[S], tmem_full[2], tmem_empty[2], drain; landed[S]: this CTA's
-  // adapter weights (kLora) or gathered rows; granted[S] (kLora): the slot is free
+  // Half tiles lay the ring out by the call's own rows and tokens, so that few of
+  // them leave more stages in flight: kSlots is the most.
+  static constexpr uint32_t kSlots = HALF ? kHalfSlots : S;
+  static_assert(!HALF || kRing >= kHalfRing, "the host counts the stages");
+  // full[kSlots], empty[kSlots], tmem_full[2], tmem_empty[2], drain; landed[kSlots]: this CTA's
+  // adapter weights (kLora) or gathered rows; granted[kSlots] (kLora): the slot is free
   // for an adapter stage; looked (kLora): the tile's adapters are looked over
-  static constexpr uint32_t kBars = (2 * S + 5 + (KIND == kLora ? 2 * S + 1 : GATHER ? S : 0)) * 8;
-  static constexpr uint32_t kLandedOff = (2 * S + 5) * 8, kGrantedOff = kLandedOff + S * 8;
-  static constexpr uint32_t kLookedOff = kGrantedOff + S * 8;
+  static constexpr uint32_t kBars = (2 * kSlots + 5 + (KIND == kLora ? 2 * kSlots + 1 : GATHER ? kSlots : 0)) * 8;
+  static constexpr uint32_t kLandedOff = (2 * kSlots + 5) * 8, kGrantedOff = kLandedOff + kSlots * 8;
+  static constexpr uint32_t kLookedOff = kGrantedOff + kSlots * 8;
   static constexpr uint32_t kGroups = KIND == kLora ? 0 : 4 * (3 * kMaxGroups + 1 + 32);
   static constexpr uint32_t kStaging = 4 * 2048;        // 2 KB per epilogue warp
   static constexpr uint32_t kBarsOff = kRing;
@@ -170,6 +177,21 @@ struct Cfg {
   // MMAs, or one of 512 tokens.
   static constexpr uint32_t kAccs = TOK == 512 ? 1 : 2;
   static constexpr uint32_t kTmemCols = kAccs * TOK;
+};
+
+// The ring's geometry: bytes of a k-block of weights and of tokens, of a stage, of a
+// unit of an adapter stage, and the stages in use.
+template <class C>
+struct Geometry {
+  uint32_t w, x, stage, slots, unit_w, unit_x;
+  __device__ __forceinline__ explicit Geometry(const RoutedParams& p) {
+    w = C::HALF ? 128u * p.w_rows : C::kW;
+    x = C::HALF ? 64u * p.tile_tokens : C::kX;
+    stage = C::KZ * (w + x);
+    slots = C::HALF ? static_cast<uint32_t>(p.stages) : C::S;
+    unit_w = C::KIND == kLora ? w / 64u * p.unit_cols : 0u;
+    unit_x = C::KIND == kLora ? x / 64u * p.unit_cols : 0u;
+  }
 };
 
 // The groups as every CTA counts them (shared memory).
@@ -424,7 +446,8 @@ __device__ __forceinline__ uint64_t unit_desc(uint32_t saddr, int cols) {
 // The MMAs of one adapter stage, by one thread: an election and fresh descriptors
 // per MMA took 75 ns of its issue, three times the tensor cores' own time.
 template <int COLS, class C>
-__device__ __forceinline__ void multiply_units(uint32_t d, uint32_t sw, uint32_t sx, uint32_t idesc, int units) {
+__device__ __forceinline__ void multiply_units(const Geometry<C>& geo, uint32_t d, uint32_t sw, uint32_t sx,
+                                               uint32_t idesc, int units) {
   uint64_t w = unit_desc(sw, COLS), x = unit_desc(sx, COLS);
   for (int u = 0; u < units; ++u) {
 #pragma unroll
@@ -435,8 +458,8 @@ __device__ __forceinline__ void multiply_units(uint32_t d, uint32_t sw, uint32_t
           "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
           "l"(w + 2 * k), "l"(x + 2 * k), "r"(idesc)
           : "memory");
-    w += 2 * C::kRows * COLS / 16;   // addresses are in units of 16 bytes
-    x += C::TOK * COLS / 16;
+    w += geo.unit_w / 16;   // addresses are in units of 16 bytes
+    x += geo.unit_x / 16;
   }
 }
 
@@ -444,9 +467,8 @@ __device__ __forceinline__ void multiply_units(uint32_t d, uint32_t sw, uint32_t
 
 struct Ring {
   uint32_t slot = 0, phase = 0;
-  template <int S>
-  __device__ __forceinline__ void next() {
-    if (++slot == S) {
+  __device__ __forceinline__ void next(uint32_t slots) {
+    if (++slot == slots) {
       slot = 0;
       phase ^= 1u;
     }
@@ -457,7 +479,8 @@ template <class C>
 __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
                         uint32_t rank, const Ctl& ctl) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
-  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::S;
+  const Geometry<C> geo(p);
+  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::kSlots;
   const uint32_t lead0 = map_shared_to_rank(full0, 0);
   const uint64_t pol_w = make_l2_policy(p.policy_w), pol_x = make_l2_policy(p.policy_x);
   int begins = 0;
@@ -488,7 +511,7 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t lead = lead0 + 8 * ring.slot;
-      const uint32_t sw = base + ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
+      const uint32_t sw = base + ring.slot * geo.stage, sx = sw + C::KZ * geo.w;
       if constexpr (C::KIND == kLora) {
         while (shard_end <= st) {
           shard_begin = shard_end;
@@ -501,37 +524,44 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
           arm(full0 + 8 * ring.slot, bytes);
           if constexpr (C::KIND == kLora) sign_many(full0 + 8 * ring.slot, 2 * kPlacers);   // nothing to place
         }
+        // A box of all the stage's k-blocks, where no shard ends inside one.
+        const bool whole = C::HALF && p.whole_boxes;
+        if (whole) {
+          copy_3d(sw, &p.tmap_w[shard], lead, 0, w_row, kx / BK, pol_w);
+          copy_3d(sx, &p.tmap_x[shard], lead, 0, x_row, kx / BK, pol_x);
+        }
 #pragma unroll
         for (int j = 0; j < C::KZ; ++j) {
-          const uint32_t dw = sw + j * C::kW;
+          if (whole) break;
+          const uint32_t dw = sw + j * geo.w;
           if constexpr (C::KIND == kLora) {
             copy_2d(dw, &p.tmap_w[shard], lead, kx + j * BK, w_row, pol_w);
-            copy_2d(sx + j * C::kX, &p.tmap_x[shard], lead, kx + j * BK, x_row, pol_x);
+            copy_2d(sx + j * geo.x, &p.tmap_x[shard], lead, kx + j * BK, x_row, pol_x);
           } else {
             copy_3d(dw, &p.tmap_w[0], lead, kx + j * BK, w_row, t.group, pol_w);
             if constexpr (C::KIND == kGated)
-              copy_3d(dw + C::kW / 2, &p.tmap_w[0], lead, kx + j * BK, p.N + w_row, t.group, pol_w);
+              copy_3d(dw + geo.w / 2, &p.tmap_w[0], lead, kx + j * BK, p.N + w_row, t.group, pol_w);
             // The map whose boxes are exactly this tile's rows.
             if constexpr (!C::GATHER && C::TOK <= 256)
-              copy_2d(sx + j * C::kX, &p.tmap_x[half / 8 - 1], lead, kx + j * BK, x_row, pol_x);
+              copy_2d(sx + j * geo.x, &p.tmap_x[half / 8 - 1], lead, kx + j * BK, x_row, pol_x);
             if constexpr (!C::GATHER && C::TOK > 256) {
               const Halves q(t.n);
-              copy_2d(sx + j * C::kX, &p.tmap_x[q.h[0] / 8 - 1], lead, kx + j * BK,
+              copy_2d(sx + j * geo.x, &p.tmap_x[q.h[0] / 8 - 1], lead, kx + j * BK,
                       t.row0 + static_cast<int>(rank) * q.h[0], pol_x);
               if (q.h[1])
-                copy_2d(sx + j * C::kX + q.h[0] * 128, &p.tmap_x[q.h[1] / 8 - 1], lead, kx + j * BK,
+                copy_2d(sx + j * geo.x + q.h[0] * 128, &p.tmap_x[q.h[1] / 8 - 1], lead, kx + j * BK,
                         t.row0 + 2 * q.h[0] + static_cast<int>(rank) * q.h[1], pol_x);
             }
           }
         }
       }
       __syncwarp();
-      if (!looked && st - t.st == C::S - 1) {   // place the next tile while the ring is full
+      if (!looked && st - t.st == static_cast<int>(geo.slots) - 1) {   // place the next tile while the ring is full
         have_next = walk.step<C>(p, g, tn);
         looked = true;
       }
       ++issued;
-      ring.next<C::S>();
+      ring.next(geo.slots);
     }
     if constexpr (C::KIND == kLora) {
       if (!ok) break;
@@ -540,7 +570,7 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
         waited = true;
         a.template begin<C>(p, t);
       }
-      const uint32_t unit_w = 2u * C::kRows * p.unit_cols, unit_bytes = 2u * p.w_rows * p.unit_cols;
+      const uint32_t unit_bytes = 2u * p.w_rows * p.unit_cols;
       for (int st = a.st; st < a.st_end; ++st) {
         ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRoleProducer << 8) | 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -558,12 +588,12 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
         for (int u = 0; u < units; ++u) {
           const int id = a.adapter(p, u0 + u);
           if (lane == 0)
-            copy_3d(base + ring.slot * C::kStage + u * unit_w, &p.tmap_b, landed,
+            copy_3d(base + ring.slot * geo.stage + u * geo.unit_w, &p.tmap_b, landed,
                     p.units_per_adapter == 2 ? ((u0 + u) & 1) * p.unit_cols : 0, w_row, id, pol_w);
         }
         __syncwarp();
         ++issued;
-        ring.next<C::S>();
+        ring.next(geo.slots);
       }
     }
     if (!looked) have_next = walk.step<C>(p, g, tn);
@@ -573,12 +603,12 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
   if (!ok) {
     // Let the copies already issued land before the shared memory goes away:
     // they complete on the leader's barriers, whose MMAs free the slots.
-    const uint32_t first = issued > C::S ? issued - C::S : 0;
+    const uint32_t first = issued > geo.slots ? issued - geo.slots : 0;
     for (uint32_t i = first; i < issued; ++i) {
       if (rank == 0)
-        wait_drain(full0 + 8 * (i % C::S), (i / C::S) & 1u, 100000000ull);
+        wait_drain(full0 + 8 * (i % geo.slots), (i / geo.slots) & 1u, 100000000ull);
       else
-        wait_drain(empty0 + 8 * (i % C::S), (i / C::S) & 1u, 100000000ull);
+        wait_drain(empty0 + 8 * (i % geo.slots), (i / geo.slots) & 1u, 100000000ull);
     }
     // Adapter weights complete on barriers that only the placing warps follow.
     if constexpr (C::KIND == kLora) {
@@ -592,8 +622,9 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
 template <class C>
 __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
                          uint32_t tmem, const Ctl& ctl) {
-  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::S;
-  const uint32_t tfull0 = empty0 + 8 * C::S, tempty0 = tfull0 + 16, drain = tempty0 + 16;
+  const Geometry<C> geo(p);
+  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::kSlots;
+  const uint32_t tfull0 = empty0 + 8 * C::kSlots, tempty0 = tfull0 + 16, drain = tempty0 + 16;
   Ring ring;
   uint32_t local = 0;
   bool ok = true, issued = false, waited = C::KIND != kLora;
@@ -620,20 +651,20 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after_sync();
-      const uint32_t sw = base + ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
+      const uint32_t sw = base + ring.slot * geo.stage, sx = sw + C::KZ * geo.w;
 #pragma unroll
       for (int j = 0; j < C::KZ; ++j) {
-        mma4_bf16_pair(d, smem_desc_sw128(sw + j * C::kW), smem_desc_sw128(sx + j * C::kX), idesc,
+        mma4_bf16_pair(d, smem_desc_sw128(sw + j * geo.w), smem_desc_sw128(sx + j * geo.x), idesc,
                        (st > t.st || j > 0) ? 1u : 0u);
         if constexpr (C::TOK > 256)
           if (q.h[1])
-            mma4_bf16_pair(d + 2 * q.h[0], smem_desc_sw128(sw + j * C::kW),
-                           smem_desc_sw128(sx + j * C::kX + q.h[0] * 128), idesc2,
+            mma4_bf16_pair(d + 2 * q.h[0], smem_desc_sw128(sw + j * geo.w),
+                           smem_desc_sw128(sx + j * geo.x + q.h[0] * 128), idesc2,
                            (st > t.st || j > 0) ? 1u : 0u);
       }
       issued = true;
       mma_commit_pair(empty0 + 8 * ring.slot, 0x3);
-      ring.next<C::S>();
+      ring.next(geo.slots);
       if (!looked) {   // place the next tile while this one's first stage runs
         have_next = walk.step<C>(p, g, tn);
         looked = true;
@@ -651,21 +682,21 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after_sync();
-        const uint32_t sw = base + ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
+        const uint32_t sw = base + ring.slot * geo.stage, sx = sw + C::KZ * geo.w;
         const int units = a.units_in(st);
         // The commit below is by the same thread.
         if (elected()) {
           if (p.unit_cols == 16)
-            multiply_units<16, C>(d, sw, sx, idesc, units);
+            multiply_units<16, C>(geo, d, sw, sx, idesc, units);
           else if (p.unit_cols == 32)
-            multiply_units<32, C>(d, sw, sx, idesc, units);
+            multiply_units<32, C>(geo, d, sw, sx, idesc, units);
           else
-            multiply_units<64, C>(d, sw, sx, idesc, units);
+            multiply_units<64, C>(geo, d, sw, sx, idesc, units);
         }
         __syncwarp();
         issued = true;
         mma_commit_pair(empty0 + 8 * ring.slot, 0x3);
-        ring.next<C::S>();
+        ring.next(geo.slots);
       }
     }
     if (!ok) break;
@@ -690,7 +721,8 @@ __device__ void gather_rows(const RoutedParams& p, const Groups& g, int tiles, u
   constexpr int kPasses = (C::TOK / 2 + 15) / 16;   // 16 rows a pass
   const int tid = static_cast<int>(threadIdx.x) - 64 - kEpi;
   const int chunk = tid & 7, row0 = tid >> 3;
-  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::S;
+  const Geometry<C> geo(p);
+  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * C::kSlots;
   const uint32_t dst0 = static_cast<uint32_t>(row0 * 128 + ((chunk ^ (row0 & 7)) << 4));
   const int K = p.K;
   Ring ring;
@@ -728,7 +760,7 @@ __device__ void gather_rows(const RoutedParams& p, const Groups& g, int tiles, u
       ok = wait_bounded(empty0 + 8 * ring.slot, ring.phase ^ 1u, ctl, (kRolePlacer << 8) | 3);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t sx = base + ring.slot * C::kStage + C::KZ * C::kW + dst0;
+      const uint32_t sx = base + ring.slot * geo.stage + C::KZ * geo.w + dst0;
 #pragma unroll
       for (int j = 0; j < C::KZ; ++j) {
         const int k0 = (st * C::KZ + j) * BK;
@@ -736,10 +768,10 @@ __device__ void gather_rows(const RoutedParams& p, const Groups& g, int tiles, u
 #pragma unroll
         for (int i = 0; i < kPasses; ++i)
           if (row0 + 16 * i < rows)
-            copy_16(sx + j * C::kX + i * 2048, src[i] + (in_k ? k0 : 0), in_k && ((real >> i) & 1u));
+            copy_16(sx + j * geo.x + i * 2048, src[i] + (in_k ? k0 : 0), in_k && ((real >> i) & 1u));
       }
       sign_copies(full0 + C::kLandedOff + 8 * ring.slot);
-      ring.next<C::S>();
+      ring.next(geo.slots);
       if (!looked) {
         have_next = walk.step<C>(p, g, tn);
         if (have_next) look(tn, next);
@@ -759,6 +791,7 @@ __device__ void gather_rows(const RoutedParams& p, const Groups& g, int tiles, u
 // stage have landed, they are made visible to the tensor cores' reads.
 template <class C>
 __device__ void sign_rows(const RoutedParams& p, int tiles, uint32_t base, const Ctl& ctl) {
+  const Geometry<C> geo(p);
   const uint32_t full0 = base + C::kBarsOff, landed0 = full0 + C::kLandedOff;
   const uint32_t lead0 = map_shared_to_rank(full0, 0);
   Ring ring;
@@ -775,17 +808,16 @@ __device__ void sign_rows(const RoutedParams& p, int tiles, uint32_t base, const
       sign_pair(lead0 + 8 * ring.slot);
     }
     __syncwarp();
-    ring.next<C::S>();
+    ring.next(geo.slots);
   }
 }
 
 // One adapter stage's rows: this lane's row `v` (COLS columns, the adapter `id`)
 // in the units of that adapter, zeros in the others.
 template <int COLS, class C>
-__device__ __forceinline__ void place_stage(const RoutedParams& p, AdapterSteps& a, uint32_t sx, int st,
+__device__ __forceinline__ void place_stage(const RoutedParams& p, AdapterSteps& a, uint32_t unit_x, uint32_t sx, int st,
                                             int id, int who, int row, int ways, int half,
                                             const uint4 (&v)[kMaxRank / 8]) {
-  constexpr uint32_t kUnitX = C::TOK * COLS;
   constexpr uint32_t kMask = COLS == 64 ? 7 : COLS == 32 ? 3 : 1;
   const int units = a.units_in(st), u0 = st * a.per_stage;
   const uint32_t at_row = static_cast<uint32_t>(row) * COLS * 2;
@@ -794,7 +826,7 @@ __device__ __forceinline__ void place_stage(const RoutedParams& p, AdapterSteps&
     const bool hit = a.adapter(p, u0 + u) == id;
     const bool upper = COLS == 64 && p.units_per_adapter == 2 && ((u0 + u) & 1);   // columns 64..127
     if (row < half) {
-      const uint32_t dst = sx + u * kUnitX;
+      const uint32_t dst = sx + u * unit_x;
 #pragma unroll
       for (int c = 0; c < COLS / 8; ++c) {
         const uint4 w = COLS == 64 && upper ? v[8 + c] : v[c];
@@ -846,7 +878,7 @@ __device__ __forceinline__ bool look_over(const RoutedParams& p, const Tile& t, 
 // adds their products to the rows that have the adapter).
 template <class C>
 __device__ __noinline__ void take_out(const RoutedParams& p, uint32_t sw, int units, int who) {
-  const uint32_t unit = 2u * C::kRows * p.unit_cols, bytes = 2u * p.w_rows * p.unit_cols;
+  const uint32_t unit = Geometry<C>(p).unit_w, bytes = 2u * p.w_rows * p.unit_cols;
   for (int u = 0; u < units; ++u)
     for (uint32_t at = 16u * who; at < bytes; at += 16 * 32 * kPlacers) {
       uint32_t w[4];
@@ -948,9 +980,10 @@ template <int TEAM, class C>
 __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local, Placing& q, int i,
                            uint32_t base, uint32_t rank, volatile int* marks, const Ctl& ctl) {
   const int lane = i & 31;
+  const Geometry<C> geo(p);
   const uint32_t full0 = base + C::kBarsOff;
   const uint32_t lead0 = map_shared_to_rank(full0, 0);
-  q.ring.slot = (q.ring.slot + static_cast<uint32_t>(t.st_end - t.st)) % C::S;
+  q.ring.slot = (q.ring.slot + static_cast<uint32_t>(t.st_end - t.st)) % geo.slots;
   AdapterSteps a{};
   a.template begin<C>(p, t);
   const int half = t.n / 2, ways = half <= 32 ? 4 : half <= 64 ? 2 : 1;
@@ -1001,13 +1034,13 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
       if (!__all_sync(0xffffffffu, ok)) return false;
       // (The producer is few tiles past the epilogue here: kMarks are enough.)
       if (marked && i == 0) marks[local % kMarks] = 1;
-      const uint32_t sw = base + q.ring.slot * C::kStage, sx = sw + C::KZ * C::kW;
+      const uint32_t sw = base + q.ring.slot * geo.stage, sx = sw + C::KZ * geo.w;
       if (p.unit_cols == 16)
-        place_stage<16, C>(p, a, sx, st, id, i, row, ways, half, v);
+        place_stage<16, C>(p, a, geo.unit_x, sx, st, id, i, row, ways, half, v);
       else if (p.unit_cols == 32)
-        place_stage<32, C>(p, a, sx, st, id, i, row, ways, half, v);
+        place_stage<32, C>(p, a, geo.unit_x, sx, st, id, i, row, ways, half, v);
       else
-        place_stage<64, C>(p, a, sx, st, id, i, row, ways, half, v);
+        place_stage<64, C>(p, a, geo.unit_x, sx, st, id, i, row, ways, half, v);
       ok = wait_bounded(full0 + C::kLandedOff + 8 * q.ring.slot, phase, ctl, (kRolePlacer << 8) | 2);
       if (!__all_sync(0xffffffffu, ok)) return false;
       if (marked) take_out<C>(p, sw, a.units_in(st), i);
@@ -1016,7 +1049,7 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
       if (lane == 0) sign_pair(lead0 + 8 * q.ring.slot);
     }
     q.phases ^= 1u << q.ring.slot;
-    q.ring.template next<C::S>();
+    q.ring.next(geo.slots);
   }
   return true;
 }
@@ -1115,7 +1148,7 @@ template <class C>
 __device__ void finish(const RoutedParams& p, const Groups& g, int tiles, uint32_t base,
                        uint8_t* base_ptr, uint32_t tmem, uint32_t rank, volatile int* last_flag,
                        Placing placing, volatile int* marks, const Ctl& ctl) {
-  const uint32_t tfull0 = base + C::kBarsOff + 16 * C::S, tempty0 = tfull0 + 16;
+  const uint32_t tfull0 = base + C::kBarsOff + 16 * C::kSlots, tempty0 = tfull0 + 16;
   const int et = static_cast<int>(threadIdx.x) - 64;
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int quad = (static_cast<int>(threadIdx.x) >> 5) & 3;   // TMEM lanes this warp may read
@@ -1317,26 +1350,31 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_routed_kernel(const __grid
     }
   }
   if (warp == 1) {
-    prefetch_tensormap(&p.tmap_w[0]);
-    if constexpr (!C::GATHER) prefetch_tensormap(&p.tmap_x[0]);
-    if constexpr (C::KIND == kLora) prefetch_tensormap(&p.tmap_b);
+    // Every descriptor that the copies may use, one per lane: each is a memory access
+    // otherwise, where a shard begins or a tile has another width.
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const int maps = C::KIND == kLora ? p.R : min(C::TOK, 256) / 16;
+    if (lane < (C::KIND == kLora ? maps : 1)) fetch_descriptor(&p.tmap_w[lane]);
+    if (!C::GATHER && lane < maps) fetch_descriptor(&p.tmap_x[lane]);
+    if (C::KIND == kLora && lane == 0) fetch_descriptor(&p.tmap_b);
+    __syncwarp();
   }
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::S; ++i) {
+    for (int i = 0; i < static_cast<int>(C::kSlots); ++i) {
       mbar_init(bars + 8 * i, C::kSigns);
-      mbar_init(bars + 8 * (C::S + i), 1);                   // empty: the MMAs' commit
+      mbar_init(bars + 8 * (C::kSlots + i), 1);                   // empty: the MMAs' commit
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + 16 * C::S + 8 * i, 1);                // accumulator full
-      mbar_init(bars + 16 * C::S + 16 + 8 * i, 8);           // empty: the pair's epilogue warps
+      mbar_init(bars + 16 * C::kSlots + 8 * i, 1);                // accumulator full
+      mbar_init(bars + 16 * C::kSlots + 16 + 8 * i, 8);           // empty: the pair's epilogue warps
     }
-    mbar_init(bars + 16 * C::S + 32, 1);
+    mbar_init(bars + 16 * C::kSlots + 32, 1);
     if constexpr (C::KIND == kLora || C::GATHER)
-      for (int i = 0; i < C::S; ++i)
+      for (int i = 0; i < static_cast<int>(C::kSlots); ++i)
         mbar_init(bars + C::kLandedOff + 8 * i, C::GATHER ? 32 * kPlacers : 1);
     if constexpr (C::KIND == kLora)
-      for (int i = 0; i < C::S; ++i) mbar_init(bars + C::kGrantedOff + 8 * i, 1);
+      for (int i = 0; i < static_cast<int>(C::kSlots); ++i) mbar_init(bars + C::kGrantedOff + 8 * i, 1);
     if constexpr (C::KIND == kLora) {
       mbar_init(bars + C::kLookedOff, kPlacers * C::kTeams);
       for (int i = 0; i < kMarks + 3; ++i) marks[i] = 0;

@@ -60,6 +60,9 @@ struct RoutedParams {  // 128-byte aligned through its CUtensorMap members
   int cta_cols, w_rows;             // output columns and weight rows of a CTA's part of a tile
   int stages_per_tile;              // ring stages of a whole tile (the base product)
   int m_tiles, tile_tokens;         // lora: token tiles and their width
+  int stages;                       // lora, half tiles: of the ring
+  int whole_boxes;                  // lora, half tiles: tmap_w and tmap_x are {64, rows, k-blocks}
+                                    // views with boxes of a stage's k-blocks
   int max_pieces, min_piece;        // of a cut tile: pieces at most, stages at least
   int whole_from;                   // remainders of at least this many tiles are not cut
   int unit_cols, units_per_adapter; // lora: columns of one step over an adapter
@@ -112,6 +115,9 @@ constexpr int kRoutedSmall = 64, kRoutedMid = 128, kRoutedWide = 256, kRoutedDou
 constexpr int routed_kblocks(bool half, int tokens) {
   return tokens == kRoutedDouble ? 1 : half && tokens <= kRoutedMid ? 4 : 2;
 }
+
+// The half tiles' ring: bytes, and stages at most.
+constexpr int kHalfRing = 196608, kHalfSlots = 16;
 
 cudaError_t prepare_routed_kernels();
 cudaError_t prepare_lowrank_kernels();
