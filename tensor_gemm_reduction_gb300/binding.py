@@ -190,7 +190,8 @@ def gemm_shard_workspace_size(plan: Plan) -> int:
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        # The raw handle: building a torch.cuda.Stream took 3 us, as long as a launch.
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
     return ctypes.c_void_p(int(stream))

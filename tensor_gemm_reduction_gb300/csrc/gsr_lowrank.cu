@@ -136,7 +136,7 @@ template <int ROWS, int NT>
 struct Stream {
   static constexpr int KSTEP = ROWS == 16 ? 128 : 64, kPitch = 2 * KSTEP, kChunks = KSTEP / 8;
   static constexpr int kLines = ROWS + 8 * NT, kStage = kLines * kPitch;
-  static constexpr int S = ROWS == 16 ? (NT == 8 ? 5 : 6) : 4;
+  static constexpr int S = ROWS == 16 ? (NT == 8 ? 5 : 6) : 3;
   static constexpr int kBytes = S * kStage;
 
   static __device__ __forceinline__ void run(const LowRankParams& p, const Shards& sh, uint32_t ring,
@@ -387,13 +387,18 @@ __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_few_kernel(const _
 }
 
 // Many rows: block x takes 128 rows, 16 per warp, and their adapters one after the
-// other, ascending.
+// other, ascending. A row has one adapter, so the turns' sums share one buffer, and
+// the cluster adds up once (4096 rows, 8 adapters, alone: 43 us adding up every turn,
+// 37 so).
+template <int NT>
+constexpr int many_bytes() { return Stream<128, NT>::kBytes + kWarps * 16 * 8 * NT * 4; }
+
 template <int NT>
 __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __grid_constant__ LowRankParams p) {
-  extern __shared__ float share[];                 // the ring; [kWarps][16][columns of a turn]
-  __shared__ int sums[kWarps], keeps[16 * kWarps], rows[16 * kWarps];
+  extern __shared__ float ring_mem[];              // the ring, then sums [128][8 NT]
+  __shared__ int sums[kWarps], keeps[16 * kWarps], rows[16 * kWarps], at[16 * kWarps];
   __shared__ Shards shards;
-  constexpr int kCols = 8 * NT < kShareCols ? 8 * NT : kShareCols, kTurnTiles = kCols / 8;
+  constexpr int kCols = 8 * NT;
   shards.fill(p);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   let_next_start();
@@ -403,39 +408,47 @@ __global__ void __launch_bounds__(kThreadsLow, 2) gsr_lowrank_kernel(const __gri
   if (static_cast<int>(blockIdx.x) >= blocks) {   // whole clusters: the token tiles' lists
     for (int tile = (static_cast<int>(blockIdx.x) - blocks) * ctas + z; tile < p.m_tiles;
          tile += (static_cast<int>(gridDim.x) - blocks) * ctas) {
-      write_list(p, tile, reinterpret_cast<uint32_t*>(share), sums);
+      write_list(p, tile, reinterpret_cast<uint32_t*>(ring_mem), sums);
       __syncthreads();
     }
     return;
   }
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(share));
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_mem));
+  float* share = ring_mem + Stream<128, NT>::kBytes / 4;
   const int m = static_cast<int>(blockIdx.x) * 16 * kWarps + tid;   // thread i < 128 has row i
   int id = tid < 16 * kWarps && m < p.M ? p.adapter[m] : -1;
   if (id < 0 || id >= p.L) id = -1;
-  for (int last = -1;;) {
-    // The smallest adapter above the last one.
-    const int mine = id > last ? id : INT32_MAX;
-    const int least = __reduce_min_sync(0xffffffffu, mine);
-    __syncthreads();   // the last turn's reads
-    if (lane == 0) sums[warp] = least;
-    __syncthreads();
-    int a = INT32_MAX;
-    for (int i = 0; i < kWarps; ++i) a = min(a, sums[i]);
-    if (a == INT32_MAX) break;
-    last = a;
-    if (tid < 16 * kWarps) {
-      rows[tid] = id == a ? m : -1;   // the others are not read (zeros)
-      keeps[tid] = a;
-    }
-    for (int pass = 0; pass < p.rank_pad; pass += 8 * NT) {
+  if (tid < 16 * kWarps) {
+    at[tid] = id >= 0 ? m : -1;
+    keeps[tid] = id;
+  }
+  for (int pass = 0; pass < p.rank_pad; pass += kCols) {
+    for (int last = -1;;) {
+      // The smallest adapter above the last one.
+      const int mine = id > last ? id : INT32_MAX;
+      const int least = __reduce_min_sync(0xffffffffu, mine);
+      __syncthreads();   // the last turn's reads
+      if (lane == 0) sums[warp] = least;
+      __syncthreads();
+      int a = INT32_MAX;
+      for (int i = 0; i < kWarps; ++i) a = min(a, sums[i]);
+      if (a == INT32_MAX) break;
+      last = a;
+      if (tid < 16 * kWarps) rows[tid] = id == a ? m : -1;   // the others are not read (zeros)
       float acc[NT][4] = {};
       Stream<128, NT>::run(p, shards, ring, rows, a, pass, z, ctas, acc);
+      // Only the adapter's own rows: zeros times an infinite weight are NaN.
+      const int group = lane >> 2, quad = lane & 3, r0 = 16 * warp + group;
 #pragma unroll
-      for (int n0 = 0; n0 < NT; n0 += kTurnTiles) {
-        put_share<kTurnTiles>(share, acc + n0, kCols);
-        write_rows<kCols, 1>(p, share, rows, keeps, pass + 8 * n0, z, ctas);
-      }
+      for (int h = 0; h < 2; ++h)
+        if (rows[r0 + 8 * h] >= 0) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<float2*>(share + (r0 + 8 * h) * kCols + 8 * n + 2 * quad) =
+                make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+        }
     }
+    write_rows<kCols, 1>(p, share, at, keeps, pass, z, ctas);
   }
 }
 
@@ -474,7 +487,7 @@ cudaError_t launch_nt(const LowRankParams& p, cudaStream_t stream) {
   const int blocks = (p.M + 16 * kWarps - 1) / (16 * kWarps);
   const int list_blocks = (std::min(p.m_tiles, 16) + kMaxCluster - 1) / kMaxCluster;
   return launch_clusters(gsr_lowrank_kernel<NT>, p, dim3(blocks + list_blocks, 1, kMaxCluster),
-                         Stream<128, NT>::kBytes, stream);
+                         many_bytes<NT>(), stream);
 }
 
 }  // namespace
@@ -485,7 +498,7 @@ cudaError_t set_limits() {
                                        Stream<16, NT>::kBytes);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(gsr_lowrank_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Stream<128, NT>::kBytes);
+                              many_bytes<NT>());
 }
 
 cudaError_t prepare_lowrank_kernels() {

@@ -88,8 +88,27 @@ __global__ void __launch_bounds__(kRouteThreads, 1) gsr_route_kernel(const Route
   int* mine = counts + warp * p.E;
   int held[kHeld];   // the entry's id, then also its place among the warp's: id << 16 | place
   if constexpr (HELD) {
+    // All loads at once: a branch on the ids' width between them would have each
+    // wait for the one before.
+    if (p.wide) {
+      long long v[kHeld];
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) held[j] = load_id(p, i0 + 32 * j + lane < i1 ? i0 + 32 * j + lane : p.n);
+      for (int j = 0; j < kHeld; ++j) {
+        const int i = i0 + 32 * j + lane;
+        v[j] = i < i1 ? __ldg(reinterpret_cast<const long long*>(p.ids) + i) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) held[j] = v[j] >= 0 && v[j] < p.E ? static_cast<int>(v[j]) : -1;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) {
+        const int i = i0 + 32 * j + lane;
+        held[j] = i < i1 ? __ldg(reinterpret_cast<const int*>(p.ids) + i) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j)
+        if (held[j] < 0 || held[j] >= p.E) held[j] = -1;
+    }
   }
   for (int e = lane; e < p.E; e += 32) mine[e] = 0;
   __syncwarp();
@@ -203,7 +222,8 @@ __global__ void __launch_bounds__(kRouteThreads, 1) gsr_route_kernel(const Route
     __syncthreads();
     for (int j = tid; j < local_kept; j += threads) {
       const int id = ordered[j] >> 16;
-      p.source[base[id] + j - begin[id]] = (first + (ordered[j] & 0xffff)) / p.topk;
+      const uint32_t i = static_cast<uint32_t>(first + (ordered[j] & 0xffff));
+      p.source[base[id] + j - begin[id]] = static_cast<int>(p.topk == 1 ? i : __umulhi(i, p.topk_magic));
     }
   } else {
     for (int i = i0; i < i1; i += 32) {
@@ -338,6 +358,9 @@ cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(threads / 32) * p.E * sizeof(int) +
                       (held ? static_cast<size_t>(threads) * kHeld * sizeof(int) : 0);
   RouteParams q = p;
+  // i / topk = (i * magic) >> 32 while i * (magic * topk - 2^32) < 2^32, that is for i <
+  // 2^25: held entries are at most 2^18.
+  q.topk_magic = static_cast<uint32_t>(((1ull << 32) + p.topk - 1) / p.topk);
   void* args[] = {&q};
   return launch_pdl(held ? reinterpret_cast<const void*>(gsr_route_kernel<true>)
                          : reinterpret_cast<const void*>(gsr_route_kernel<false>),

@@ -95,6 +95,7 @@ struct RouteParams {
   int32_t* source;
   int32_t* position;
   int n, topk, E, wide;             // wide: 64-bit ids
+  uint32_t topk_magic;              // set by the launcher
 };
 
 struct CombineParams {

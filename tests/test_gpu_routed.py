@@ -393,6 +393,41 @@ def test_calls_on_another_stream_and_in_a_graph(setup):
     assert torch.equal(Y, first.flip(0))
 
 
+def test_two_streams_at_once(setup):
+    """Calls of two streams, each with a workspace of its own, in flight together."""
+    plan, _ = setup
+    g = U.gen(15)
+    jobs = []
+    for i, (M, N, K, L, rank) in enumerate([(128, 1024, 1024, 20, 32), (700, 520, 512, 3, 16)]):
+        ws = B.gemm_routed_workspace_alloc(plan)
+        B.gemm_routed_workspace_init(plan, ws)
+        X, W = U.normal(g, M, K), U.normal(g, N, K, std=K ** -0.5)
+        A, Bm = U.normal(g, L, rank, K, std=K ** -0.5), U.normal(g, L, N, rank, std=rank ** -0.5)
+        a = adapters(g, M, L, 1, 0.1)
+        We = U.normal(g, 4, N, K, std=K ** -0.5)
+        off = U.offsets_of([M // 2, 0, M // 3, M - M // 2 - M // 3])
+        Y, Z = (torch.empty(M, N, dtype=torch.bfloat16, device=U.DEV) for _ in range(2))
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        calls = [B.prepare_ar_lora(plan, [X], [W], [A], Bm, a, Y, ws, stream=stream),
+                 B.prepare_grouped(plan, X, We, off, Z, ws, stream=stream)]
+        jobs.append((calls, Y, Z, stream, ws))
+    alone = []
+    for calls, Y, Z, stream, ws in jobs:
+        for c in calls:
+            c()
+        torch.cuda.synchronize()
+        alone.append((Y.clone(), Z.clone()))
+    for _ in range(20):
+        for k in range(2):
+            for calls, *_ in jobs:
+                calls[k]()
+    torch.cuda.synchronize()
+    for (calls, Y, Z, stream, ws), (y, z) in zip(jobs, alone):
+        B.gemm_shard_check_status(plan, ws)
+        assert torch.equal(Y, y) and torch.equal(Z, z)
+
+
 @pytest.mark.parametrize("tokens,graph", [(1, False), (33, False), (300, True)])
 def test_the_example_runs_them_together(tokens, graph):
     import importlib.util
