@@ -398,7 +398,8 @@ gsr_status gemm_shard_pack_gather(const gemm_shard_plan *plan, int R, const int6
  *     gemm_routed_workspace_init and left ready for the next call by every
  *     call. gemm_shard_check_status reads its status word. gemm_group_route and
  *     gemm_group_combine need none.
- *   - Options: GSR_OPT_TIMEOUT_NS and GSR_OPT_MAX_CTAS apply; the others do not.
+ *   - Options: GSR_OPT_TIMEOUT_NS and GSR_OPT_MAX_CTAS apply to the products; the
+ *     others do not.
  *   - Results are reproducible: sums run in an order that depends on the shapes
  *     and the group sizes alone.
  *   - Graphs: the calls may be recorded in a CUDA graph; a replay reads the
@@ -432,7 +433,8 @@ gsr_status gemm_routed_workspace_init(const gemm_shard_plan *plan, void *ws, siz
  *   position  device out, T x topk int32: the sorted row of each entry, -1 for a
  *             dropped one
  * Within a group rows keep the entries' order. T * topk may not exceed the
- * plan's max_M. T == 0 writes offsets (zeros) alone.
+ * plan's max_M. The outputs overlap neither one another nor ids (position is
+ * scratch meanwhile). T == 0 writes offsets (zeros) alone.
  */
 gsr_status gemm_group_route(const gemm_shard_plan *plan, int64_t T, int topk, int E,
                             const void *ids, int id_bytes, int32_t *offsets, int32_t *source,

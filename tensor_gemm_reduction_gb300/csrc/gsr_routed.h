@@ -95,7 +95,10 @@ struct RouteParams {
   int32_t* source;
   int32_t* position;
   int n, topk, E, wide;             // wide: 64-bit ids
-  uint32_t topk_magic;              // set by the launcher
+  // Set by the launcher. The entries in parts, one per CTA: of units + 1 times 32 entries
+  // the first `longer`, of units times 32 the others (the last may be short of 32).
+  int parts, units, longer;
+  uint32_t topk_magic;              // 0: divide
 };
 
 struct CombineParams {

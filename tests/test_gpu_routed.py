@@ -75,6 +75,64 @@ def test_route_of_many_entries(T, topk, E):
     assert torch.equal(position.reshape(-1).long(), back)
 
 
+def route_by_sorting(ids, E):
+    """The route's outputs by a stable sort, ids out of range dropped."""
+    flat = ids.reshape(-1).long()
+    live = (flat >= 0) & (flat < E)
+    order = torch.argsort(torch.where(live, flat, E), stable=True)
+    kept = int(live.sum())
+    offsets = torch.zeros(E + 1, dtype=torch.int64, device=ids.device)
+    offsets[1:] = torch.bincount(flat[live], minlength=E).cumsum(0)
+    source, position = torch.full_like(flat, -1), torch.full_like(flat, -1)
+    source[:kept] = order[:kept] // ids.shape[1]
+    position[order[:kept]] = torch.arange(kept, device=ids.device)
+    return offsets, source, position.reshape(ids.shape)
+
+
+@pytest.mark.parametrize("T,topk", [(2048, 1), (683, 3), (8191, 6), (8193, 6), (65551, 1), (103, 128),
+                                    (1000001, 5), (1 << 25, 1), ((1 << 25) // 3 + 7, 3)])
+@pytest.mark.parametrize("E,one", [(1, False), (9, False), (1024, False), (1000, True)])
+def test_route_from_few_entries_to_very_many(T, topk, E, one):
+    """Numbers of entries around the changes of form, parts that end unevenly, a group of
+    everything, and entries past 2^25."""
+    plan = B.gemm_shard_plan_create(0, T * topk, 64, 64, 1)
+    ids = torch.randint(-1, E + 1, (T, topk), generator=U.gen(E), device=U.DEV, dtype=torch.int32)
+    if one:
+        ids.fill_(E - 1)
+    i32 = dict(dtype=torch.int32, device=U.DEV)
+    have = torch.full((E + 1,), 7, **i32), torch.full((T * topk,), 7, **i32), torch.full((T, topk), 7, **i32)
+    B.gemm_group_route(plan, ids, E, *have)
+    for a, b, name in zip(have, route_by_sorting(ids, E), ("offsets", "source", "position")):
+        assert torch.equal(a.long(), b), name
+
+
+def test_routes_of_many_entries_follow_one_another(setup):
+    """Calls in a row, recorded in a graph, whose ids change between replays."""
+    T, topk, E = 9001, 7, 200
+    plan = B.gemm_shard_plan_create(0, T * topk, 64, 64, 1)
+    i32 = dict(dtype=torch.int32, device=U.DEV)
+    ids = [torch.zeros(T, topk, **i32) for _ in range(3)]
+    outs = [(torch.empty(E + 1, **i32), torch.empty(T * topk, **i32), torch.empty(T, topk, **i32)) for _ in ids]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        B.gemm_group_route(plan, ids[0], E, *outs[0])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ids[1].copy_(ids[0] + 1)
+        for x, out in zip(ids, outs):
+            B.gemm_group_route(plan, x, E, *out)
+        ids[2].copy_(ids[1] * 2)      # read by the next replay
+    for k in range(4):
+        ids[0].copy_(torch.randint(-1, E, (T, topk), generator=U.gen(k), device=U.DEV, dtype=torch.int32))
+        read = [ids[0].clone(), ids[0] + 1, ids[2].clone()]
+        graph.replay()
+        for x, out in zip(read, outs):
+            for a, b in zip(out, route_by_sorting(x, E)):
+                assert torch.equal(a.long(), b)
+
+
 # ---------------------------------------------------------------- grouped
 
 GROUPS = [
