@@ -166,7 +166,12 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
 
   // The instance by the mean group: the rows of a group are few where the
   // weights are the traffic, and a capacity near them leaves shared memory for a
-  // deeper ring. Any instance is right for any sizes.
+  // deeper ring; but groups differ in size, and one larger than the capacity reads its
+  // weights again. Any instance is right for any sizes. Measured with 64 groups of
+  // uneven sizes (64 / 128 / 256 tokens, us): grouped N = 7168, K = 896, mean 16 132 / 131
+  // / 134, 32 141 / 135 / 137, 64 163 / 145 / 147, 96 181 / 162 / 154, 128 225 / 181 / 166;
+  // gated N = 896, K = 7168, gathered, 16 240 / 244 / 256, 32 243 / 246 / 260, 64 262 / 255
+  // / 267, 96 312 / 274 / 280, 128 336 / 284 / 290, 192 418 / 343 / 312.
   // Large groups: tiles of 512 tokens read the weights half as often from L2, which
   // bounds the 256-token tiles, but have one accumulator, so nothing hides the
   // epilogue; a long k makes up for that. Rows that do not start on 128-byte lines
@@ -176,8 +181,8 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
   // With gathered rows the copies' latency eats the gain (567 / 622, K = 7168).
   const int64_t mean = cdiv(M, E);
   const bool long_k = K >= (K % BK ? 1000 : 2560);
-  const int tokens = mean <= gsr::kRoutedSmall ? gsr::kRoutedSmall
-                     : mean <= gsr::kRoutedMid ? gsr::kRoutedMid
+  const int tokens = mean <= 24   ? gsr::kRoutedSmall
+                     : mean <= 96 ? gsr::kRoutedMid
                      : mean <= gsr::kRoutedWide || !long_k || rows ? gsr::kRoutedWide
                                                             : gsr::kRoutedDouble;
   const int64_t ctas = 2 * std::min<int64_t>(pairs_of(P), (cdiv(M, tokens) + E) * n_tiles *
