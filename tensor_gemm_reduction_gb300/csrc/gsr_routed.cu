@@ -13,10 +13,13 @@
 // tile. A group's tokens are cut into tiles of equal width.
 //
 // Every CTA counts the tiles itself from the offsets (a scan over the groups in
-// shared memory). Whole waves of tiles are dealt round-robin; the k-range of
-// the remaining ones is cut into equal contiguous ranges (stream-K), walked
-// first, whose fp32 partials the last piece to arrive sums in k order. The
-// cuts depend on the group sizes alone, so results are reproducible.
+// shared memory). Whole waves of tiles are dealt round-robin. The remaining ones are
+// walked first; where their number leaves pairs idle and k is long, each is cut
+// along k into equal pieces, one per pair, whose fp32 partials the last piece to
+// arrive sums in k order. The cuts depend on the group sizes alone, so results are
+// reproducible. (Cutting the remaining k evenly over all pairs, most of which then
+// hold pieces of two tiles, was slower in every case measured: 36 tiles of 256 rows
+// x 256 tokens, K = 7168, 49 us whole tiles 44; 24 tiles 41, in threes 38.)
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (the pair's leader), warps 2..5
 // epilogue. With gathered rows, warps 6..9 copy them and warp 10 signs them.
@@ -266,61 +269,46 @@ struct Halves {
   }
 };
 
-// Every role walks the same tiles: this worker's range of the cut tiles, then
-// its whole tiles.
+constexpr int kMinPiece = 2;   // stages of a piece, at least
+
+// Every role walks the same tiles: this worker's piece of a cut tile, or a whole
+// one, of the remainder, then its other tiles.
 struct Walk {
-  int w, G, Gc, next, whole, S;
-  uint32_t it, it_end, iters;
+  int G, next, whole, S;
+  int cut, piece, pieces;   // of the remainder: tile (-1: none, or done), piece of it
 
   __device__ __forceinline__ void begin(const RoutedParams& p, int tiles) {
-    w = static_cast<int>(blockIdx.x) >> 1;
+    const int w = static_cast<int>(blockIdx.x) >> 1;
     G = static_cast<int>(gridDim.x) >> 1;
     S = p.stages_per_tile;
     const int rem = tiles % G;
     whole = tiles - rem;
     next = w;
-    Gc = rem;
-    if (rem > 0 && rem < p.whole_from && p.max_pieces > 1) {
-      const int most = static_cast<int>(min(static_cast<long long>(rem) * p.max_pieces,
-                                            static_cast<long long>(rem) * S / p.min_piece));
-      Gc = max(rem, min(G, most));
+    pieces = 1;
+    if (rem > 0) {
+      const int n = min(min(G / rem, p.max_pieces), S / kMinPiece);
+      if (n > 1 && S - S / n > (whole ? p.cut_ahead : p.cut_alone)) pieces = n;
     }
-    iters = static_cast<uint32_t>(rem) * static_cast<uint32_t>(S);
-    it = it_end = 0;
-    if (w < Gc) {
-      if (Gc == rem) {
-        it = static_cast<uint32_t>(w) * S;
-        it_end = it + S;
-      } else {
-        it = static_cast<uint32_t>(w) * iters / Gc;
-        it_end = static_cast<uint32_t>(w + 1) * iters / Gc;
-      }
-    }
+    cut = w < rem * pieces ? w / pieces : -1;
+    piece = w % pieces;
   }
-  __device__ __forceinline__ int worker_of(uint32_t i) const {
-    return static_cast<int>(((i + 1) * Gc + iters - 1) / iters) - 1;
+  // First stage of a piece.
+  __device__ __forceinline__ int bound(int i) const {
+    return static_cast<int>(static_cast<long long>(i) * S / pieces);
   }
 
   template <class C>
   __device__ __forceinline__ bool step(const RoutedParams& p, const Groups& g, Tile& t) {
     int id;
-    if (it < it_end) {
-      const uint32_t cut = it / S, lo = it - cut * S;
-      const uint32_t hi = min(static_cast<uint32_t>(S), lo + (it_end - it));
-      it += hi - lo;
-      id = whole + static_cast<int>(cut);
-      t.cut = static_cast<int>(cut);
-      t.st = static_cast<int>(lo);
-      t.st_end = static_cast<int>(hi);
-      t.piece = 0;
-      t.npieces = 1;
-      t.slot = 0;
-      if (Gc > static_cast<int>(iters / S)) {
-        const int first = worker_of(cut * S), last = worker_of((cut + 1) * S - 1);
-        t.piece = w - first;
-        t.npieces = last - first + 1;
-        t.slot = t.cut + first;   // tile + worker numbers the pieces without collision
-      }
+    if (cut >= 0) {
+      id = whole + cut;
+      t.cut = cut;
+      t.st = bound(piece);
+      t.st_end = bound(piece + 1);
+      t.piece = piece;
+      t.npieces = pieces;
+      t.slot = cut * pieces;
+      cut = -1;
     } else {
       if (next >= whole) return false;
       id = next;
@@ -797,7 +785,7 @@ __device__ void sign_rows(const RoutedParams& p, int tiles, uint32_t base, const
   Ring ring;
   Walk walk;
   walk.begin(p, tiles);
-  uint32_t stages = walk.it_end - walk.it;
+  uint32_t stages = walk.cut >= 0 ? walk.bound(walk.piece + 1) - walk.bound(walk.piece) : 0;
   for (int id = walk.next; id < walk.whole; id += walk.G) stages += walk.S;
   for (; stages > 0; --stages) {
     bool ok = wait_bounded(landed0 + 8 * ring.slot, ring.phase, ctl, (kRolePlacer << 8) | 4);

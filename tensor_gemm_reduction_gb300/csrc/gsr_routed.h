@@ -63,8 +63,10 @@ struct RoutedParams {  // 128-byte aligned through its CUtensorMap members
   int stages;                       // lora, half tiles: of the ring
   int whole_boxes;                  // lora, half tiles: tmap_w and tmap_x are {64, rows, k-blocks}
                                     // views with boxes of a stage's k-blocks
-  int max_pieces, min_piece;        // of a cut tile: pieces at most, stages at least
-  int whole_from;                   // remainders of at least this many tiles are not cut
+  int max_pieces;                   // of a cut tile
+  // Remaining tiles are cut when a piece is shorter than the tile by more stages than
+  // this: when no whole tiles follow, and when they do and hide the sum.
+  int cut_alone, cut_ahead;
   int unit_cols, units_per_adapter; // lora: columns of one step over an adapter
   int rank_pad;                     // lora: unit_cols * units_per_adapter
   int policy_w, policy_x;

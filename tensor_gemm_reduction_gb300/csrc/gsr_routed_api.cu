@@ -36,10 +36,9 @@ int64_t pairs_of(const gemm_shard_plan* P) {
 
 // Workspace regions after the header and the counters.
 size_t partial_bytes(const gemm_shard_plan* P) {
-  // Cut tiles are fewer than the pairs, and each pair's range cuts at most one
-  // more: two slots per pair, one half per CTA.
+  // A pair has one piece at most: a slot per pair, one half per CTA.
   const size_t pairs = static_cast<size_t>(std::max(1, P->sm_count / 2));
-  return 2 * pairs * 2 * gsr::kRoutedDouble * 128 * sizeof(float);
+  return pairs * 2 * gsr::kRoutedDouble * 128 * sizeof(float);
 }
 size_t low_bytes(const gemm_shard_plan* P) {
   return round256(static_cast<size_t>(P->max_M) * gsr::kMaxRank * 2);
@@ -111,20 +110,23 @@ CUresult encode_stack(CUtensorMap* m, const void* ptr, int64_t count, int64_t ro
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// Fields that every kind shares. `tokens`: the instance's capacity.
+// Fields that every kind shares. `tokens`: the instance's capacity, `kblocks`: of a stage.
 void fill_routed(gsr::RoutedParams& p, const gemm_shard_plan* P, int64_t M, int64_t N, int stages,
-                 int tokens, void* ws) {
+                 int kblocks, int tokens, void* ws) {
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.stages_per_tile = stages;
-  const int64_t pairs = pairs_of(P);
   // How finely a remainder of tiles is cut: narrow tiles are streams of weights
   // with small partials, wide ones pay 128 KB of partial per piece and CTA.
+  // Cutting costs the partials' way through L2 and the last arrival's sum. Measured
+  // in whole tiles / cut ones (us, K = 7168): 8 tiles of 64 tokens 21.9 / 16.9 in 9
+  // pieces, 24 23.5 / 23.4 in 3, 36 27.7 / 28.9 in 2; of 256 tokens, 16 41.3 / 32.5, 36
+  // 44.1 / 43.0; after one more wave, 36 of 64 tokens 67.4 / 66.0, of 256 91.1 / 83.6.
+  // K = 2048: 16 tiles of 256 tokens 17.3 / 23.3, 12 of 64 tokens after a wave 22.9 /
+  // 23.4. So a cut has to save some 60 k-blocks (narrow) or 52, or 40 after a wave.
   p.max_pieces = tokens == gsr::kRoutedSmall ? 32 : tokens == gsr::kRoutedMid ? 8 : 4;
-  p.min_piece = 2;
-  p.whole_from = static_cast<int>(tokens >= gsr::kRoutedWide ? cdiv(pairs * 4, 5) : pairs);
-  // The stream-K arithmetic is 32-bit.
-  if (static_cast<double>(pairs) * (pairs + 1) * stages >= 4294967296.0) p.max_pieces = 1;
+  p.cut_alone = (tokens <= gsr::kRoutedMid ? 60 : 52) / kblocks;
+  p.cut_ahead = 40 / kblocks;
   p.timeout_ns = P->timeout_ns;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.status = reinterpret_cast<uint32_t*>(w);
@@ -196,7 +198,8 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
 
   gsr::RoutedParams p;
   std::memset(&p, 0, sizeof p);
-  fill_routed(p, P, M, N, static_cast<int>(cdiv(K, stage_k(false, tokens))), tokens, ws);
+  fill_routed(p, P, M, N, static_cast<int>(cdiv(K, stage_k(false, tokens))),
+              gsr::routed_kblocks(false, tokens), tokens, ws);
   p.E = E;
   p.T = static_cast<int>(T);
   p.K = static_cast<int>(K);
@@ -393,7 +396,7 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
 
   gsr::RoutedParams p;
   std::memset(&p, 0, sizeof p);
-  fill_routed(p, P, M, N, static_cast<int>(stages), tokens, ws);
+  fill_routed(p, P, M, N, static_cast<int>(stages), gsr::routed_kblocks(half, tokens), tokens, ws);
   p.R = R;
   p.L = L;
   p.adapter = adapter;
@@ -405,7 +408,6 @@ gsr_status gemm_ar_lora(const gemm_shard_plan* P, int64_t M, int64_t N, int R, c
   p.n_tiles = static_cast<int>(n_tiles);
   p.cta_cols = p.w_rows = static_cast<int>(tile_rows / 2);
   if (half) {
-    p.whole_from = static_cast<int>(cdiv(3 * pairs_of(P), 5));
     const int64_t stage = kStageK / BK * (128 * p.w_rows + 64 * width);
     p.stages = static_cast<int>(std::min<int64_t>(gsr::kHalfSlots, gsr::kHalfRing / stage));
   }
