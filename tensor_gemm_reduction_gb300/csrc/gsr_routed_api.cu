@@ -170,23 +170,23 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
   // weights are the traffic, and a capacity near them leaves shared memory for a
   // deeper ring; but groups differ in size, and one larger than the capacity reads its
   // weights again. Any instance is right for any sizes. Measured with 64 groups of
-  // uneven sizes (64 / 128 / 256 tokens, us): grouped N = 7168, K = 896, mean 16 132 / 131
-  // / 134, 32 141 / 135 / 137, 64 163 / 145 / 147, 96 181 / 162 / 154, 128 225 / 181 / 166;
-  // gated N = 896, K = 7168, gathered, 16 240 / 244 / 256, 32 243 / 246 / 260, 64 262 / 255
-  // / 267, 96 312 / 274 / 280, 128 336 / 284 / 290, 192 418 / 343 / 312.
-  // Large groups: tiles of 512 tokens read the weights half as often from L2, which
-  // bounds the 256-token tiles, but have one accumulator, so nothing hides the
-  // epilogue; a long k makes up for that. Rows that do not start on 128-byte lines
-  // take two lines per 128 bytes of k, so there it pays sooner. Measured at 512 rows
-  // per group, N = 3584 (256 / 512 tokens, us): K = 1024 201 / 221, 1792 299 / 309,
-  // 2688 415 / 410, 3584 546 / 521; K = 520 99 / 111, 1000 150 / 148, 2008 266 / 226.
+  // uneven sizes (64 / 128 / 256 tokens, us): grouped N = 7168, K = 896, mean 16 128 / 126
+  // / 130, 32 133 / 130 / 132, 64 146 / 137 / 137, 96 168 / 149 / 143, 128 192 / 159 / 150;
+  // gated N = 896, K = 7168, gathered, 16 239 / 243 / 256, 32 243 / 245 / 259, 64 258 / 255
+  // / 267, 96 302 / 270 / 280, 128 334 / 285 / 293.
+  // Large groups: tiles of 512 tokens read the weights half as often from L2, but have
+  // one accumulator, so nothing hides the epilogue, and fewer sizes between them. Rows
+  // that do not start on 128-byte lines take two lines per 128 bytes of k: L2 then
+  // bounds the product and the larger tiles pay. Measured with 16 groups or fewer, N =
+  // 4096 (256 / 512 tokens, us), 384 rows per group: K = 264 34 / 33, 520 47 / 43, 1000 71 /
+  // 62, but 1024 49 / 55, 4096 152 / 151; 2048 rows: 264 129 / 113, 520 186 / 148, 1000
+  // 290 / 230, but 1024 168 / 205, 2048 159 / 175, 4096 154 / 159, 7168 146 / 132.
   // With gathered rows the copies' latency eats the gain (567 / 622, K = 7168).
   const int64_t mean = cdiv(M, E);
-  const bool long_k = K >= (K % BK ? 1000 : 2560);
   const int tokens = mean <= 24   ? gsr::kRoutedSmall
                      : mean <= 96 ? gsr::kRoutedMid
-                     : mean <= gsr::kRoutedWide || !long_k || rows ? gsr::kRoutedWide
-                                                            : gsr::kRoutedDouble;
+                     : mean <= gsr::kRoutedWide || K % BK == 0 || rows ? gsr::kRoutedWide
+                                                                      : gsr::kRoutedDouble;
   const int64_t ctas = 2 * std::min<int64_t>(pairs_of(P), (cdiv(M, tokens) + E) * n_tiles *
                                                               cdiv(K, 2 * stage_k(false, tokens)));
   if (gsr::log_config_enabled())

@@ -184,6 +184,25 @@ def test_grouped_long_k(setup, counts, gated, gather):
     assert U.untouched(full, M, torch.ones(M, dtype=torch.bool, device=U.DEV))
 
 
+@pytest.mark.parametrize("each,gather", [(12, True), (12, False), (90, True), (250, True), (250, False), (300, False)])
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+def test_whole_tiles_and_cut_ones(setup, each, gather, gated):
+    """More tiles than pairs, and a k long enough that the remaining ones are cut."""
+    plan, ws = setup
+    N, K, counts = 1088 // (2 if gated else 1), 5160, [each] * 19 + [each - 5]
+    M = sum(counts)
+    g = U.gen(each)
+    X = U.normal(g, M, K)
+    W = U.normal(g, len(counts), 2 * N if gated else N, K, std=K ** -0.5)
+    rows = torch.randint(0, M, (M,), generator=g, device=U.DEV, dtype=torch.int32) if gather else None
+    full, Y = U.guarded(M, N)
+    (B.gemm_grouped_gated if gated else B.gemm_grouped)(plan, X, W, U.offsets_of(counts), Y, ws, rows=rows)
+    status_ok(setup)
+    ref, bound = U.grouped_ref(X, W, counts, rows, gated)
+    U.close(Y, ref, bound)
+    assert U.untouched(full, M, torch.ones(M, dtype=torch.bool, device=U.DEV))
+
+
 @pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
 def test_rows_of_no_group_stay(setup, gated):
     """Offsets that start past 0 and end before M: the other rows are not written."""
