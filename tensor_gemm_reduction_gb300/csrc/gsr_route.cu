@@ -18,7 +18,7 @@
 // above with those beginnings in place of its own. It starts beside the first two and
 // waits for them only after it has matched and ordered its own entries. A CTA's
 // counts and beginnings live in its own part of position, at least E entries, which
-// that CTA alone reads back before it writes positions there: no workspace. 13.3 us
+// that CTA alone reads back before it writes positions there: no workspace. 11.5 us
 // for those 262144, three quarters of it the chain of launches.
 //
 // Combine. Y[t] = base[t] + sum_j weight[t, j] * Z[position[t, j]], fp32, j
@@ -39,7 +39,8 @@ constexpr int kRouteWarps = 32;         // at most
 constexpr int kRouteThreads = 32 * kRouteWarps;
 constexpr int kHeld = 16;               // entries per thread, at most
 constexpr int kHeldMax = kRouteThreads * kHeld;   // per CTA
-constexpr int kScanCtas = 8;            // the cluster of the second launch
+constexpr int kScanCtas = 16;           // the cluster of the second launch
+constexpr int kScanThreads = 512;       // of them each, at most
 constexpr int kScanRows = 8;            // CTAs' counts that a thread keeps in registers
 enum RouteForm : int { kAlone = 0, kCluster = 1, kChain = 2 };
 constexpr int kRouteCluster = 16;       // CTAs of kCluster
@@ -120,18 +121,18 @@ __global__ void __launch_bounds__(kRouteThreads, 1) gsr_route_count_kernel(const
 // Second launch: the counts c[part][e] become the sorted rows at which they begin. A
 // CTA of the cluster has a run of groups; its threads are a grid of groups times runs
 // of parts.
-__global__ void __launch_bounds__(kRouteThreads, 1) gsr_route_scan_kernel(const RouteParams p) {
-  __shared__ int sums[kRouteThreads], groups[kRouteThreads];
+__global__ void __launch_bounds__(kScanThreads, 1) gsr_route_scan_kernel(const RouteParams p) {
+  __shared__ int sums[kScanThreads], groups[kMaxGroups / kScanCtas];
   __shared__ int total;
   // The third launch may start: the first has begun, so every kernel before it is done.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = static_cast<int>(threadIdx.x);
+  const int tid = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x);
   const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
   const int own = (p.E + ctas - 1) / ctas, e0 = cta * own, width = min(own, max(p.E - e0, 0));
   const int shift = 32 - __clz(own - 1);   // 2^shift >= own
   const int columns = 1 << shift;
   const int x = tid & (columns - 1), y = tid >> shift;
-  const int per = (p.parts + (kRouteThreads >> shift) - 1) / (kRouteThreads >> shift);
+  const int per = (p.parts + (threads >> shift) - 1) / (threads >> shift);
   const int r0 = min(y * per, p.parts), r1 = x < width ? min(r0 + per, p.parts) : r0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   auto load = [&](int r, int (&v)[kScanRows]) {
@@ -151,13 +152,13 @@ __global__ void __launch_bounds__(kRouteThreads, 1) gsr_route_scan_kernel(const 
   // Inclusive sums down a group's runs of parts, then over the CTA's groups.
   sums[tid] = sum;
   __syncthreads();
-  for (int d = columns; d < kRouteThreads; d *= 2) {
+  for (int d = columns; d < threads; d *= 2) {
     const int v = tid >= d ? sums[tid - d] : 0;
     __syncthreads();
     sums[tid] += v;
     __syncthreads();
   }
-  const int of_group = sums[kRouteThreads - columns + x];
+  const int of_group = sums[threads - columns + x];
   if (y == 0) groups[x] = of_group;
   __syncthreads();
   for (int d = 1; d < columns; d *= 2) {
@@ -443,6 +444,8 @@ cudaError_t prepare_route_kernels() {
     e = cudaFuncSetAttribute(gsr_route_kernel<kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(gsr_route_kernel<kChain>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(gsr_route_scan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
 }
 
@@ -451,8 +454,8 @@ cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
   const int64_t units = (static_cast<int64_t>(p.n) + 31) / 32;
   // One CTA, the cluster, or three launches, measured side by side in loops of calls
   // (us, 64 groups): 1024 entries 4.0 / 4.2 / -, 2048 4.8 / 4.4, 4096 7.2 / 4.6 / 10, 16384
-  // - / 6.0 / 10.4, 32768 7.0 / 10.7, 65536 10.4 / 10.8, 131072 13.4 / 10.9, 262144 19.5 /
-  // 12.4; with 1000 groups 2048 6.3 / 11, 4096 8.9 / 11.2, 32768 - / 13.2 / 11.9.
+  // - / 6.0 / 10.4, 32768 7.0 / 9.5, 65536 10.4 / 9.5, 131072 13.4 / 9.7, 262144 19.5 /
+  // 11; with 1000 groups 2048 6.3 / 11, 4096 8.9 / 11.2, 32768 - / 13.2 / 11.
   const RouteForm form = p.n <= 2048 ? kAlone : p.n <= 49152 ? kCluster : kChain;
   // kChain: parts of some 2048 entries, on every SM twice, or, if those are too few, of a
   // CTA's capacity; never fewer entries than kMaxGroups.
@@ -479,8 +482,10 @@ cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
   };
   if (form == kAlone) return launch(gsr_route_kernel<kAlone>, grid, threads, smem, 0);
   if (form == kCluster) return launch(gsr_route_kernel<kCluster>, grid, threads, smem, kRouteCluster);
+  // The scan: threads for its groups times runs of parts, few for cheap barriers (262144
+  // entries of 256 groups, 256 / 512 threads 11.5 / 12.6 us, of 1000 groups 17.6 / 16.2).
   cudaError_t e = launch(gsr_route_count_kernel, grid, threads, 0, 0);
-  if (e == cudaSuccess) e = launch(gsr_route_scan_kernel, dim3(kScanCtas), kRouteThreads, 0, kScanCtas);
+  if (e == cudaSuccess) e = launch(gsr_route_scan_kernel, dim3(kScanCtas), p.E <= 512 ? 256 : kScanThreads, 0, kScanCtas);
   if (e == cudaSuccess) e = launch(gsr_route_kernel<kChain>, grid, threads, smem, 0);
   return e;
 }
