@@ -989,8 +989,9 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
   if (id >= p.L) id = -1;   // no adapter of the list is negative
   const bool self = C::SELF && p.self_rows;
   if (self) {
-    // Half a tile's tokens are 8 at least, so rank 0 holds every row.
-    if (local == 0 && rank == 0) self_rows(p, *q.table, q.part, i + TEAM * 32 * kPlacers);
+    // Rank 0 places every row (half a tile's tokens are 8 at least), but either CTA's
+    // epilogue may need them (add_unbounded).
+    if (local == 0) self_rows(p, *q.table, q.part, i + TEAM * 32 * kPlacers);
   } else {
 #pragma unroll
     for (int c = 0; c < kMaxRank / 8; ++c)
