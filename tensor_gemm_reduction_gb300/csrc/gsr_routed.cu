@@ -988,6 +988,8 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
   if (row < half && m < p.M) id = p.adapter[m];
   if (id >= p.L) id = -1;   // no adapter of the list is negative
   const bool self = C::SELF && p.self_rows;
+  // Columns from the rank to its padding are zeros here, whatever the low-rank rows
+  // hold there: an infinite activation times the padding of A is NaN.
   if (self) {
     // Rank 0 places every row (half a tile's tokens are 8 at least), but either CTA's
     // epilogue may need them (add_unbounded).
@@ -995,7 +997,7 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
   } else {
 #pragma unroll
     for (int c = 0; c < kMaxRank / 8; ++c)
-      v[c] = id >= 0 && 8 * c < p.rank_pad
+      v[c] = id >= 0 && 8 * c < p.rank
                  ? __ldcg(reinterpret_cast<const uint4*>(p.low + static_cast<size_t>(m) * p.rank_pad) + c)
                  : make_uint4(0, 0, 0, 0);
   }
@@ -1014,7 +1016,7 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
 #pragma unroll
     for (int c = 0; c < kMaxRank / 8; ++c) {
       uint32_t w[4] = {0, 0, 0, 0};
-      if (8 * c < kSelfElements && id >= 0 && 8 * c < p.rank_pad) {
+      if (8 * c < kSelfElements && id >= 0 && 8 * c < p.rank) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           w[i] = self_low(p, q.part, m, 8 * c + 2 * i, scale) |

@@ -1,5 +1,5 @@
 """AR with adapters where values are not finite: infinite weights in either CTA's
-half of a weight tile."""
+half of a weight tile, infinite activations and scales at ranks that are padded."""
 import pytest
 import torch
 
@@ -57,3 +57,30 @@ def test_infinite_weights_in_both_halves_of_a_tile(setup, M, rank):
         adapter[0] = 2
     ref, bound = U.lora_ref([X], [W], [A], Bm, adapter, scale)
     same_beyond_finite(call(setup, [X], [W], [A], Bm, adapter, scale), ref, bound)
+
+
+@pytest.mark.parametrize("rank", [8, 24, 40, 72, 64])
+@pytest.mark.parametrize("M", [1, 2, 40, 300, 1100])
+def test_infinite_activations_and_scales(setup, M, rank):
+    """Ranks below their padded width. All low-rank rows are positive, so that a column
+    whose weights are positive gets an infinity and not NaN."""
+    g = U.gen(M + rank)
+    N, K, L = 264, 136, 4
+    X, W = U.normal(g, M, K).abs(), U.normal(g, N, K, std=K ** -0.5)
+    A = U.normal(g, L, rank, K, std=K ** -0.5).abs()
+    Bm = U.normal(g, L, N, rank, std=rank ** -0.5)
+    Bm[:, ::2] = Bm[:, ::2].abs() + 2.0 ** -10
+    scale = torch.tensor([0.5, float("inf"), 1.0, 0.25], device=U.DEV)
+    adapter = (torch.arange(M, device=U.DEV) % (L + 1)).to(torch.int32)   # L: none
+    rows = {}
+    for m, a in ((0, 0), (5, 0), (M // 2, 1), (M - 2, 2), (M - 1, L)):
+        if 0 <= m < M:
+            rows.setdefault(m, a)
+    for m, a in rows.items():
+        adapter[m] = a
+        if a != 1:
+            X[m, 77] = float("inf")
+    ref, bound = U.lora_ref([X], [W], [A], Bm, adapter, scale)
+    Y = call(setup, [X], [W], [A], Bm, adapter, scale)
+    assert torch.isinf(ref).any()
+    same_beyond_finite(Y, ref, bound)
