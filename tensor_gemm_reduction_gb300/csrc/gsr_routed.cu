@@ -869,8 +869,10 @@ __device__ __forceinline__ bool look_over(const RoutedParams& p, const Tile& t, 
   return ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0;
 }
 
-// The weights of a marked tile's stage that are not finite become 0 (the epilogue
-// adds their products to the rows that have the adapter).
+// The weights of a marked tile's stage that are not finite become 1 or -1, by their
+// sign (the epilogue adds their products to the rows that have the adapter). A masked
+// row's product with those is 0, a finite row's is lost in the infinity or NaN that is
+// added, and an infinite row's is the infinity that it is due; with 0 it would be NaN.
 template <class C>
 __device__ __noinline__ void take_out(const RoutedParams& p, uint32_t sw, int units, int who) {
   const uint32_t unit = Geometry<C>(p).unit_w, bytes = 2u * p.w_rows * p.unit_cols;
@@ -885,7 +887,8 @@ __device__ __noinline__ void take_out(const RoutedParams& p, uint32_t sw, int un
       for (int j = 0; j < 4; ++j) {
         // Bits 15 and 31: an exponent of all ones in the half below.
         const uint32_t odd = ((w[j] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-        w[j] &= ~((odd >> 15) * 0xffffu);
+        const uint32_t taken = (odd >> 15) * 0xffffu;
+        w[j] = (w[j] & ~taken) | (((w[j] & 0x80008000u) | 0x3f803f80u) & taken);
       }
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sw + u * unit + at), "r"(w[0]),
                    "r"(w[1]), "r"(w[2]), "r"(w[3])

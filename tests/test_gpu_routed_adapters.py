@@ -1,5 +1,6 @@
 """AR with adapters where values are not finite: infinite weights in either CTA's
-half of a weight tile, infinite activations and scales at ranks that are padded."""
+half of a weight tile, infinite activations and scales at ranks that are padded,
+and both together."""
 import pytest
 import torch
 
@@ -84,3 +85,23 @@ def test_infinite_activations_and_scales(setup, M, rank):
     Y = call(setup, [X], [W], [A], Bm, adapter, scale)
     assert torch.isinf(ref).any()
     same_beyond_finite(Y, ref, bound)
+
+
+@pytest.mark.parametrize("M,rank", [(1, 16), (2, 16), (1, 8), (40, 16), (40, 72), (300, 24), (1100, 16)])
+def test_infinite_activations_meet_infinite_weights(setup, M, rank):
+    """Infinity times infinity is an infinity: columns whose infinite and finite weights
+    have one sign."""
+    g = U.gen(30 + M + rank)
+    N, K, L = 264, 136, 3
+    X, W = U.normal(g, M, K).abs(), U.normal(g, N, K, std=K ** -0.5)
+    A = U.normal(g, L, rank, K, std=K ** -0.5).abs()
+    Bm = U.normal(g, L, N, rank, std=rank ** -0.5).abs() + 2.0 ** -10
+    Bm[:, 1::2] *= -1
+    for i, n in enumerate([0, 5, 40, 63, 130, 255, 256, 263]):
+        Bm[1, n, i % rank] *= float("inf")
+    adapter = (torch.arange(M, device=U.DEV) % L).to(torch.int32)
+    adapter[M - 1] = 1
+    X[M - 1, 77] = float("inf")
+    ref, bound = U.lora_ref([X], [W], [A], Bm, adapter, None)
+    assert torch.isinf(ref[M - 1, [0, 5, 40, 63, 130, 255, 256, 263]]).any()
+    same_beyond_finite(call(setup, [X], [W], [A], Bm, adapter), ref, bound)
