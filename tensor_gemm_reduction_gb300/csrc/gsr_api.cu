@@ -644,7 +644,7 @@ gsr_status run_ksharded(const gemm_shard_plan* P, int mode, int64_t M, int64_t N
                            : encode_kmajor(&p.tmap_a[r], X_r[r], M, K_r[r], c.small ? c.x_rows : BM);
     if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding X_r[%d] descriptor failed (%d)", r, (int)cr);
     cr = c.kz > 1 ? encode_kmajor_3d(&p.tmap_b[r], W_r[r], N, K_r[r], c.block_n / 2, c.kz)
-                  : encode_kmajor(&p.tmap_b[r], W_r[r], N, K_r[r], c.block_n / c.cta_group);
+                  : encode_kmajor(&p.tmap_b[r], W_r[r], N, K_r[r], c.block_n / std::min(c.cta_group, 2));
     if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding W_r[%d] descriptor failed (%d)", r, (int)cr);
   }
   for (int r = R; r <= kMaxShards; ++r) p.shard_kb_begin[r] = kb;
@@ -947,7 +947,7 @@ static gsr_status run_ag(const gemm_shard_plan* P, int64_t N, int64_t K, int R, 
     p.shard_row_begin[r] = row;
   }
   p.ag_halves = mt;
-  CUresult cr = encode_kmajor(&p.tmap_b[0], W, N, K, c.block_n / c.cta_group);
+  CUresult cr = encode_kmajor(&p.tmap_b[0], W, N, K, c.block_n / std::min(c.cta_group, 2));
   if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding the W descriptor failed (%d)", (int)cr);
   p.y = static_cast<uint16_t*>(Y);
   p.ready = ready;

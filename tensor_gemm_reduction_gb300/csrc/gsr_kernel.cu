@@ -262,8 +262,7 @@ __host__ __device__ constexpr uint32_t acc_stride() { return tmem_cols<BN>() / 2
 template <int BN, int STAGES, int CG>
 struct Layout {
   static constexpr uint32_t kABytes = BM * BK * 2;            // this CTA's rows of A
-  // This CTA's columns of B: all of them, or its half of a pair's (with two
-  // pairs in a cluster, each pair loads half of that half and multicasts it).
+  // This CTA's columns of B: all of them, or its half of a pair's.
   static constexpr uint32_t kBBytes = (BN / (CG == 1 ? 1 : 2)) * BK * 2;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes;
   static constexpr uint32_t kTiles = STAGES * kStageBytes;
@@ -369,12 +368,9 @@ __device__ void run_producer(const Params& p, uint32_t tiles_base, uint32_t bars
     const int a_row = t.shard >= 0 ? t.m0 : p.shard_rows[p.ag_pad_shard];
     const int a_shard_b = shard_b >= 0 ? shard_b : p.ag_pad_shard;
     const int a_row_b = shard_b >= 0 ? m0b : p.shard_rows[p.ag_pad_shard];
-    // CG = 4: this CTA's columns of B (its pair half) are loaded as two
-    // quarter boxes, one by each pair, and multicast to the CTA at the same
-    // place in both pairs; quarter p lands BN/4 rows into the half.
+    // CG = 4: each of the two pairs copies its own B, the same columns.
     const int b_row = CG <= 2 ? t.n0 + static_cast<int>(rank * (tile_mma_n<BN>(p, t) / CG))
-                              : t.n0 + static_cast<int>((rank & 1u) * (tile_mma_n<BN>(p, t) / 2)) +
-                                    static_cast<int>(rank >> 1) * (BN / 4);
+                              : t.n0 + static_cast<int>((rank & 1u) * (tile_mma_n<BN>(p, t) / 2));
     // AR/RS: shard r holds k-blocks [r_begin, r_end). The search stops at a
     // shard whose range holds kb_begin (< the k-block count, and every shard
     // has at least one k-block).
@@ -434,22 +430,13 @@ __device__ void run_producer(const Params& p, uint32_t tiles_base, uint32_t bars
           // measured as issue time on this loop.
           const uint32_t lead_full = lead_full0 + 8 * stage;
           const bool leader = (rank & 1u) == 0;
-          if constexpr (CG == 4) {
-            // The pair's bytes (its A rows and both halves of its B columns,
-            // whichever pair loaded them) complete on its leader's barrier.
+          if constexpr (kTwo) {
             if (leader) mbar_arrive_expect_tx(full, 2 * L::kStageBytes);
-            tma_load_2d_pair(sa, ma, lead_full, kx, a_row, pol_a);
-            if constexpr (kTwo) tma_load_2d_pair(sa + kHalfA, ma_b, lead_full, kx, a_row_b, pol_a);
-            const uint16_t both = static_cast<uint16_t>((1u << (rank & 1u)) | (4u << (rank & 1u)));
-            tma_load_2d_pair_multicast(sb + (rank >> 1) * (L::kBBytes / 2), mb, lead_full, kx, b_row,
-                                       both, pol_b);
-          } else if constexpr (kTwo) {
-            if (leader) mbar_arrive_expect_tx(full, CG * L::kStageBytes);
             tma_load_2d_pair(sa, ma, lead_full, kx, a_row, pol_a);
             tma_load_2d_pair(sa + kHalfA, ma_b, lead_full, kx, a_row_b, pol_a);
             tma_load_2d_pair(sb, mb, lead_full, kx, b_row, pol_b);
           } else {
-            stage_copies_pair(leader ? 1u : 0u, full, CG * L::kStageBytes, lead_full, sa, ma,
+            stage_copies_pair(leader ? 1u : 0u, full, 2 * L::kStageBytes, lead_full, sa, ma,
                               a_row, sb, mb, b_row, kx, pol_a, pol_b);
           }
         }
@@ -481,10 +468,7 @@ __device__ void run_mma(const Params& p, uint32_t tiles_base, uint32_t bars, uin
   const uint32_t full0 = bars, tfull0 = bars + 16 * STAGES, tempty0 = tfull0 + 16;
   const uint32_t empty0 = bars + 8 * STAGES, drain = tempty0 + 16;
   // Only a pair's leader issues its MMAs (rank 0, or 0 and 2 with two pairs).
-  // A stage is freed in every CTA its copies wrote: both CTAs of the pair, or
-  // all four with two pairs (each CTA's empty barrier then counts both
-  // leaders' commits). The accumulator is the pair's.
-  constexpr uint16_t kFreeMask = CG == 4 ? 0xF : 0x3;
+  // A stage and the accumulator are the pair's.
   const uint16_t pair_mask = static_cast<uint16_t>(0x3u << (rank & ~1u));
   uint32_t stage = 0, phase = 0, local = 0;   // next ring slot and its fill phase
   bool ok = true, issued_any = false;
@@ -545,7 +529,7 @@ __device__ void run_mma(const Params& p, uint32_t tiles_base, uint32_t bars, uin
       if constexpr (CG == 1)
         mma_commit(empty0 + 8 * cur);
       else
-        mma_commit_pair(empty0 + 8 * cur, kFreeMask);   // frees the slot in every CTA it fed
+        mma_commit_pair(empty0 + 8 * cur, pair_mask);   // frees the slot in both CTAs
       if (!looked_ahead) {
         have_next = sched_next<BN, CG>(p, sch, tn, rank);
         looked_ahead = true;
@@ -798,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) gsr_gemm_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(bars + 8 * i, 1);                 // full: the (leader's) expect_tx + TMA bytes
-      mbar_init(bars + 8 * (STAGES + i), CG == 4 ? 2 : 1);   // empty: each feeding leader's commit
+      mbar_init(bars + 8 * (STAGES + i), 1);      // empty: the MMAs' commit
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + 16 * STAGES + 8 * i, 1);               // tmem_full: MMA commit
@@ -869,7 +853,7 @@ template <> struct Stages<128, 1> { static constexpr int value = 6; };   // 32 K
 template <> struct Stages<256, 2> { static constexpr int value = 7; };   // 32 KB per CTA
 template <> struct Stages<128, 2> { static constexpr int value = 8; };   // 24 KB per CTA
 template <> struct Stages<192, 2> { static constexpr int value = 8; };   // 28 KB per CTA
-// Two CTA pairs per cluster (B multicast between the pairs): the same stages.
+// Two CTA pairs per cluster: the same stages.
 template <> struct Stages<256, 4> { static constexpr int value = 7; };
 template <> struct Stages<128, 4> { static constexpr int value = 8; };
 template <> struct Stages<192, 4> { static constexpr int value = 8; };
