@@ -1,0 +1,134 @@
+"""The routed projections' kernels and branches that small calls do not reach: adapters
+of more than 1024 rows, adapters whose tiles are cut along k, more than sixteen token
+tiles of one group or call, and combines with two vectors per thread."""
+import pytest
+import torch
+
+from tensor_gemm_reduction_gb300 import binding as B
+from tensor_gemm_reduction_gb300 import build as gbuild
+
+import routed_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def setup():
+    gbuild.build()
+    plan = B.gemm_shard_plan_create(0, 32768, 8192, 8192, 16)
+    ws = B.gemm_routed_workspace_alloc(plan)
+    B.gemm_routed_workspace_init(plan, ws)
+    return plan, ws
+
+
+def adapters(g, M, L, run, none):
+    a = torch.randint(0, L, (-(-M // run),), generator=g, device=U.DEV, dtype=torch.int32).repeat_interleave(run)[:M]
+    return a.masked_fill(torch.rand(M, generator=g, device=U.DEV) < none, -1).contiguous()
+
+
+def lora(setup, M, N, K_r, L, rank, run, none=0.2, odd=()):
+    """One case against the 64-bit product; `odd`: (adapter, column, place, value) of B."""
+    plan, ws = setup
+    g = U.gen(M + N + rank)
+    K = sum(K_r)
+    X_r = [U.normal(g, M, k) for k in K_r]
+    W_r = [U.normal(g, N, k, std=K ** -0.5) for k in K_r]
+    A_r = [U.normal(g, L, rank, k, std=K ** -0.5) for k in K_r]
+    Bm = U.normal(g, L, N, rank, std=rank ** -0.5)
+    for a, n, j, value in odd:
+        Bm[a, n, j] = value
+    adapter = adapters(g, M, L, run, none)
+    if odd:
+        adapter[:3] = torch.arange(3, device=U.DEV)
+    scale = torch.randn(L, generator=g, device=U.DEV)
+    outs = []
+    for _ in range(2):
+        full, Y = U.guarded(M, N)
+        B.gemm_ar_lora(plan, X_r, W_r, A_r, Bm, adapter, Y, ws, scale=scale)
+        outs.append(full)
+        assert U.untouched(full, M, torch.ones(M, dtype=torch.bool, device=U.DEV))
+    B.gemm_shard_check_status(plan, ws)
+    assert torch.equal(outs[0], outs[1]), "two calls on the same inputs differ"
+    ref, bound = U.lora_ref(X_r, W_r, A_r, Bm, adapter, scale)
+    finite, infinite = torch.isfinite(ref), torch.isinf(ref)
+    assert bool(odd) != bool(finite.all())
+    assert torch.equal(torch.isnan(Y), torch.isnan(ref))
+    assert torch.equal(Y[infinite].double(), ref[infinite])
+    U.close(Y[finite], ref[finite], bound[finite])
+
+
+ODD = [(1, 3, 0, float("inf")), (1, 150, 7, float("-inf")), (2, 40, 2, float("nan")), (0, 255, 5, float("inf"))]
+
+
+@pytest.mark.parametrize("M,N,K_r,L,rank,run", [
+    (1025, 264, [200], 5, 24, 1), (1100, 520, [328, 72], 9, 96, 200), (1300, 264, [136], 200, 16, 1),
+    (2100, 264, [256], 7, 64, 1), (2100, 520, [72, 200], 3, 128, 300), (4200, 264, [72], 6, 40, 17),
+    (2049, 200, [64] * 5, 1, 8, 1),
+], ids=lambda v: str(v).replace(" ", ""))
+def test_lora_of_many_rows(setup, M, N, K_r, L, rank, run):
+    lora(setup, M, N, K_r, L, rank, run)
+
+
+def test_lora_of_many_rows_without_an_adapter_and_with_one_each(setup):
+    lora(setup, 1153, 264, [136], 4, 48, 1, none=1.0)
+    lora(setup, 1153, 264, [136], 4, 48, 1, none=0.0)
+
+
+def test_lora_of_many_rows_with_infinite_weights(setup):
+    lora(setup, 1500, 264, [136], 4, 96, 40, odd=ODD)
+
+
+@pytest.mark.parametrize("M,N,L,rank", [(40, 264, 40, 16), (100, 264, 60, 32), (100, 264, 5, 128), (200, 264, 200, 24),
+                                        (256, 520, 50, 72), (300, 4096, 30, 64), (300, 4096, 100, 16),
+                                        (300, 4096, 9, 128)])
+@pytest.mark.parametrize("odd", [False, True], ids=["finite", "infinite"])
+def test_lora_cut_along_k(setup, M, N, L, rank, odd):
+    """Few tiles and a long k: pieces share the adapters' steps."""
+    K_r = [6168, 1000] if M == 300 else [4160, 1000]
+    lora(setup, M, N, K_r, L, rank, 1, odd=ODD if odd else ())
+
+
+@pytest.mark.parametrize("counts,N,K", [
+    ([1100] + [0] * 60, 264, 136),           # 64-token tiles
+    ([0] * 20 + [2200], 264, 72),            # 128
+    ([4500], 264, 128), ([3, 4700, 5], 520, 64),   # 256
+    ([8400], 264, 72), ([8350, 1, 300], 264, 200),   # 512
+], ids=lambda v: "-".join(map(str, v)) if isinstance(v, list) and len(v) < 9 else str(len(v)) if isinstance(v, list) else str(v))
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("gather", [False, True], ids=["rows", "gathered"])
+def test_more_than_sixteen_token_tiles(setup, counts, N, K, gated, gather):
+    plan, ws = setup
+    g = U.gen(sum(counts) + N)
+    M, E = sum(counts), len(counts)
+    T = M // 2 if gather else M
+    X = U.normal(g, T, K)
+    W = U.normal(g, E, 2 * N if gated else N, K, std=K ** -0.5)
+    rows = torch.randint(0, T, (M,), generator=g, device=U.DEV, dtype=torch.int32) if gather else None
+    full, Y = U.guarded(M, N)
+    (B.gemm_grouped_gated if gated else B.gemm_grouped)(plan, X, W, U.offsets_of(counts), Y, ws, rows=rows)
+    B.gemm_shard_check_status(plan, ws)
+    ref, bound = U.grouped_ref(X, W, counts, rows, gated)
+    U.close(Y, ref, bound)
+    assert U.untouched(full, M, torch.ones(M, dtype=torch.bool, device=U.DEV))
+
+
+@pytest.mark.parametrize("T,topk,H", [(701, 3, 3592), (400, 9, 6288), (5000, 1, 512)])
+@pytest.mark.parametrize("base", ["none", "apart", "output"])
+def test_combine_of_many_vectors(setup, T, topk, H, base):
+    plan, _ = setup
+    g = U.gen(T + H)
+    Z = U.normal(g, T * topk, H)
+    position = torch.randint(-2, T * topk + 5, (T, topk), generator=g, device=U.DEV, dtype=torch.int32)
+    weights = torch.randn(T, topk, generator=g, device=U.DEV)
+    dead = (position < 0) | (position >= Z.shape[0])
+    weights[dead] = float("nan")
+    added = U.normal(g, T, H) if base != "none" else None
+    full, Y = U.guarded(T, H)
+    if base == "output":
+        Y.copy_(added)
+    B.gemm_group_combine(plan, Z, position, weights, Y, base=Y if base == "output" else added)
+    w = torch.where(dead, 0.0, weights.double())
+    rows = Z.double()[position.long().clamp(0, Z.shape[0] - 1)] * w[:, :, None]
+    ref = rows.sum(1) + (added.double() if added is not None else 0.0)
+    U.close(Y, ref, U.ROUND * ref.abs() + U.SUM * (rows.abs().sum(1) + 1) + 1e-30)
+    assert U.untouched(full, T, torch.ones(T, dtype=torch.bool, device=U.DEV))
