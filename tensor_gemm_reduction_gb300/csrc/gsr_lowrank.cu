@@ -259,7 +259,7 @@ __device__ __forceinline__ void write_rows(const LowRankParams& p, float* share,
     float sum = v[0];
 #pragma unroll
     for (int c = 1; c < kMaxCluster; ++c) sum += v[c];
-    const float s = p.scale ? __ldg(p.scale + keeps[row]) : 1.f;
+    const float s = p.scale ? p.scale[keeps[row]] : 1.f;
     p.low[static_cast<size_t>(at[row]) * p.rank_pad + first + e - row * COLS] =
         __bfloat16_as_ushort(__float2bfloat16(sum * s));
   }

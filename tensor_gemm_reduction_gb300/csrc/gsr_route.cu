@@ -75,13 +75,13 @@ __device__ __forceinline__ void load_ids(const RouteParams& p, int i, int step, 
     long long v[kHeld];
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
-      v[j] = i + step * j < end ? __ldg(reinterpret_cast<const long long*>(p.ids) + i + step * j) : -1;
+      v[j] = i + step * j < end ? reinterpret_cast<const long long*>(p.ids)[i + step * j] : -1;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) id[j] = v[j] >= 0 && v[j] < p.E ? static_cast<int>(v[j]) : -1;
   } else {
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
-      id[j] = i + step * j < end ? __ldg(reinterpret_cast<const int*>(p.ids) + i + step * j) : -1;
+      id[j] = i + step * j < end ? reinterpret_cast<const int*>(p.ids)[i + step * j] : -1;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
       if (id[j] < 0 || id[j] >= p.E) id[j] = -1;
@@ -348,10 +348,12 @@ __device__ __forceinline__ void add_row(float (&acc)[8], uint4 v, float w) {
   }
 }
 
-// A read that is not kept in L1 (each row of Z is read once).
+// A read that is not kept in L1 (each row of Z is read once). No load here is a
+// non-coherent one: those are for memory that nothing writes while the kernel runs, and
+// this one may be resident while its predecessor writes, and base may be Y.
 __device__ __forceinline__ uint4 load_once(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(256, ITEMS == 2 ? 3 : 4) gsr_combine_kernel(co
       z[q] = reinterpret_cast<const uint4*>(p.z) + (i - t[q] * p.vecs);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[q][j] = 0.f;
-      if (p.base && i < total) add_row(acc[q], __ldg(reinterpret_cast<const uint4*>(p.base) + i), 1.f);
+      if (p.base && i < total) add_row(acc[q], reinterpret_cast<const uint4*>(p.base)[i], 1.f);
     }
     for (int j0 = 0; j0 < p.topk; j0 += 8) {
       uint4 v[ITEMS][8];
@@ -388,10 +390,10 @@ __global__ void __launch_bounds__(256, ITEMS == 2 ? 3 : 4) gsr_combine_kernel(co
         const float* wts = p.weights + t[q] * p.topk + j0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int at = j0 + j < p.topk && i0 + 256 * q < total ? __ldg(pos + j) : -1;
+          const int at = j0 + j < p.topk && i0 + 256 * q < total ? pos[j] : -1;
           const bool live = at >= 0 && at < p.z_rows;
           // An absent entry adds nothing, whatever its weight is.
-          w[q][j] = live ? __ldg(wts + j) : 0.f;
+          w[q][j] = live ? wts[j] : 0.f;
           v[q][j] = live ? load_once(z[q] + static_cast<int64_t>(at) * p.vecs) : make_uint4(0, 0, 0, 0);
         }
       }

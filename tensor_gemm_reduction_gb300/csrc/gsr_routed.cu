@@ -736,7 +736,7 @@ __device__ void gather_rows(const RoutedParams& p, const Groups& g, int tiles, u
     const int first = q.row0 + static_cast<int>(rank) * (q.n / 2), rows = rows_of(q);
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
-      r[i] = row0 + 16 * i < rows ? __ldg(p.rows + first + row0 + 16 * i) : -1;
+      r[i] = row0 + 16 * i < rows ? p.rows[first + row0 + 16 * i] : -1;
   };
   bool have = walk.step<C>(p, g, t);
   if (have) look(t, at);
@@ -918,12 +918,12 @@ __device__ __forceinline__ void self_rows(const RoutedParams& p, const SelfTable
           continue;
         }
         if (at < K) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(s.x[r] + static_cast<size_t>(m) * K + at));
+          const uint4 u = __ldcg(reinterpret_cast<const uint4*>(s.x[r] + static_cast<size_t>(m) * K + at));
           const uint16_t* a = s.a[r] + (static_cast<size_t>(id) * p.rank + j0) * K + at;
           uint4 v[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            v[j] = j0 + j < p.rank ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<size_t>(j) * K))
+            v[j] = j0 + j < p.rank ? __ldcg(reinterpret_cast<const uint4*>(a + static_cast<size_t>(j) * K))
                                    : make_uint4(0, 0, 0, 0);
           const uint32_t xw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -1015,7 +1015,7 @@ __device__ bool place_tile(const RoutedParams& p, const Tile& t, uint32_t local,
   if (!__all_sync(0xffffffffu, all)) return false;
   const bool marked = seen[local % 3] != 0;
   if (self) {
-    const float scale = id >= 0 && p.scale ? __ldg(p.scale + id) : 1.f;
+    const float scale = id >= 0 && p.scale ? p.scale[id] : 1.f;
 #pragma unroll
     for (int c = 0; c < kMaxRank / 8; ++c) {
       uint32_t w[4] = {0, 0, 0, 0};
@@ -1108,7 +1108,7 @@ __device__ __noinline__ void add_unbounded(const RoutedParams& p, const float* p
       const uint32_t w = p.b[(static_cast<size_t>(id) * p.N + n) * p.rank + k];
       if ((w & 0x7f80u) != 0x7f80u) continue;
       const uint32_t x = C::SELF && p.self_rows
-                             ? self_low(p, part, m, k, p.scale ? __ldg(p.scale + id) : 1.f)
+                             ? self_low(p, part, m, k, p.scale ? p.scale[id] : 1.f)
                              : __ldcg(p.low + static_cast<size_t>(m) * p.rank_pad + k);
       sum += __uint_as_float(w << 16) * __uint_as_float(x << 16);
       any = true;
