@@ -482,6 +482,7 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
   if constexpr (C::KIND == kLora) begins = p.shard_st_begin[lane <= kMaxShards ? lane : kMaxShards];
   Ring ring;
   uint32_t issued = 0;
+  uint32_t weighed = 0, weighings = 0;   // slots that had adapter stages; the parity of their number
   bool ok = true, waited = C::KIND != kLora;
   Walk walk;
   walk.begin(p, tiles);
@@ -587,6 +588,8 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
                     p.units_per_adapter == 2 ? ((u0 + u) & 1) * p.unit_cols : 0, w_row, id, pol_w);
         }
         __syncwarp();
+        weighed |= 1u << ring.slot;
+        weighings ^= 1u << ring.slot;
         ++issued;
         ring.next(geo.slots);
       }
@@ -595,22 +598,21 @@ __device__ void produce(const RoutedParams& p, const Groups& g, int tiles, uint3
     t = tn;
     have = have_next;
   }
-  if (!ok) {
-    // Let the copies already issued land before the shared memory goes away:
-    // they complete on the leader's barriers, whose MMAs free the slots.
-    const uint32_t first = issued > geo.slots ? issued - geo.slots : 0;
-    for (uint32_t i = first; i < issued; ++i) {
-      if (rank == 0)
-        wait_drain(full0 + 8 * (i % geo.slots), (i / geo.slots) & 1u, 100000000ull);
-      else
-        wait_drain(empty0 + 8 * (i % geo.slots), (i / geo.slots) & 1u, 100000000ull);
-    }
-    // Adapter weights complete on barriers that only the placing warps follow.
-    if constexpr (C::KIND == kLora) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
-    }
+  // Let the copies issued land before the shared memory goes away, whether this role
+  // gave up or another one did: they complete on the leader's barriers, whose MMAs free
+  // the slots, and adapter weights on a barrier of their own. (Otherwise they have
+  // landed before the epilogue is done.)
+  const uint32_t first = issued > geo.slots ? issued - geo.slots : 0;
+  for (uint32_t i = first; i < issued; ++i) {
+    if (rank == 0)
+      wait_drain(full0 + 8 * (i % geo.slots), (i / geo.slots) & 1u, 100000000ull);
+    else
+      wait_drain(empty0 + 8 * (i % geo.slots), (i / geo.slots) & 1u, 100000000ull);
   }
+  if constexpr (C::KIND == kLora)
+    for (uint32_t i = 0; i < geo.slots; ++i)
+      if ((weighed >> i) & 1u)
+        wait_drain(full0 + C::kLandedOff + 8 * i, ((weighings >> i) & 1u) ^ 1u, 100000000ull);
 }
 
 // The pair's MMAs (rank 0).
@@ -700,7 +702,8 @@ __device__ void multiply(const RoutedParams& p, const Groups& g, int tiles, uint
     t = tn;
     have = have_next;
   }
-  if (!ok && issued) {
+  // No MMA may be in flight when the accumulators go away, whichever role gave up.
+  if (issued) {
     mma_commit_pair(drain, 0x1);
     wait_drain(drain, 0, 100000000ull);
   }

@@ -132,3 +132,41 @@ def test_combine_of_many_vectors(setup, T, topk, H, base):
     ref = rows.sum(1) + (added.double() if added is not None else 0.0)
     U.close(Y, ref, U.ROUND * ref.abs() + U.SUM * (rows.abs().sum(1) + 1) + 1e-30)
     assert U.untouched(full, T, torch.ones(T, dtype=torch.bool, device=U.DEV))
+
+
+@pytest.mark.parametrize("kind", ["grouped", "gathered", "gated", "wide", "lora few", "lora half", "lora"])
+def test_waits_of_a_nanosecond(kind):
+    """The shortest limit that a wait can have: the call gives its result or a status, never
+    a fault, and after another init the same workspace serves the same call."""
+    gbuild.build()
+    g = U.gen(len(kind))
+    M = {"lora few": 1, "lora half": 100, "wide": 2000}.get(kind, 700)
+    N, K, L, rank = 520, 2008, 5, 16
+    X, W = U.normal(g, M, K), U.normal(g, 3, 2 * N if kind == "gated" else N, K, std=K ** -0.5)
+    full, Y = U.guarded(M, N)
+    counts = [M // 2, 0, M - M // 2]
+    A, Bm = U.normal(g, L, rank, K, std=K ** -0.5), U.normal(g, L, N, rank, std=rank ** -0.5)
+    adapter = adapters(g, M, L, 1, 0.1)
+    rows = torch.randint(0, M, (M,), generator=g, device=U.DEV, dtype=torch.int32) if kind == "gathered" else None
+    for limit in (1, 0):   # 0: the default
+        plan = B.gemm_shard_plan_create(0, 4096, 1024, 4096, 1)
+        B.gemm_shard_plan_set_option(plan, B.GSR_OPT_TIMEOUT_NS, limit)
+        if limit:
+            ws = B.gemm_routed_workspace_alloc(plan)
+        B.gemm_routed_workspace_init(plan, ws)
+        if kind.startswith("lora"):
+            B.gemm_ar_lora(plan, [X], [W[0]], [A], Bm, adapter, Y, ws)
+        elif kind == "gated":
+            B.gemm_grouped_gated(plan, X, W, U.offsets_of(counts), Y, ws)
+        else:
+            B.gemm_grouped(plan, X, W, U.offsets_of(counts), Y, ws, rows=rows)
+        torch.cuda.synchronize()
+        assert U.untouched(full, M, torch.ones(M, dtype=torch.bool, device=U.DEV))
+        try:
+            B.gemm_shard_check_status(plan, ws)
+        except B.GsrError as e:
+            assert limit and e.status == B.GSR_ERR_TIMEOUT
+            continue
+        ref, bound = (U.lora_ref([X], [W[0]], [A], Bm, adapter, None) if kind.startswith("lora")
+                      else U.grouped_ref(X, W, counts, rows, kind == "gated"))
+        U.close(Y, ref, bound)
