@@ -1,6 +1,10 @@
 """The routed projections' kernels and branches that small calls do not reach: adapters
 of more than 1024 rows, adapters whose tiles are cut along k, more than sixteen token
-tiles of one group or call, and combines with two vectors per thread."""
+tiles of one group or call, several weight tiles per CTA pair, combines with two vectors
+per thread, and tensors of more than 2^32 elements.
+
+The bounds are routed_util's: a sum of K products is within 2^-17 of sum |x w| for every
+K here (sqrt(K) * 2^-24 < 2^-17 up to K = 16384)."""
 import pytest
 import torch
 
@@ -39,7 +43,7 @@ def lora(setup, M, N, K_r, L, rank, run, none=0.2, odd=()):
         Bm[a, n, j] = value
     adapter = adapters(g, M, L, run, none)
     if odd:
-        adapter[:3] = torch.arange(3, device=U.DEV)
+        adapter[:3] = torch.arange(min(3, M), device=U.DEV)
     scale = torch.randn(L, generator=g, device=U.DEV)
     outs = []
     for _ in range(2):
@@ -170,3 +174,99 @@ def test_waits_of_a_nanosecond(kind):
         ref, bound = (U.lora_ref([X], [W[0]], [A], Bm, adapter, None) if kind.startswith("lora")
                       else U.grouped_ref(X, W, counts, rows, kind == "gated"))
         U.close(Y, ref, bound)
+
+
+@pytest.mark.parametrize("M,L,rank,odd", [(1, 3, 16, False), (2, 3, 16, True), (1, 3, 32, True), (40, 40, 16, True),
+                                          (100, 60, 32, False), (128, 9, 128, True), (200, 200, 24, False),
+                                          (256, 50, 72, True)])
+@pytest.mark.parametrize("N,ctas", [(4096, 8), (4096, 2), (12008, 0)])
+def test_several_weight_tiles_per_pair(M, L, rank, odd, N, ctas):
+    """Few rows and more weight tiles than CTA pairs: tiles follow one another in the same
+    ring, accumulators and teams."""
+    gbuild.build()
+    plan = B.gemm_shard_plan_create(0, 1024, 16384, 4096, 4)
+    B.gemm_shard_plan_set_option(plan, B.GSR_OPT_MAX_CTAS, ctas)
+    ws = B.gemm_routed_workspace_alloc(plan)
+    B.gemm_routed_workspace_init(plan, ws)
+    lora((plan, ws), M, N, [328, 1000], L, rank, 1, none=0.0 if M < 3 else 0.2, odd=[
+        (a % (L if M > 2 else M), n, j, v) for a, n, j, v in ODD + [(1, 2050, 1, float("inf")), (0, 4090, 3, float("-inf"))]
+    ] if odd else ())
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+
+def big(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16, device=U.DEV)
+
+
+def test_grouped_weights_and_rows_past_32_bits(setup):
+    """E x N x K and T x K above 2^32 elements: the last group's weights, the last rows."""
+    plan, ws = setup
+    g = U.gen(40)
+    E, N, K, T = 70, 8192, 8192, 600000
+    W, X = big(E, N, K), big(T, K)
+    counts = [0] * E
+    counts[0], counts[E - 2], counts[E - 1] = 5, 30, 3
+    for e in (0, E - 2, E - 1):
+        W[e].normal_(0.0, K ** -0.5, generator=g)
+    rows = torch.randint(T - 100, T, (38,), generator=g, device=U.DEV, dtype=torch.int32)
+    rows[::3] -= T - 100
+    X[-100:].normal_(generator=g)
+    X[:100].normal_(generator=g)
+    for gather in (True, False):
+        Y = torch.empty(38, N, dtype=torch.bfloat16, device=U.DEV)
+        x = X if gather else X[-38:]
+        B.gemm_grouped(plan, x, W, U.offsets_of(counts), Y, ws, rows=rows if gather else None)
+        B.gemm_shard_check_status(plan, ws)
+        x = x[rows.long()] if gather else x
+        at = 0
+        for e in (0, E - 2, E - 1):
+            part, n = x[at:at + counts[e]], counts[e]
+            ref, bound = U.grouped_ref(part, W[e:e + 1], [n], None, False)
+            U.close(Y[at:at + n], ref, bound, f"group {e}")
+            at += n
+
+
+def test_combined_rows_past_32_bits(setup):
+    plan, _ = setup
+    g = U.gen(41)
+    rows, H = 600000, 7168
+    Z = big(rows, H)
+    Z[-50:].normal_(generator=g)
+    Z[:50].normal_(generator=g)
+    for T in (7, 400):
+        position = torch.randint(rows - 50, rows, (T, 2), generator=g, device=U.DEV, dtype=torch.int32)
+        position[:, 1] -= rows - 50
+        weights = torch.randn(T, 2, generator=g, device=U.DEV)
+        Y = torch.empty(T, H, dtype=torch.bfloat16, device=U.DEV)
+        B.gemm_group_combine(plan, Z, position, weights, Y)
+        part = Z[position.long()].double() * weights.double()[:, :, None]
+        ref = part.sum(1)
+        U.close(Y, ref, U.ROUND * ref.abs() + U.SUM * (part.abs().sum(1) + 1) + 1e-30)
+
+
+@pytest.mark.parametrize("M", [2, 40, 300, 1100])
+def test_adapters_past_32_bits(setup, M):
+    """L x N x rank and L x rank x K above 2^32 elements, adapters of both ends."""
+    plan, ws = setup
+    g = U.gen(42)
+    L, N, K, rank = 65536, 1032, 1032, 64
+    A, Bm = big(L, rank, K), big(L, N, rank)
+    used = [0, 1, 40000, L - 2, L - 1]
+    for a in used:
+        A[a].normal_(0.0, K ** -0.5, generator=g)
+        Bm[a].normal_(0.0, rank ** -0.5, generator=g)
+    Bm[L - 1, 700, 5] = float("inf")
+    X, W = U.normal(g, M, K), U.normal(g, N, K, std=K ** -0.5)
+    adapter = torch.tensor(used, device=U.DEV)[torch.arange(M, device=U.DEV) % 5].to(torch.int32)
+    adapter[M - 1] = L - 1
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device=U.DEV)
+    B.gemm_ar_lora(plan, [X], [W], [A], Bm, adapter, Y, ws)
+    B.gemm_shard_check_status(plan, ws)
+    few = torch.full_like(adapter, -1)
+    for i, a in enumerate(used):
+        few[adapter == a] = i
+    ref, bound = U.lora_ref([X], [W], [A[used]], Bm[used], few, None)
+    finite, infinite = torch.isfinite(ref), torch.isinf(ref)
+    assert torch.equal(Y[infinite].double(), ref[infinite]) and torch.equal(torch.isnan(Y), torch.isnan(ref))
+    U.close(Y[finite], ref[finite], bound[finite])
