@@ -397,8 +397,8 @@ gsr_status gemm_shard_pack_gather(const gemm_shard_plan *plan, int R, const int6
  *     gemm_routed_workspace_init and left ready for the next call by every
  *     call. gemm_shard_check_status reads its status word. gemm_group_route and
  *     gemm_group_combine need none.
- *   - Options: GSR_OPT_TIMEOUT_NS and GSR_OPT_MAX_CTAS apply to the products; the
- *     others do not.
+ *   - Options: GSR_OPT_TIMEOUT_NS and GSR_OPT_MAX_CTAS (in whole CTA pairs, one at
+ *     least) apply to the products; the others do not.
  *   - Results are reproducible: sums run in an order that depends on the shapes
  *     and the group sizes alone.
  *   - Graphs: the calls may be recorded in a CUDA graph; a replay reads the
@@ -499,6 +499,8 @@ gsr_status gemm_group_combine(const gemm_shard_plan *plan, int64_t T, int topk, 
  * The low-rank rows (scale included) are rounded to bf16 between the two
  * products; both products accumulate in fp32 in one accumulator with the base
  * product, and Y is rounded once. Only adapters that some row names are read.
+ * Values that are not finite give what the formula gives, in the rows and columns
+ * that it uses them in, and change no other.
  * M <= max_M; Y must not overlap an input. Other arguments as gemm_ar, with
  * the routed workspace.
  */

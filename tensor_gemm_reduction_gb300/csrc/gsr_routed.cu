@@ -35,12 +35,14 @@
 // row. (Stores of two columns straight from registers took 6.3 us for 256 tokens
 // x 128 columns, more than the MMAs of a tile at K = 896.)
 //
-// Measured, back to back. Streams of weights: 64 groups of a row or two, N = 7168, K =
-// 896, 104 us (0.97 of the copy bandwidth); AR with adapters, M = 1, N = K = 7168, 26 us
-// (a single launch's fixed cost beside 15). Tiles: one group of 4096 rows, N = K = 7168,
-// 1.95 PFLOP/s; 64 uneven groups of about 512, bound by reading tiles from L2 (14 TB/s)
-// and by their starts, 1.36 at K = 896 and 1.47 gathered, gated, at K = 7168; M = 4096
-// with 8 adapters of rank 64, 1.58 with the low-rank kernel's 20 of 270 us.
+// Measured. Streams of weights: 64 groups of a row or two, N = 7168, K = 896, 104 us
+// (0.97 of the copy bandwidth); AR with adapters, M = 1, N = K = 7168, 25 us (a single
+// launch's fixed cost beside 15). Tiles, in short bursts, below the power limit: one
+// group of 4096 rows, N = K = 7168, 1.95 PFLOP/s; 64 uneven groups of about 512, bound by
+// reading tiles from L2 (14 TB/s) and by their starts, 1.36 at K = 896 and 1.47 gathered,
+// gated, at K = 7168; M = 4096 with 8 adapters of rank 64, 1.58 with the low-rank kernel's
+// 20 of 270 us. In long runs at the limit the last three take 350, 655 and 304 us: 1.20,
+// 1.28 and 1.40 PFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -899,7 +901,7 @@ __device__ __noinline__ void take_out(const RoutedParams& p, uint32_t sw, int un
     }
 }
 
-// Up to kSelfRows rows: the two teams compute the low-rank rows themselves, in
+// One row or two: the two teams compute the low-rank rows themselves, in
 // every CTA that holds them, from L2 and while the weights stream, and no kernel
 // runs before the product. The 8 warps take every 8th chunk of 256 k of all columns
 // (16 rows of A in flight per warp); part[w][m][j] is warp w's sum.
