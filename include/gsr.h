@@ -510,6 +510,92 @@ gsr_status gemm_ar_lora(const gemm_shard_plan *plan, int64_t M, int64_t N, int R
                         const int32_t *adapter, const float *scale, void *Y, void *ws,
                         size_t ws_bytes, gsr_stream_t stream);
 
+/* ------------------------------------------------------- 8-bit projections
+ * The AR and AG products on 8-bit operands, and what feeds them: the residual's
+ * addition with the RMS norm, and the quantisation. (The pages this library
+ * restates have no counterpart; a serving model stores the weights and sends the
+ * activations this way.) Conventions as above, and:
+ *   - 8 bits are e4m3 (1, 4, 3 bits; finite up to 448), one byte an element, rows
+ *     dense. A group of elements shares an fp32 scale; an element stands for q *
+ *     scale. Groups of activations are 128 columns of one row, groups of weights
+ *     blocks of 128 x 128; a last group may be short. A K-shard starts its own.
+ *   - Scales of rows are stored by column block: element (b, m) of a dense
+ *     ceil(K / 128) x M array belongs to columns 128 b .. of row m. Scales of blocks
+ *     are row-major, ceil(N / 128) x ceil(K / 128). Pointers 4-byte aligned. Any
+ *     fp32 values are allowed.
+ *   - K, K_r (and H with Q) are multiples of 16.
+ *   - Quantising a group of values v: scale = max(max|v| / 448, 2^-126), q = v * (1 /
+ *     scale) to the nearest e4m3, ties to even, at most 448 in magnitude. A group
+ *     that holds NaN has scale NaN, one that holds an infinity scale infinity, and
+ *     what it stands for is NaN.
+ *   - Options: GSR_OPT_TIMEOUT_NS and GSR_OPT_MAX_CTAS (in whole CTA pairs, one at
+ *     least) apply to the products; the others do not.
+ *   - The workspace is gemm_shard_workspace_size's; the products use its status word
+ *     alone. The norm and the quantisation need none.
+ *   - Graphs, streams and errors as for gemm_ar.
+ */
+
+/*
+ * Residual sum and RMS norm, for rows of H columns:
+ *     h = X + residual,  y = h * (mean(h^2) + eps)^-1/2 * gamma.
+ *   H         a multiple of 8 (of 16 with Q), at most 32768 and the larger of max_N and
+ *             max_K
+ *   X         M x H bf16; M <= max_M, 0 returns GSR_OK with no launch
+ *   residual  M x H bf16, or NULL (0)
+ *   gamma     H bf16, or NULL (1)
+ *   eps       finite, >= 0
+ *   sum       M x H bf16 out: h, or NULL
+ *   Y         M x H bf16 out: y, or NULL
+ *   Q, scale  M x H e4m3 and ceil(H / 128) x M fp32 out: y in 8 bits, or both NULL
+ * One output at least. Everything is fp32 in between; sum, Y and Q are each rounded
+ * once from the unrounded values. sum and Y may each be X or residual itself (not one
+ * another's buffer); otherwise the outputs overlap nothing.
+ */
+gsr_status gemm_shard_rms_norm(const gemm_shard_plan *plan, int64_t M, int64_t H, const void *X,
+                               const void *residual, const void *gamma, float eps, void *sum,
+                               void *Y, void *Q, float *scale, gsr_stream_t stream);
+
+/*
+ * Quantise a matrix of rows x cols bf16 to e4m3.
+ *   block_rows  1: a scale for each row and 128 columns (activations; rows <=
+ *               max_M, scale ceil(cols / 128) x rows); 128: for each block of 128 x
+ *               128 (weights; rows <= max_N, scale ceil(rows / 128) x ceil(cols / 128))
+ *   cols        a multiple of 16, at most max_K
+ *   Q, scale    out, overlapping nothing; rows == 0 returns GSR_OK with no launch
+ */
+gsr_status gemm_shard_quantize(const gemm_shard_plan *plan, int64_t rows, int64_t cols,
+                               int block_rows, const void *X, void *Q, float *scale,
+                               gsr_stream_t stream);
+
+/*
+ * AR on 8-bit operands: Y = sum_r X_r . W_r^T over what the operands stand for.
+ *   X_r, SX_r  host arrays of R device pointers: X_r[r] is M x K_r e4m3, SX_r[r] its
+ *              row scales, ceil(K_r / 128) x M
+ *   W_r, SW_r  W_r[r] is N x K_r e4m3, SW_r[r] its block scales, ceil(N / 128) x
+ *              ceil(K_r / 128)
+ *   Y          M x N bf16
+ * The products of a block of 128 columns are summed in the tensor cores, times the
+ * product of its two scales added up in fp32, blocks ascending, and Y is rounded once.
+ * A value that is not finite reaches the rows and columns that use it and no other.
+ * The sums' order depends on the shapes alone. Other arguments as gemm_ar.
+ */
+gsr_status gemm_ar_fp8(const gemm_shard_plan *plan, int64_t M, int64_t N, int R,
+                       const int64_t *K_r, const void *const *X_r, const float *const *SX_r,
+                       const void *const *W_r, const float *const *SW_r, void *Y, void *ws,
+                       size_t ws_bytes, gsr_stream_t stream);
+
+/*
+ * AG on 8-bit operands: Y = concat_r(A_r) . W^T over what the operands stand for.
+ *   A_r, SA_r  host arrays of R device pointers: A_r[r] is M_r x K e4m3, SA_r[r] its
+ *              row scales, ceil(K / 128) x M_r (both ignored when M_r[r] == 0)
+ *   W, SW      N x K e4m3 and its block scales
+ * Otherwise as gemm_ar_fp8 and gemm_ag.
+ */
+gsr_status gemm_ag_fp8(const gemm_shard_plan *plan, int64_t N, int64_t K, int R,
+                       const int64_t *M_r, const void *const *A_r, const float *const *SA_r,
+                       const void *W, const float *SW, void *Y, void *ws, size_t ws_bytes,
+                       gsr_stream_t stream);
+
 /*
  * Synchronise `stream`, read the workspace status word, clear it and return
  * GSR_OK or GSR_ERR_TIMEOUT (the code of the first wait that ran out is

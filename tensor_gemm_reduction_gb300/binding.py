@@ -57,6 +57,7 @@ EXPORTED = (
     "gemm_shard_pack_gather", "gemm_ar_noalloc_check_status",
     "gemm_routed_workspace_size", "gemm_routed_workspace_init", "gemm_group_route",
     "gemm_grouped", "gemm_grouped_gated", "gemm_group_combine", "gemm_ar_lora",
+    "gemm_shard_rms_norm", "gemm_shard_quantize", "gemm_ar_fp8", "gemm_ag_fp8",
 )
 
 
@@ -123,6 +124,11 @@ def load_library() -> ctypes.CDLL:
     lib.gemm_group_combine.argtypes = [vp, i64, i32, i64, i64, vp, vp, vp, vp, vp, vp]
     lib.gemm_ar_lora.argtypes = [vp, i64, i64, i32, i64_arr, ptr_arr, ptr_arr, i32, i32, ptr_arr,
                                  vp, vp, vp, vp, vp, sz, vp]
+    lib.gemm_shard_rms_norm.argtypes = [vp, i64, i64, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp]
+    lib.gemm_shard_quantize.argtypes = [vp, i64, i64, i32, vp, vp, vp, vp]
+    lib.gemm_ar_fp8.argtypes = [vp, i64, i64, i32, i64_arr, ptr_arr, ptr_arr, ptr_arr, ptr_arr, vp,
+                                vp, sz, vp]
+    lib.gemm_ag_fp8.argtypes = [vp, i64, i64, i32, i64_arr, ptr_arr, ptr_arr, vp, vp, vp, vp, sz, vp]
     lib.gsr_last_error_string.restype = ctypes.c_char_p
     lib.gemm_shard_describe.argtypes = [vp, i32, i64, i64, i64, i32, i64_arr,
                                         ctypes.POINTER(GsrConfig)]
@@ -682,3 +688,154 @@ def prepare_ar_lora(plan: Plan, X_r, W_r, A_r, B, adapter, Y, ws, scale=None, st
     """gemm_ar_lora on fixed buffers, validated and marshalled once."""
     args, keep = _lora_args(plan, X_r, W_r, A_r, B, adapter, Y, ws, scale)
     return PreparedCall(load_library().gemm_ar_lora, args, keep, stream)
+
+
+# ------------------------------------------------------------ 8-bit projections
+
+_E4M3 = torch.float8_e4m3fn
+SCALE_BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return -(-n // SCALE_BLOCK)
+
+
+def _norm_args(plan, X, gamma, eps, residual, sum, Y, Q, scale):
+    _bf16_2d(X, "X")
+    M, H = X.shape
+    for t, name in ((residual, "residual"), (sum, "sum"), (Y, "Y")):
+        if t is not None:
+            _dense(t, name, _BF16, (M, H))
+    if gamma is not None:
+        _dense(gamma, "gamma", _BF16, (H,))
+    if (Q is None) != (scale is None):
+        raise ValueError("Q and scale come together")
+    if Q is not None:
+        _dense(Q, "Q", _E4M3, (M, H))
+        _dense(scale, "scale", torch.float32, (_blocks(H), M))
+    args = (plan.handle, M, H, _ptr(X), _ptr(residual), _ptr(gamma), float(eps), _ptr(sum), _ptr(Y), _ptr(Q),
+            _ptr(scale))
+    return args, (X, gamma, residual, sum, Y, Q, scale)
+
+
+def gemm_shard_rms_norm(plan: Plan, X: torch.Tensor, gamma: Optional[torch.Tensor], eps: float,
+                        residual: Optional[torch.Tensor] = None, sum: Optional[torch.Tensor] = None,
+                        Y: Optional[torch.Tensor] = None, Q: Optional[torch.Tensor] = None,
+                        scale: Optional[torch.Tensor] = None, stream=None):
+    """h = X + residual; sum = h; Y = h / sqrt(mean(h^2) + eps) * gamma (M x H, bf16), and
+    the same in 8 bits: Q (e4m3) with scale (ceil(H / 128) x M, fp32). Returns (sum, Y, Q,
+    scale); each may be None, not all."""
+    args, _ = _norm_args(plan, X, gamma, eps, residual, sum, Y, Q, scale)
+    _check(load_library().gemm_shard_rms_norm(*args, _stream(stream)))
+    return sum, Y, Q, scale
+
+
+def prepare_rms_norm(plan: Plan, X, gamma, eps, residual=None, sum=None, Y=None, Q=None, scale=None,
+                     stream=None) -> PreparedCall:
+    """gemm_shard_rms_norm on fixed buffers, validated and marshalled once."""
+    args, keep = _norm_args(plan, X, gamma, eps, residual, sum, Y, Q, scale)
+    return PreparedCall(load_library().gemm_shard_rms_norm, args, keep, stream)
+
+
+def _quantize_args(plan, X, Q, scale, block_rows):
+    _bf16_2d(X, "X")
+    rows, cols = X.shape
+    _dense(Q, "Q", _E4M3, (rows, cols))
+    _dense(scale, "scale", torch.float32,
+           (_blocks(cols), rows) if int(block_rows) == 1 else (_blocks(rows), _blocks(cols)))
+    args = (plan.handle, rows, cols, int(block_rows), _ptr(X), _ptr(Q), _ptr(scale))
+    return args, (X, Q, scale)
+
+
+def gemm_shard_quantize(plan: Plan, X: torch.Tensor, Q: torch.Tensor, scale: torch.Tensor,
+                        block_rows: int = 1, stream=None):
+    """X (rows x cols, bf16) in 8 bits: Q (e4m3) with a scale for each row and 128 columns
+    (block_rows 1; scale: ceil(cols / 128) x rows) or for each block of 128 x 128
+    (block_rows 128; scale: ceil(rows / 128) x ceil(cols / 128)). Returns (Q, scale)."""
+    args, _ = _quantize_args(plan, X, Q, scale, block_rows)
+    _check(load_library().gemm_shard_quantize(*args, _stream(stream)))
+    return Q, scale
+
+
+def prepare_quantize(plan: Plan, X, Q, scale, block_rows=1, stream=None) -> PreparedCall:
+    """gemm_shard_quantize on fixed buffers, validated and marshalled once."""
+    args, keep = _quantize_args(plan, X, Q, scale, block_rows)
+    return PreparedCall(load_library().gemm_shard_quantize, args, keep, stream)
+
+
+def _ar_fp8_args(plan, X_r, SX_r, W_r, SW_r, Y, ws):
+    R = len(X_r)
+    if R == 0 or not R == len(SX_r) == len(W_r) == len(SW_r):
+        raise ValueError("X_r, SX_r, W_r and SW_r need the same, non-zero number of shards")
+    _bf16_2d(Y, "Y")
+    M, N = Y.shape
+    K_r = []
+    for r in range(R):
+        _dense(X_r[r], f"X_r[{r}]", _E4M3, (M, None))
+        k = X_r[r].shape[1]
+        _dense(SX_r[r], f"SX_r[{r}]", torch.float32, (_blocks(k), M))
+        _dense(W_r[r], f"W_r[{r}]", _E4M3, (N, k))
+        _dense(SW_r[r], f"SW_r[{r}]", torch.float32, (_blocks(N), _blocks(k)))
+        K_r.append(k)
+    k, ka = _i64s(K_r)
+    xp, xa = _ptrs(X_r)
+    sxp, sxa = _ptrs(SX_r)
+    wp, wa = _ptrs(W_r)
+    swp, swa = _ptrs(SW_r)
+    wsp, wsn = _ws(ws)
+    args = (plan.handle, M, N, R, k, xp, sxp, wp, swp, _ptr(Y), wsp, wsn)
+    return args, (ka, xa, sxa, wa, swa, X_r, SX_r, W_r, SW_r, Y, ws)
+
+
+def gemm_ar_fp8(plan: Plan, X_r: Sequence[torch.Tensor], SX_r: Sequence[torch.Tensor],
+                W_r: Sequence[torch.Tensor], SW_r: Sequence[torch.Tensor], Y: torch.Tensor,
+                ws: torch.Tensor, stream=None) -> torch.Tensor:
+    """Y = sum_r X_r @ W_r.T over what 8-bit operands stand for (X_r: M x K_r and W_r: N x
+    K_r, e4m3; SX_r: ceil(K_r / 128) x M and SW_r: ceil(N / 128) x ceil(K_r / 128), fp32;
+    Y: M x N, bf16)."""
+    args, _ = _ar_fp8_args(plan, X_r, SX_r, W_r, SW_r, Y, ws)
+    _check(load_library().gemm_ar_fp8(*args, _stream(stream)))
+    return Y
+
+
+def prepare_ar_fp8(plan: Plan, X_r, SX_r, W_r, SW_r, Y, ws, stream=None) -> PreparedCall:
+    """gemm_ar_fp8 on fixed buffers, validated and marshalled once."""
+    args, keep = _ar_fp8_args(plan, X_r, SX_r, W_r, SW_r, Y, ws)
+    return PreparedCall(load_library().gemm_ar_fp8, args, keep, stream)
+
+
+def _ag_fp8_args(plan, A_r, SA_r, W, SW, Y, ws):
+    R = len(A_r)
+    if R == 0 or R != len(SA_r):
+        raise ValueError("A_r and SA_r need the same, non-zero number of shards")
+    _dense(W, "W", _E4M3, dim=2)
+    N, K = W.shape
+    _dense(SW, "SW", torch.float32, (_blocks(N), _blocks(K)))
+    M_r = []
+    for r in range(R):
+        _dense(A_r[r], f"A_r[{r}]", _E4M3, (None, K))
+        m = A_r[r].shape[0]
+        _dense(SA_r[r], f"SA_r[{r}]", torch.float32, (_blocks(K), m))
+        M_r.append(m)
+    _dense(Y, "Y", _BF16, (sum(M_r), N))
+    m, ma = _i64s(M_r)
+    ap, aa = _ptrs([a if a.numel() else None for a in A_r])
+    sp, sa = _ptrs([s if s.numel() else None for s in SA_r])
+    wsp, wsn = _ws(ws)
+    args = (plan.handle, N, K, R, m, ap, sp, _ptr(W), _ptr(SW), _ptr(Y), wsp, wsn)
+    return args, (ma, aa, sa, A_r, SA_r, W, SW, Y, ws)
+
+
+def gemm_ag_fp8(plan: Plan, A_r: Sequence[torch.Tensor], SA_r: Sequence[torch.Tensor], W: torch.Tensor,
+                SW: torch.Tensor, Y: torch.Tensor, ws: torch.Tensor, stream=None) -> torch.Tensor:
+    """Y = cat(A_r) @ W.T over what 8-bit operands stand for (A_r: M_r x K and W: N x K,
+    e4m3; SA_r: ceil(K / 128) x M_r and SW: ceil(N / 128) x ceil(K / 128), fp32)."""
+    args, _ = _ag_fp8_args(plan, A_r, SA_r, W, SW, Y, ws)
+    _check(load_library().gemm_ag_fp8(*args, _stream(stream)))
+    return Y
+
+
+def prepare_ag_fp8(plan: Plan, A_r, SA_r, W, SW, Y, ws, stream=None) -> PreparedCall:
+    """gemm_ag_fp8 on fixed buffers, validated and marshalled once."""
+    args, keep = _ag_fp8_args(plan, A_r, SA_r, W, SW, Y, ws)
+    return PreparedCall(load_library().gemm_ag_fp8, args, keep, stream)

@@ -1,0 +1,530 @@
+// gsr_fp8.cu -- products of 8-bit operands with scales per block of 128, for GB300
+// (sm_103a): the K-sharded sum (AR) and the product of gathered row shards (AG).
+//
+//   Y[m, n] = sum_b sx[b, m] * sw[n / 128, b] * sum_{k in b} x[m, k] * w[n, k]
+//
+// over the blocks b of 128 columns of every K-shard, x and w in e4m3. The inner sums
+// run on the tensor cores (tcgen05.mma kind::f8f6f4, fp32), a block in a fresh
+// accumulator; the epilogue warps multiply each block's sums by its scales and add
+// them up in fp32 registers: the scales are any fp32 numbers, so they cannot go into
+// the tensor cores' own block scales (powers of two).
+//
+// So that a scale is one number per thread, the tokens are the MMA's M: a TMEM lane is
+// a token row, and a warp's columns lie in two blocks of weight rows at most. A CTA
+// pair owns a tile of tokens x tile_n weight rows over the whole of K:
+// - kFp8Wide: 256 tokens (128 per CTA) x up to 256, a k-block per ring stage. A CTA's
+//   128 x 256 sums are 128 registers of each of its 256 epilogue threads, and two
+//   accumulators fill the TMEM: while the tensor cores fill one, the other is read.
+// - kFp8Narrow: up to 128 tokens x up to 128, a stream of weights. The pair MMA of 128
+//   rows keeps a CTA's 64 rows twice over in TMEM: lanes 64..127 hold the second half
+//   of the columns. A stage is four k-blocks, each with an accumulator of its own, so
+//   that the hand-over between the roles comes once per stage.
+//
+// A CTA's tokens are `boxes` boxes of box_rows rows, each from one row shard, so that
+// short row shards share a tile.
+//
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (the pair's leader), warps 4 and up
+// epilogue. Every wait is bounded like the other kernels'.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gsr_device.cuh"
+#include "gsr_fp8.h"
+
+namespace gsr {
+namespace {
+
+template <int FORM_>
+struct Cfg {
+  static constexpr int FORM = FORM_, KZ = fp8_kblocks(FORM);
+  static constexpr bool WIDE = FORM == kFp8Wide;
+  static constexpr int kRows = fp8_cta_rows(FORM);          // token rows of a CTA
+  static constexpr int kEpi = WIDE ? 256 : 128;
+  static constexpr int kThreads = 128 + kEpi;
+  // Registers: three warpgroups of kFp8Wide leave 168 a thread, too few for an epilogue
+  // thread's 128 sums, so the first one gives some of its own up (504 = 72 + 2 x 216).
+  static constexpr int kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
+  static_assert(kRoleRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "more registers than the launch's");
+  static constexpr int kCols = fp8_max_tile_n(FORM) / 2;    // columns of an epilogue warp, at most
+  static constexpr int kChunk = WIDE ? 32 : 16;             // read from TMEM at a time
+  // TMEM columns of a k-block's sums, and accumulators (of KZ k-blocks).
+  static constexpr uint32_t kAccCols = WIDE ? 256 : 64;
+  static constexpr uint32_t kAccs = 2;
+  static constexpr uint32_t kTmemCols = kAccs * KZ * kAccCols;
+  static_assert(kTmemCols == 512, "all of the TMEM");
+  // full[16], empty[16], tmem_full[2], tmem_empty[2], drain
+  static constexpr uint32_t kBars = (2 * kFp8MaxRing + 2 * kAccs + 1) * 8;
+  static constexpr uint32_t kBarsOff = kFp8RingBytes;
+  static constexpr uint32_t kMiscOff = kBarsOff + kBars;
+  static constexpr uint32_t kTableOff = (kMiscOff + 16 + 15) / 16 * 16;
+};
+
+// The shards as the epilogue reads them (a cold parameter is a memory access).
+struct Table {
+  const float *sx[kMaxShards], *sw[kMaxShards];
+  int64_t row_begin[kMaxShards];
+  int kb[kMaxShards], rows[kMaxShards], box_begin[kMaxShards + 1];
+};
+
+template <class C>
+constexpr uint32_t smem_bytes() { return 1024 + C::kTableOff + sizeof(Table); }
+static_assert(smem_bytes<Cfg<kFp8Wide>>() <= kSmallSmemLimit, "shared memory");
+
+// The four MMAs of one k-block of 128 e4m3 columns (32 columns, 32 bytes, each), into a
+// fresh accumulator.
+__device__ __forceinline__ void mma4_e4m3_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t"
+      "setp.ne.b32 p, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %5, %9, p;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %2, %6, %9, t;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %3, %7, %9, t;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %4, %8, %9, t;\n\t}" ::"r"(d),
+      "l"(a), "l"(a + 2), "l"(a + 4), "l"(a + 6), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(idesc)
+      : "memory");
+}
+
+// Instruction descriptor for kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B e4m3 (7-9 and
+// 10-12 = 0), both K-major, N >> 3 in 17-22, M >> 4 in 24-28.
+__device__ __forceinline__ uint32_t make_idesc_e4m3(uint32_t mma_m, uint32_t mma_n) {
+  return (1u << 4) | ((mma_n >> 3) << 17) | ((mma_m >> 4) << 24);
+}
+
+// The commits of mma_commit_pair by the one thread that issues.
+__device__ __forceinline__ void commit_pair_here(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(0x3))
+      : "memory");
+}
+
+// Token tile and first weight row of tile `id`: group_m token tiles run before the
+// next weight tile, so that concurrent pairs share both operands in L2.
+__device__ __forceinline__ void place(const Fp8Params& p, int id, int& m, int& n0) {
+  const int span = p.group_m * p.n_tiles;
+  const int sup = id / span, in = id - sup * span;
+  const int gm = min(p.m_tiles - sup * p.group_m, p.group_m);
+  const int col = in / gm;
+  m = sup * p.group_m + in - col * gm;
+  n0 = col * p.tile_n;
+}
+
+// Row shard and first row in it of box `b` of the call (past the last one: a row that
+// no shard has).
+__device__ __forceinline__ void find_box(const Fp8Params& p, const int* box_begin, int b, int& shard, int& row) {
+  shard = p.pad_shard;
+  row = 1 << 30;
+  for (int r = 0; r < p.m_shards; ++r)
+    if (b >= box_begin[r] && b < box_begin[r + 1]) {
+      shard = r;
+      row = (b - box_begin[r]) * p.box_rows;
+    }
+}
+
+template <class C>
+__device__ void produce(const Fp8Params& p, const Table& table, uint32_t base, uint32_t rank, const Ctl& ctl) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * kFp8MaxRing;
+  const uint32_t lead0 = map_shared_to_rank(full0, 0);
+  const uint64_t pol_w = make_l2_policy(p.policy_w), pol_x = make_l2_policy(p.policy_x);
+  const uint32_t w_bytes = p.tile_n / 2 * kScaleBlock, box_bytes = p.box_rows * kScaleBlock;
+  const uint32_t x_bytes = p.boxes * box_bytes;
+  const uint32_t stage_bytes = C::KZ * (w_bytes + x_bytes);
+  const uint32_t ring = p.ring;
+  const int begins = p.shard_st_begin[lane <= kMaxShards ? lane : kMaxShards];
+  const int G = static_cast<int>(gridDim.x) >> 1;
+  uint32_t slot = 0, phase = 1, issued = 0;
+  bool ok = true;
+  for (int id = static_cast<int>(blockIdx.x) >> 1; ok && id < p.tiles; id += G) {
+    int m, n0;
+    place(p, id, m, n0);
+    const int w_row = n0 + static_cast<int>(rank) * (p.tile_n / 2);
+    const int box0 = (2 * m + static_cast<int>(rank)) * p.boxes;
+    // Lane i holds box i of this CTA.
+    int shard_x, row_x;
+    find_box(p, table.box_begin, box0 + lane, shard_x, row_x);
+    int shard = 0, begin = 0, end = __shfl_sync(0xffffffffu, begins, 1);
+    for (int st = 0; st < p.stages_per_tile; ++st) {
+      ok = wait_bounded(empty0 + 8 * slot, phase, ctl, (kRoleProducer << 8) | 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      while (end <= st) {
+        begin = end;
+        end = __shfl_sync(0xffffffffu, begins, ++shard + 1);
+      }
+      const int kb = (st - begin) * C::KZ;
+      const uint32_t lead = lead0 + 8 * slot, sw = base + slot * stage_bytes, sx = sw + C::KZ * w_bytes;
+      if (lane == 0) {
+        if (rank == 0) arm(full0 + 8 * slot, 2 * stage_bytes);
+        if (p.whole_boxes) {
+          copy_3d(sw, &p.tmap_w[shard], lead, 0, w_row, kb, pol_w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < C::KZ; ++j)
+            copy_2d(sw + j * w_bytes, &p.tmap_w[shard], lead, (kb + j) * kScaleBlock, w_row, pol_w);
+        }
+      }
+      __syncwarp();
+      if (lane < p.boxes) {
+        const CUtensorMap* map = &p.tmap_x[p.ag ? shard_x : shard];
+        const uint32_t dst = sx + lane * box_bytes;
+        if (p.whole_boxes && p.boxes == 1) {
+          copy_3d(dst, map, lead, 0, row_x, kb, pol_x);
+        } else {
+#pragma unroll
+          for (int j = 0; j < C::KZ; ++j)
+            if (p.whole_boxes)
+              copy_3d(dst + j * x_bytes, map, lead, 0, row_x, kb + j, pol_x);
+            else
+              copy_2d(dst + j * x_bytes, map, lead, (kb + j) * kScaleBlock, row_x, pol_x);
+        }
+      }
+      __syncwarp();
+      ++issued;
+      if (++slot == ring) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+  // Let the copies issued land, and the commits that free their slots, before the shared
+  // memory goes away. (If a role gave up, no commit may come for the last ones: then the
+  // copies complete on the leader's barriers, and the peer waits its limit.)
+  const uint32_t first = issued > ring ? issued - ring : 0;
+  for (uint32_t i = first; i < issued; ++i) {
+    const uint32_t s = i % ring, parity = (i / ring) & 1u;
+    if (rank == 0) wait_drain(full0 + 8 * s, parity, 100000000ull);
+    if (ok)
+      ok = __all_sync(0xffffffffu, wait_bounded(empty0 + 8 * s, parity, ctl, (kRoleProducer << 8) | 2));
+    else if (rank != 0)
+      wait_drain(empty0 + 8 * s, parity, 100000000ull);
+  }
+}
+
+// The pair's MMAs (rank 0).
+template <class C>
+__device__ void multiply(const Fp8Params& p, uint32_t base, uint32_t tmem, const Ctl& ctl) {
+  const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * kFp8MaxRing;
+  const uint32_t tfull0 = empty0 + 8 * kFp8MaxRing, tempty0 = tfull0 + 8 * C::kAccs, drain = tempty0 + 8 * C::kAccs;
+  const uint32_t w_bytes = p.tile_n / 2 * kScaleBlock, x_bytes = p.boxes * p.box_rows * kScaleBlock;
+  const uint32_t stage_bytes = C::KZ * (w_bytes + x_bytes), ring = p.ring;
+  const uint32_t idesc = make_idesc_e4m3(2 * C::kRows, p.tile_n);
+  const int G = static_cast<int>(gridDim.x) >> 1;
+  uint32_t slot = 0, phase = 0, acc = 0, acc_phase = 1;
+  bool ok = true, issued = false;
+  for (int id = static_cast<int>(blockIdx.x) >> 1; ok && id < p.tiles; id += G) {
+    for (int st = 0; st < p.stages_per_tile; ++st) {
+      ok = wait_bounded(tempty0 + 8 * acc, acc_phase, ctl, (kRoleMma << 8) | 1) &&
+           wait_bounded(full0 + 8 * slot, phase, ctl, (kRoleMma << 8) | 2);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t sw = base + slot * stage_bytes, sx = sw + C::KZ * w_bytes;
+      if (elected()) {
+#pragma unroll
+        for (int j = 0; j < C::KZ; ++j)
+          mma4_e4m3_pair(tmem + (acc * C::KZ + j) * C::kAccCols, smem_desc_sw128(sx + j * x_bytes),
+                         smem_desc_sw128(sw + j * w_bytes), idesc);
+        commit_pair_here(tfull0 + 8 * acc);
+        commit_pair_here(empty0 + 8 * slot);
+      }
+      __syncwarp();
+      issued = true;
+      if (++slot == ring) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      if (++acc == C::kAccs) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+  // No MMA may be in flight when the accumulators go away, whichever role gave up.
+  if (issued) {
+    mma_commit_pair(drain, 0x1);
+    wait_drain(drain, 0, 100000000ull);
+  }
+}
+
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair_of(float a, float b) {
+  f32x2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ float2 both(f32x2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+
+// The scales of the next four k-blocks of the tile's walk over K, of one token row and
+// of the warp's two blocks of weight rows, each loaded when the one four before it has
+// been used. Positions that pad a shard to whole stages have scale 0 (their sums are 0).
+template <int KZ>
+struct Scales {
+  float x[4], w0[4], w1[4];
+  int shard, kb, row, nb0, nb1;
+  int64_t stride;   // rows of the token shard
+  const float* ag_x;
+  bool live;
+  __device__ __forceinline__ void load(const Fp8Params& p, const Table& t, int i) {
+    x[i] = w0[i] = w1[i] = 0.f;
+    if (shard >= p.k_shards) return;
+    const int n = t.kb[shard];
+    if (kb < n) {
+      if (live) x[i] = (p.ag ? ag_x : t.sx[shard])[kb * stride + row];
+      const float* w = t.sw[shard] + kb;
+      w0[i] = w[static_cast<int64_t>(nb0) * n];
+      w1[i] = w[static_cast<int64_t>(nb1) * n];
+    }
+    if (++kb >= (n + KZ - 1) / KZ * KZ) {
+      kb = 0;
+      ++shard;
+    }
+  }
+};
+
+// wait_bounded without its call, across which the epilogue's registers would be saved.
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, const Ctl& c, uint32_t site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns(), limit = c.timeout_ns * (site >> 8);
+  while (!mbar_try_wait(bar, parity)) {
+    if (*c.abort) return false;
+    if (global_timer_ns() - t0 > limit) {
+      *c.abort = 1;
+      atomicCAS(c.status, 0u, kStatusTimeout | site);
+      return false;
+    }
+  }
+  return true;
+}
+
+template <class C>
+__device__ void finish(const Fp8Params& p, const Table& table, uint32_t base, uint32_t tmem, uint32_t rank,
+                       const Ctl& ctl) {
+  const uint32_t tfull0 = base + C::kBarsOff + 16 * kFp8MaxRing, tempty0 = tfull0 + 8 * C::kAccs;
+  const uint32_t lead_tempty = map_shared_to_rank(tempty0, 0);
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const int warp = static_cast<int>(threadIdx.x) >> 5;
+  const int quad = warp & 3;                        // TMEM lanes this warp may read
+  const int half = C::WIDE ? (warp - 4) >> 2 : quad >> 1;   // of the tile's columns
+  const int in_cta = C::WIDE ? quad * 32 + lane : (quad & 1) * 32 + lane;   // token row of the CTA
+  const int cols = p.tile_n / 2;
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (C::WIDE ? half * cols : 0);
+  const int G = static_cast<int>(gridDim.x) >> 1;
+  uint32_t acc = 0, acc_phase = 0;
+  bool ok = true;
+  for (int id = static_cast<int>(blockIdx.x) >> 1; ok && id < p.tiles; id += G) {
+    int m, n0;
+    place(p, id, m, n0);
+    const int col0 = n0 + half * cols;
+    // This thread's row: its box, the box's shard and row.
+    const int box = in_cta / p.box_rows, in_box = in_cta - box * p.box_rows;
+    int shard, row;
+    find_box(p, table.box_begin, (2 * m + static_cast<int>(rank)) * p.boxes + box, shard, row);
+    row += in_box;
+    const bool live = box < p.boxes && row < table.rows[shard];
+    Scales<C::KZ> scales;
+    scales.shard = scales.kb = 0;
+    scales.row = row;
+    scales.nb0 = min(col0, p.N - 1) / kScaleBlock;
+    scales.nb1 = min(scales.nb0 + 1, (p.N - 1) / kScaleBlock);
+    scales.stride = table.rows[shard];
+    scales.ag_x = table.sx[shard];
+    scales.live = live;
+    const int split = (scales.nb0 + 1) * kScaleBlock - col0;   // columns before the second block
+    f32x2 sum[C::kCols / 2];
+#pragma unroll
+    for (int i = 0; i < C::kCols / 2; ++i) sum[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scales.load(p, table, i);
+    for (int st = 0; ok && st < p.stages_per_tile;) {
+#pragma unroll
+      for (int u = 0; u < 4 / C::KZ; ++u) {
+        if (st >= p.stages_per_tile) break;
+        ok = wait_here(tfull0 + 8 * acc, acc_phase, ctl, (kRoleEpilogue << 8) | 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int j = 0; j < C::KZ; ++j) {
+          const int i = u * C::KZ + j;
+          const float s0 = scales.x[i] * scales.w0[i], s1 = scales.x[i] * scales.w1[i];
+          scales.load(p, table, i);
+          const uint32_t at = taddr + (acc * C::KZ + j) * C::kAccCols;
+#pragma unroll
+          for (int c = 0; c < C::kCols; c += C::kChunk) {
+            if (c < cols) {
+              const float s = c < split ? s0 : s1;
+              const f32x2 ss = pair_of(s, s);
+              uint32_t v[C::kChunk];
+              if constexpr (C::kChunk == 32) {
+                tmem_ld_32cols(at + c, v);
+                tmem_ld_wait(v);
+              } else {
+                tmem_ld_16cols_wait(at + c, v);
+              }
+#pragma unroll
+              for (int e = 0; e < C::kChunk; e += 2)
+                sum[(c + e) / 2] = fma2(pair_of(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), ss, sum[(c + e) / 2]);
+            }
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) sign_pair(lead_tempty + 8 * acc);
+        ++st;
+        if (++acc == C::kAccs) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) break;
+    if (live) {
+      uint16_t* y = p.y + static_cast<size_t>(table.row_begin[shard] + row) * p.N + col0;
+#pragma unroll
+      for (int c = 0; c < C::kCols; c += 8)
+        if (c < cols && col0 + c < p.N) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = both(sum[c / 2 + e]);
+            w[e] = pack_bf16x2(__float_as_uint(f.x), __float_as_uint(f.y));
+          }
+          *reinterpret_cast<uint4*>(y + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1) gsr_fp8_kernel(const __grid_constant__ Fp8Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
+  Table& table = *reinterpret_cast<Table*>(base_ptr + C::kTableOff);
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+  const uint32_t rank = cluster_rank();
+  const uint32_t bars = base + C::kBarsOff;
+  if (warp == 0) {
+    if (lane < p.k_shards) fetch_descriptor(&p.tmap_w[lane]);
+    if (lane < (p.ag ? p.m_shards : p.k_shards)) fetch_descriptor(&p.tmap_x[lane]);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (uint32_t i = 0; i < kFp8MaxRing; ++i) {
+        mbar_init(bars + 8 * i, 1);                    // full: the leader's expect_tx + the pair's bytes
+        mbar_init(bars + 8 * (kFp8MaxRing + i), 1);    // empty: the MMAs' commit
+      }
+      for (uint32_t i = 0; i < C::kAccs; ++i) {
+        mbar_init(bars + 16 * kFp8MaxRing + 8 * i, 1);                             // sums ready
+        mbar_init(bars + 16 * kFp8MaxRing + 8 * (C::kAccs + i), 2 * C::kEpi / 32);   // read by the pair's warps
+      }
+      mbar_init(bars + 16 * kFp8MaxRing + 16 * C::kAccs, 1);
+      *abort_flag = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish_pair();
+  } else if (warp == 2) {
+    if (lane < kMaxShards) {
+      table.sx[lane] = p.sx[lane];
+      table.sw[lane] = p.sw[lane];
+      table.row_begin[lane] = p.shard_row_begin[lane];
+      table.kb[lane] = p.shard_kb[lane];
+      table.rows[lane] = p.shard_rows[lane];
+    }
+    if (lane <= kMaxShards) table.box_begin[lane] = p.box_begin[lane];
+  }
+  tc_fence_before_sync();
+  cluster_barrier();
+  tc_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dependency_wait();
+
+  Ctl ctl{abort_flag, p.status, p.timeout_ns};
+  if (warp < 4) {
+    if constexpr (C::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRoleRegs));
+    if (warp == 0)
+      produce<C>(p, table, base, rank, ctl);
+    else if (warp == 1 && rank == 0)
+      multiply<C>(p, base, tmem, ctl);
+  } else {
+    if constexpr (C::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
+    finish<C>(p, table, base, tmem, rank, ctl);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_barrier();   // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, C::kTmemCols);
+  }
+  // After a timed-out wait, the peer may have sent what this CTA stopped waiting for:
+  // the CTA stays until that has surely landed.
+  if (threadIdx.x == 0 && *abort_flag) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 20000ull) __nanosleep(1000);
+  }
+}
+
+template <class C>
+cudaError_t set_limit() {
+  if (C::WIDE) {   // the split of the registers counts on the launch's
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, gsr_fp8_kernel<C>);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs < C::kLaunchRegs) return cudaErrorInvalidKernelImage;
+  }
+  return cudaFuncSetAttribute(gsr_fp8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(smem_bytes<C>()));
+}
+
+template <class C>
+cudaError_t launch_one(const Fp8Params& p, int ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem_bytes<C>();
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gsr_fp8_kernel<C>, p);
+}
+
+}  // namespace
+
+cudaError_t prepare_fp8_kernels() {
+  cudaError_t e = set_limit<Cfg<kFp8Wide>>();
+  if (e == cudaSuccess) e = set_limit<Cfg<kFp8Narrow>>();
+  return e;
+}
+
+cudaError_t launch_fp8(const Fp8Params& p, int form, int ctas, cudaStream_t stream) {
+  return form == kFp8Wide ? launch_one<Cfg<kFp8Wide>>(p, ctas, stream)
+                          : launch_one<Cfg<kFp8Narrow>>(p, ctas, stream);
+}
+
+}  // namespace gsr
