@@ -410,6 +410,8 @@ gsr_status gemm_shard_pack_gather(const gemm_shard_plan *plan, int R, const int6
 #define GSR_MAX_TOPK 128        /* entries of one token                        */
 #define GSR_MAX_RANK 128        /* columns of an adapter                       */
 #define GSR_MAX_ADAPTERS 65536  /* L                                           */
+#define GSR_MAX_LAYER_TOKENS 64    /* T of gemm_expert_layer                   */
+#define GSR_MAX_LAYER_ENTRIES 1024 /* its T * topk                             */
 
 /* Bytes of workspace for every routed call under the plan; 0 for a NULL plan. */
 size_t gemm_routed_workspace_size(const gemm_shard_plan *plan);
@@ -485,6 +487,34 @@ gsr_status gemm_group_combine(const gemm_shard_plan *plan, int64_t T, int topk, 
                               int64_t z_rows, const void *Z, const int32_t *position,
                               const float *weights, const void *base, void *Y,
                               gsr_stream_t stream);
+
+/*
+ * Expert layer of a few tokens: what gemm_group_route, gemm_grouped_gated,
+ * gemm_grouped and gemm_group_combine do together, in two launches:
+ *     Y[t] = base[t] + sum_j weights[t, j] * W_down[e] . h_tj,
+ *     h_tj = silu(G[e] . X[t]) * (U[e] . X[t]),  e = ids[t, j],
+ * G[e] and U[e] the first and the last N rows of W_up[e].
+ *   T, topk   tokens and entries of each: T <= GSR_MAX_LAYER_TOKENS, T * topk <=
+ *             GSR_MAX_LAYER_ENTRIES and max_M; T == 0 returns GSR_OK with no launch
+ *   E, N, K   experts, their inner and the outer width: multiples of 8, N <= max_N, K <=
+ *             max_N and max_K
+ *   ids       device, T x topk integers of id_bytes (4 or 8) bytes; a value outside
+ *             0..E-1 drops the entry, whatever its weight holds. A token may name an
+ *             expert twice.
+ *   weights   device, T x topk fp32
+ *   X, base   device, T x K bf16; base may be NULL (0)
+ *   W_up      device, E x 2N x K bf16; W_down: E x K x N bf16
+ *   Y         device, T x K bf16; may be base or X
+ * The products accumulate in fp32, h is rounded to bf16 between them, the weighted sum is
+ * fp32 (experts ascending, and the entries of one expert in order, in parts of k whose
+ * number depends on the shapes) and Y is rounded once. Only the weights of named experts
+ * are read.
+ */
+gsr_status gemm_expert_layer(const gemm_shard_plan *plan, int64_t T, int topk, int E, int64_t N,
+                             int64_t K, const void *ids, int id_bytes, const float *weights,
+                             const void *X, const void *W_up, const void *W_down,
+                             const void *base, void *Y, void *ws, size_t ws_bytes,
+                             gsr_stream_t stream);
 
 /*
  * AR with low-rank adapters: gemm_ar's sum plus each row's own adapter,

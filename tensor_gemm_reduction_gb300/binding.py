@@ -58,6 +58,7 @@ EXPORTED = (
     "gemm_routed_workspace_size", "gemm_routed_workspace_init", "gemm_group_route",
     "gemm_grouped", "gemm_grouped_gated", "gemm_group_combine", "gemm_ar_lora",
     "gemm_shard_rms_norm", "gemm_shard_quantize", "gemm_ar_fp8", "gemm_ag_fp8",
+    "gemm_expert_layer",
 )
 
 
@@ -129,6 +130,7 @@ def load_library() -> ctypes.CDLL:
     lib.gemm_ar_fp8.argtypes = [vp, i64, i64, i32, i64_arr, ptr_arr, ptr_arr, ptr_arr, ptr_arr, vp,
                                 vp, sz, vp]
     lib.gemm_ag_fp8.argtypes = [vp, i64, i64, i32, i64_arr, ptr_arr, ptr_arr, vp, vp, vp, vp, sz, vp]
+    lib.gemm_expert_layer.argtypes = [vp, i64, i32, i32, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.gsr_last_error_string.restype = ctypes.c_char_p
     lib.gemm_shard_describe.argtypes = [vp, i32, i64, i64, i64, i32, i64_arr,
                                         ctypes.POINTER(GsrConfig)]
@@ -653,6 +655,46 @@ def prepare_group_combine(plan: Plan, Z, position, weights, Y, base=None, stream
     """gemm_group_combine on fixed buffers, validated and marshalled once."""
     args, keep = _combine_args(plan, Z, position, weights, Y, base)
     return PreparedCall(load_library().gemm_group_combine, args, keep, stream)
+
+
+def _layer_args(plan, X, ids, weights, W_up, W_down, Y, ws, base):
+    _bf16_2d(X, "X")
+    T, K = X.shape
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be int32 or int64")
+    _dense(ids, "ids", ids.dtype, (T, None))
+    topk = ids.shape[1]
+    _dense(weights, "weights", torch.float32, (T, topk))
+    _dense(W_up, "W_up", _BF16, (None, None, K))
+    E, wide, _ = W_up.shape
+    if wide % 2:
+        raise ValueError("W_up must hold as many gate as up rows")
+    N = wide // 2
+    _dense(W_down, "W_down", _BF16, (E, K, N))
+    _dense(Y, "Y", _BF16, (T, K))
+    if base is not None:
+        _dense(base, "base", _BF16, (T, K))
+    wsp, wsn = _ws(ws)
+    args = (plan.handle, T, topk, E, N, K, _ptr(ids), ids.element_size(), _ptr(weights), _ptr(X), _ptr(W_up),
+            _ptr(W_down), _ptr(base), _ptr(Y), wsp, wsn)
+    return args, (X, ids, weights, W_up, W_down, Y, ws, base)
+
+
+def gemm_expert_layer(plan: Plan, X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W_up: torch.Tensor,
+                      W_down: torch.Tensor, Y: torch.Tensor, ws: torch.Tensor,
+                      base: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y[t] = base[t] + sum_j weights[t, j] * W_down[e] @ (silu(W_up[e, :N] @ X[t]) * (W_up[e, N:] @
+    X[t])), e = ids[t, j] (int32 or int64; outside 0..E-1: dropped), for up to 64 tokens (W_up:
+    E x 2N x K, W_down: E x K x N, weights: fp32; the routed workspace)."""
+    args, _ = _layer_args(plan, X, ids, weights, W_up, W_down, Y, ws, base)
+    _check(load_library().gemm_expert_layer(*args, _stream(stream)))
+    return Y
+
+
+def prepare_expert_layer(plan: Plan, X, ids, weights, W_up, W_down, Y, ws, base=None, stream=None) -> PreparedCall:
+    """gemm_expert_layer on fixed buffers, validated and marshalled once."""
+    args, keep = _layer_args(plan, X, ids, weights, W_up, W_down, Y, ws, base)
+    return PreparedCall(load_library().gemm_expert_layer, args, keep, stream)
 
 
 def _lora_args(plan, X_r, W_r, A_r, B, adapter, Y, ws, scale):

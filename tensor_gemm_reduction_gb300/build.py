@@ -26,10 +26,10 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libgsr.so")
 SOURCES = ["gsr_kernel.cu", "gsr_small.cu", "gsr_pack.cu", "gsr_api.cu", "gsr_routed.cu",
            "gsr_lowrank.cu", "gsr_route.cu", "gsr_routed_api.cu", "gsr_fp8.cu", "gsr_quant.cu",
-           "gsr_fp8_api.cu"]
+           "gsr_fp8_api.cu", "gsr_layer.cu"]
 HEADERS = [os.path.join(CSRC, "gsr_params.h"), os.path.join(CSRC, "gsr_device.cuh"),
            os.path.join(CSRC, "gsr_host.h"), os.path.join(CSRC, "gsr_routed.h"),
-           os.path.join(CSRC, "gsr_fp8.h"),
+           os.path.join(CSRC, "gsr_fp8.h"), os.path.join(CSRC, "gsr_layer.h"),
            os.path.join(INCLUDE, "gsr.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -10,6 +10,7 @@
 
 #include "gsr.h"
 #include "gsr_host.h"
+#include "gsr_layer.h"
 #include "gsr_routed.h"
 
 using gsr::aligned16;
@@ -47,10 +48,14 @@ int64_t max_lists(const gemm_shard_plan* P) { return P->max_M / 128 + 2; }
 size_t list_bytes(const gemm_shard_plan* P) {
   return round256(static_cast<size_t>(max_lists(P)) * gsr::kAdapterListStride * sizeof(int32_t));
 }
+// The expert layer's rows between its products.
+size_t layer_bytes(const gemm_shard_plan* P) {
+  return round256(static_cast<size_t>(std::min<int64_t>(P->max_M, gsr::kLayerEntries)) * P->max_N * 2);
+}
 constexpr size_t kPartialsAt = gsr::kWsHeader + gsr::kRoutedCounterBytes;
 
 size_t workspace_bytes(const gemm_shard_plan* P) {
-  return kPartialsAt + partial_bytes(P) + low_bytes(P) + list_bytes(P);
+  return kPartialsAt + partial_bytes(P) + low_bytes(P) + list_bytes(P) + layer_bytes(P);
 }
 
 gsr_status check_routed_ws(const gemm_shard_plan* P, const void* ws, size_t ws_bytes) {
@@ -337,6 +342,64 @@ gsr_status gemm_group_combine(const gemm_shard_plan* P, int64_t T, int topk, int
   DeviceScope scope(P->device);
   if (scope.err != cudaSuccess) return cuda_fail(scope.err, "selecting the plan's device");
   cudaError_t e = gsr::launch_combine(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+  return ok();
+}
+
+gsr_status gemm_expert_layer(const gemm_shard_plan* P, int64_t T, int topk, int E, int64_t N, int64_t K,
+                             const void* ids, int id_bytes, const float* weights, const void* X, const void* W_up,
+                             const void* W_down, const void* base, void* Y, void* ws, size_t ws_bytes,
+                             gsr_stream_t stream) {
+  gsr_status s = check_plan(P);
+  if (s) return s;
+  if (E < 1 || E > gsr::kMaxGroups)
+    return fail(GSR_ERR_INVALID_VALUE, "E=%d outside 1..%d", E, gsr::kMaxGroups);
+  if (topk < 1 || topk > gsr::kMaxTopk)
+    return fail(GSR_ERR_INVALID_VALUE, "topk=%d outside 1..%d", topk, gsr::kMaxTopk);
+  if (T < 0 || T > gsr::kLayerTokens || T * topk > gsr::kLayerEntries || T * topk > P->max_M)
+    return fail(GSR_ERR_INVALID_VALUE, "T=%lld outside 0..%d, or T * topk above %d or the plan's max_M=%lld",
+                (long long)T, gsr::kLayerTokens, gsr::kLayerEntries, (long long)P->max_M);
+  if (N < 8 || N % 8 || N > P->max_N || N > INT32_MAX / 2048)
+    return fail(GSR_ERR_INVALID_VALUE, "N=%lld must be a positive multiple of 8, at most the plan's max_N=%lld",
+                (long long)N, (long long)P->max_N);
+  if (K < 8 || K % 8 || K > P->max_K || K > P->max_N || K > INT32_MAX / 2048)
+    return fail(GSR_ERR_INVALID_VALUE, "K=%lld must be a positive multiple of 8, at most the plan's max_K=%lld and max_N=%lld",
+                (long long)K, (long long)P->max_K, (long long)P->max_N);
+  if (id_bytes != 4 && id_bytes != 8)
+    return fail(GSR_ERR_INVALID_VALUE, "id_bytes must be 4 or 8 (got %d)", id_bytes);
+  if (T > 0 && (!ids || !weights || !X || !Y))
+    return fail(GSR_ERR_INVALID_VALUE, "ids, weights, X and Y must not be NULL");
+  if (!aligned_to(ids, id_bytes) || !aligned_to(weights, 4))
+    return fail(GSR_ERR_INVALID_VALUE, "ids and weights must be aligned to their elements");
+  if (!W_up || !W_down || !aligned16(W_up) || !aligned16(W_down))
+    return fail(GSR_ERR_INVALID_VALUE, "W_up and W_down must be non-NULL and 16-byte aligned");
+  if (!aligned16(X) || !aligned16(base) || !aligned16(Y))
+    return fail(GSR_ERR_INVALID_VALUE, "X, base and Y must be 16-byte aligned");
+  s = check_routed_ws(P, ws, ws_bytes);
+  if (s) return s;
+  if (T == 0) return ok();
+  if (gsr::log_config_enabled())
+    std::fprintf(stderr, "gsr: expert_layer T=%lld topk=%d E=%d N=%lld K=%lld kernel=layer\n", (long long)T, topk, E,
+                 (long long)N, (long long)K);
+  if (P->device < 0) return fail(GSR_ERR_UNSUPPORTED, "host plan: arguments are valid, nothing launched");
+  gsr::LayerParams p = {};
+  p.ids = ids;
+  p.weights = weights;
+  p.x = static_cast<const uint16_t*>(X);
+  p.up = static_cast<const uint16_t*>(W_up);
+  p.down = static_cast<const uint16_t*>(W_down);
+  p.base = static_cast<const uint16_t*>(base);
+  p.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + workspace_bytes(P) - layer_bytes(P));
+  p.y = static_cast<uint16_t*>(Y);
+  p.T = static_cast<int>(T);
+  p.topk = topk;
+  p.E = E;
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.wide = id_bytes == 8;
+  DeviceScope scope(P->device);
+  if (scope.err != cudaSuccess) return cuda_fail(scope.err, "selecting the plan's device");
+  cudaError_t e = gsr::launch_layer(p, P->sm_count, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
   return ok();
 }
