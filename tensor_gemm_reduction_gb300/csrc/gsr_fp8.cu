@@ -23,8 +23,9 @@
 // A CTA's tokens are `boxes` boxes of box_rows rows, each from one row shard, so that
 // short row shards share a tile.
 //
-// Roles: warp 0 TMA producer, warp 1 MMA issuer (the pair's leader), warps 4 and up
-// epilogue. Every wait is bounded like the other kernels'.
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (the pair's leader), warp 2 copies the
+// scales into a ring of their own (loaded by the epilogue itself, even four k-blocks
+// ahead, they cost it 0.4 us a k-block), warps 4 and up epilogue. Every wait is bounded like the other kernels'.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,9 +37,9 @@
 namespace gsr {
 namespace {
 
-template <int FORM_>
+template <int FORM_, int TILE_N_>
 struct Cfg {
-  static constexpr int FORM = FORM_, KZ = fp8_kblocks(FORM);
+  static constexpr int FORM = FORM_, TILE_N = TILE_N_, KZ = fp8_kblocks(FORM);
   static constexpr bool WIDE = FORM == kFp8Wide;
   static constexpr int kRows = fp8_cta_rows(FORM);          // token rows of a CTA
   static constexpr int kEpi = WIDE ? 256 : 128;
@@ -47,20 +48,30 @@ struct Cfg {
   // thread's 128 sums, so the first one gives some of its own up (504 = 72 + 2 x 216).
   static constexpr int kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
   static_assert(kRoleRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "more registers than the launch's");
-  static constexpr int kCols = fp8_max_tile_n(FORM) / 2;    // columns of an epilogue warp, at most
-  static constexpr int kChunk = WIDE ? 32 : 16;             // read from TMEM at a time
+  static constexpr int kCols = TILE_N / 2;                  // columns of an epilogue warp
+  // A stage's sums are read from TMEM in units, one of 32 columns of the stage's k-block or
+  // a k-block's each, the next one while one is added up.
+  static constexpr int kUnit = WIDE ? 32 : kCols, kUnits = WIDE ? kCols / 32 : KZ;
   // TMEM columns of a k-block's sums, and accumulators (of KZ k-blocks).
   static constexpr uint32_t kAccCols = WIDE ? 256 : 64;
   static constexpr uint32_t kAccs = 2;
   static constexpr uint32_t kTmemCols = kAccs * KZ * kAccCols;
   static_assert(kTmemCols == 512, "all of the TMEM");
-  // full[16], empty[16], tmem_full[2], tmem_empty[2], drain
-  static constexpr uint32_t kBars = (2 * kFp8MaxRing + 2 * kAccs + 1) * 8;
-  static constexpr uint32_t kBarsOff = kFp8RingBytes;
+  // full[16], empty[16], tmem_full[2], tmem_empty[2], drain, scales_full[4], scales_empty[4]
+  static constexpr uint32_t kScaleBarsOff = (2 * kFp8MaxRing + 2 * kAccs + 1) * 8;
+  static constexpr uint32_t kBars = kScaleBarsOff + 2 * kFp8ScaleRing * 8;
+  static constexpr uint32_t kStagingOff = fp8_ring_bytes(FORM);
+  static constexpr uint32_t kBarsOff = kStagingOff + fp8_staging_bytes(FORM);
   static constexpr uint32_t kMiscOff = kBarsOff + kBars;
   static constexpr uint32_t kTableOff = (kMiscOff + 16 + 15) / 16 * 16;
 };
 
+// The scales of four k-blocks: of the CTA's token rows and of the blocks of weight rows
+// that the tile meets (three at most).
+template <class C>
+struct GroupScales {
+  float x[4][C::kRows], w[4][4];
+};
 // The shards as the epilogue reads them (a cold parameter is a memory access).
 struct Table {
   const float *sx[kMaxShards], *sw[kMaxShards];
@@ -69,8 +80,14 @@ struct Table {
 };
 
 template <class C>
-constexpr uint32_t smem_bytes() { return 1024 + C::kTableOff + sizeof(Table); }
-static_assert(smem_bytes<Cfg<kFp8Wide>>() <= kSmallSmemLimit, "shared memory");
+struct Shared {
+  Table table;
+  GroupScales<C> scales[kFp8ScaleRing];
+};
+template <class C>
+constexpr uint32_t smem_bytes() { return 1024 + C::kTableOff + sizeof(Shared<C>); }
+static_assert(smem_bytes<Cfg<kFp8Wide, 256>>() <= kSmallSmemLimit, "shared memory");
+static_assert(smem_bytes<Cfg<kFp8Narrow, 128>>() <= kSmallSmemLimit, "shared memory");
 
 // The four MMAs of one k-block of 128 e4m3 columns (32 columns, 32 bytes, each), into a
 // fresh accumulator.
@@ -129,7 +146,7 @@ __device__ void produce(const Fp8Params& p, const Table& table, uint32_t base, u
   const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * kFp8MaxRing;
   const uint32_t lead0 = map_shared_to_rank(full0, 0);
   const uint64_t pol_w = make_l2_policy(p.policy_w), pol_x = make_l2_policy(p.policy_x);
-  const uint32_t w_bytes = p.tile_n / 2 * kScaleBlock, box_bytes = p.box_rows * kScaleBlock;
+  const uint32_t w_bytes = C::TILE_N / 2 * kScaleBlock, box_bytes = p.box_rows * kScaleBlock;
   const uint32_t x_bytes = p.boxes * box_bytes;
   const uint32_t stage_bytes = C::KZ * (w_bytes + x_bytes);
   const uint32_t ring = p.ring;
@@ -140,7 +157,7 @@ __device__ void produce(const Fp8Params& p, const Table& table, uint32_t base, u
   for (int id = static_cast<int>(blockIdx.x) >> 1; ok && id < p.tiles; id += G) {
     int m, n0;
     place(p, id, m, n0);
-    const int w_row = n0 + static_cast<int>(rank) * (p.tile_n / 2);
+    const int w_row = n0 + static_cast<int>(rank) * (C::TILE_N / 2);
     const int box0 = (2 * m + static_cast<int>(rank)) * p.boxes;
     // Lane i holds box i of this CTA.
     int shard_x, row_x;
@@ -208,9 +225,9 @@ template <class C>
 __device__ void multiply(const Fp8Params& p, uint32_t base, uint32_t tmem, const Ctl& ctl) {
   const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * kFp8MaxRing;
   const uint32_t tfull0 = empty0 + 8 * kFp8MaxRing, tempty0 = tfull0 + 8 * C::kAccs, drain = tempty0 + 8 * C::kAccs;
-  const uint32_t w_bytes = p.tile_n / 2 * kScaleBlock, x_bytes = p.boxes * p.box_rows * kScaleBlock;
+  const uint32_t w_bytes = C::TILE_N / 2 * kScaleBlock, x_bytes = p.boxes * p.box_rows * kScaleBlock;
   const uint32_t stage_bytes = C::KZ * (w_bytes + x_bytes), ring = p.ring;
-  const uint32_t idesc = make_idesc_e4m3(2 * C::kRows, p.tile_n);
+  const uint32_t idesc = make_idesc_e4m3(2 * C::kRows, C::TILE_N);
   const int G = static_cast<int>(gridDim.x) >> 1;
   uint32_t slot = 0, phase = 0, acc = 0, acc_phase = 1;
   bool ok = true, issued = false;
@@ -266,32 +283,80 @@ __device__ __forceinline__ float2 both(f32x2 v) {
   return f;
 }
 
-// The scales of the next four k-blocks of the tile's walk over K, of one token row and
-// of the warp's two blocks of weight rows, each loaded when the one four before it has
-// been used. Positions that pad a shard to whole stages have scale 0 (their sums are 0).
-template <int KZ>
-struct Scales {
-  float x[4], w0[4], w1[4];
-  int shard, kb, row, nb0, nb1;
-  int64_t stride;   // rows of the token shard
-  const float* ag_x;
-  bool live;
-  __device__ __forceinline__ void load(const Fp8Params& p, const Table& t, int i) {
-    x[i] = w0[i] = w1[i] = 0.f;
-    if (shard >= p.k_shards) return;
-    const int n = t.kb[shard];
-    if (kb < n) {
-      if (live) x[i] = (p.ag ? ag_x : t.sx[shard])[kb * stride + row];
-      const float* w = t.sw[shard] + kb;
-      w0[i] = w[static_cast<int64_t>(nb0) * n];
-      w1[i] = w[static_cast<int64_t>(nb1) * n];
+// 4 bytes to shared memory, or zeros; asynchronous.
+__device__ __forceinline__ void copy_4(uint32_t dst, const float* src, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+}
+
+// The scales, by one warp, four k-blocks of the tile's walk over K at a time. Rows that no
+// shard has and positions past the walk's end or that pad a K-shard to whole stages have
+// scale 0 (the sums of the latter are 0).
+template <class C>
+__device__ void copy_scales(const Fp8Params& p, Shared<C>& sh, uint32_t base, uint32_t rank, const Ctl& ctl) {
+  constexpr int kPer = C::kRows / 32;   // rows of a lane
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const uint32_t sfull0 = base + C::kBarsOff + C::kScaleBarsOff, sempty0 = sfull0 + 8 * kFp8ScaleRing;
+  const int G = static_cast<int>(gridDim.x) >> 1;
+  const int last_block = (p.N - 1) / kScaleBlock;
+  uint32_t slot = 0, phase = 1;
+  bool ok = true;
+  for (int id = static_cast<int>(blockIdx.x) >> 1; ok && id < p.tiles; id += G) {
+    int m, n0;
+    place(p, id, m, n0);
+    int shard_x[kPer], row[kPer];
+    bool live[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = lane + 32 * i, box = r / p.box_rows;
+      find_box(p, sh.table.box_begin, (2 * m + static_cast<int>(rank)) * p.boxes + box, shard_x[i], row[i]);
+      row[i] += r - box * p.box_rows;
+      live[i] = box < p.boxes && row[i] < sh.table.rows[shard_x[i]];
     }
-    if (++kb >= (n + KZ - 1) / KZ * KZ) {
-      kb = 0;
-      ++shard;
+    const int block = min(n0 / kScaleBlock + lane, last_block);   // of lanes 0..3
+    int shard = 0, n = sh.table.kb[0], kb = 0;
+    const float *x[kPer], *w = nullptr;
+    int64_t step[kPer];
+    auto enter = [&]() {   // K-shard `shard`
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = sh.table.sx[p.ag ? shard_x[i] : shard] + (live[i] ? row[i] : 0);
+      w = sh.table.sw[shard] + static_cast<int64_t>(block) * n;
+    };
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) step[i] = live[i] ? sh.table.rows[shard_x[i]] : 0;
+    enter();
+    while (shard < p.k_shards) {
+      ok = wait_bounded(sempty0 + 8 * slot, phase, ctl, (kRoleProducer << 8) | 3);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const GroupScales<C>& to = sh.scales[slot];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool real = shard < p.k_shards && kb < n;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) copy_4(smem_u32(&to.x[j][lane + 32 * i]), x[i], real && live[i]);
+        if (lane < 4) copy_4(smem_u32(&to.w[j][lane]), w, real);
+        if (real && kb + 1 < n) {   // (never past the last one's address)
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) x[i] += step[i];
+          ++w;
+        }
+        if (++kb >= (n + C::KZ - 1) / C::KZ * C::KZ && shard < p.k_shards) {
+          kb = 0;
+          if (++shard < p.k_shards) {
+            n = sh.table.kb[shard];
+            enter();
+          }
+        }
+      }
+      sign_copies(sfull0 + 8 * slot);
+      if (++slot == kFp8ScaleRing) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
   }
-};
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
 
 // wait_bounded without its call, across which the epilogue's registers would be saved.
 __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, const Ctl& c, uint32_t site) {
@@ -308,103 +373,180 @@ __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, const C
   return true;
 }
 
+// N columns of the sums at `at`, a multiple of 16 up to 64: issued, and waited for.
+template <int N>
+__device__ __forceinline__ void read_sums(uint32_t at, uint32_t (&v)[N]) {
+  if constexpr (N == 64) {
+    tmem_ld_64cols(at, v);
+  } else if constexpr (N == 16) {
+    tmem_ld_16cols(at, v);
+  } else {
+    tmem_ld_32cols(at, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+    if constexpr (N == 48) tmem_ld_16cols(at + 32, &v[32]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void wait_sums(uint32_t (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  // No use of the registers before the wait.
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]),
+                      "+r"(v[i + 6]), "+r"(v[i + 7]));
+}
+
+__device__ __forceinline__ uint4 pack_8(const f32x2* sum) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = both(sum[e]);
+    w[e] = pack_bf16x2(__float_as_uint(f.x), __float_as_uint(f.y));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A warp's 32 rows x COLS columns through its 4 KB of staging: 64 or 32 columns at a time
+// in the swizzled layout of the copy (128 or 64 bytes a row: 8 lanes' 16-byte stores meet
+// in no bank), then one copy, which leaves out what lies past the shard's rows and N.
+// Stored straight from the registers, a row per lane, a tile took 2.6 us.
+template <int COLS>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t staging, int row, int col, int N, bool rows,
+                                           const f32x2* sum) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  constexpr int kWidth = fp8_store_cols(2 * COLS);
+  const uint32_t at = staging + lane * (2 * kWidth);
+  const int turn = kWidth == 64 ? lane & 7 : lane >> 1 & 3;
+#pragma unroll
+  for (int c = 0; c < COLS; c += kWidth) {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // (lane 0's: the others have none)
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < kWidth; e += 8) {
+      const uint4 w = pack_8(sum + (c + e) / 2);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((e >> 3) ^ turn) << 4)), "r"(w.x),
+                   "r"(w.y), "r"(w.z), "r"(w.w)
+                   : "memory");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0 && rows && col + c < N) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                   "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                   "r"(col + c), "r"(row), "r"(staging)
+                   : "memory");
+    }
+  }
+}
+
 template <class C>
-__device__ void finish(const Fp8Params& p, const Table& table, uint32_t base, uint32_t tmem, uint32_t rank,
+__device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, uint32_t tmem, uint32_t rank,
                        const Ctl& ctl) {
+  const Table& table = sh.table;
   const uint32_t tfull0 = base + C::kBarsOff + 16 * kFp8MaxRing, tempty0 = tfull0 + 8 * C::kAccs;
+  const uint32_t sfull0 = base + C::kBarsOff + C::kScaleBarsOff, sempty0 = sfull0 + 8 * kFp8ScaleRing;
   const uint32_t lead_tempty = map_shared_to_rank(tempty0, 0);
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int warp = static_cast<int>(threadIdx.x) >> 5;
   const int quad = warp & 3;                        // TMEM lanes this warp may read
   const int half = C::WIDE ? (warp - 4) >> 2 : quad >> 1;   // of the tile's columns
-  const int in_cta = C::WIDE ? quad * 32 + lane : (quad & 1) * 32 + lane;   // token row of the CTA
-  const int cols = p.tile_n / 2;
-  const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (C::WIDE ? half * cols : 0);
+  const int row0 = C::WIDE ? quad * 32 : (quad & 1) * 32;   // first token row of the CTA
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (C::WIDE ? half * C::kCols : 0);
   const int G = static_cast<int>(gridDim.x) >> 1;
-  uint32_t acc = 0, acc_phase = 0;
+  uint32_t acc = 0, acc_phase = 0, slot = 0, phase = 0;
   bool ok = true;
   for (int id = static_cast<int>(blockIdx.x) >> 1; ok && id < p.tiles; id += G) {
     int m, n0;
     place(p, id, m, n0);
-    const int col0 = n0 + half * cols;
-    // This thread's row: its box, the box's shard and row.
-    const int box = in_cta / p.box_rows, in_box = in_cta - box * p.box_rows;
-    int shard, row;
-    find_box(p, table.box_begin, (2 * m + static_cast<int>(rank)) * p.boxes + box, shard, row);
-    row += in_box;
-    const bool live = box < p.boxes && row < table.rows[shard];
-    Scales<C::KZ> scales;
-    scales.shard = scales.kb = 0;
-    scales.row = row;
-    scales.nb0 = min(col0, p.N - 1) / kScaleBlock;
-    scales.nb1 = min(scales.nb0 + 1, (p.N - 1) / kScaleBlock);
-    scales.stride = table.rows[shard];
-    scales.ag_x = table.sx[shard];
-    scales.live = live;
-    const int split = (scales.nb0 + 1) * kScaleBlock - col0;   // columns before the second block
+    const int col0 = n0 + half * C::kCols;
+    // The warp's blocks of weight rows among the tile's, and its columns before the second.
+    const int first = col0 / kScaleBlock, b0 = first - n0 / kScaleBlock, b1 = min(b0 + 1, 3);
+    const int split = (first + 1) * kScaleBlock - col0;
     f32x2 sum[C::kCols / 2];
 #pragma unroll
     for (int i = 0; i < C::kCols / 2; ++i) sum[i] = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) scales.load(p, table, i);
     for (int st = 0; ok && st < p.stages_per_tile;) {
+      // Four k-blocks' scales, then their sums.
+      ok = wait_here(sfull0 + 8 * slot, phase, ctl, (kRoleEpilogue << 8) | 2);
+      const GroupScales<C>& scales = sh.scales[slot];
+      float s0[4], s1[4];
 #pragma unroll
-      for (int u = 0; u < 4 / C::KZ; ++u) {
+      for (int j = 0; j < 4; ++j) {
+        const float x = scales.x[j][row0 + lane];
+        s0[j] = x * scales.w[j][b0];
+        s1[j] = x * scales.w[j][b1];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sempty0 + 8 * slot);
+      if (++slot == kFp8ScaleRing) {
+        slot = 0;
+        phase ^= 1u;
+      }
+#pragma unroll
+      for (int i = 0; i < 4 / C::KZ; ++i) {
         if (st >= p.stages_per_tile) break;
-        ok = wait_here(tfull0 + 8 * acc, acc_phase, ctl, (kRoleEpilogue << 8) | 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        ++st;
+        ok = ok && wait_here(tfull0 + 8 * acc, acc_phase, ctl, (kRoleEpilogue << 8) | 1);
+        // Every lane together, also after a wait that ran out.
+        __syncwarp();
         tc_fence_after_sync();
+        const uint32_t at = taddr + acc * C::KZ * C::kAccCols;
+        uint32_t v[2][C::kUnit];
+        read_sums<C::kUnit>(at, v[0]);
 #pragma unroll
-        for (int j = 0; j < C::KZ; ++j) {
-          const int i = u * C::KZ + j;
-          const float s0 = scales.x[i] * scales.w0[i], s1 = scales.x[i] * scales.w1[i];
-          scales.load(p, table, i);
-          const uint32_t at = taddr + (acc * C::KZ + j) * C::kAccCols;
+        for (int u = 0; u < C::kUnits; ++u) {
+          wait_sums<C::kUnit>(v[u & 1]);
+          if (u + 1 < C::kUnits) {
+            read_sums<C::kUnit>(at + (u + 1) * (C::WIDE ? 32 : C::kAccCols), v[(u + 1) & 1]);
+          } else {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) sign_pair(lead_tempty + 8 * acc);
+          }
+          const int j = C::WIDE ? i : u, c0 = C::WIDE ? 32 * u : 0;
 #pragma unroll
-          for (int c = 0; c < C::kCols; c += C::kChunk) {
-            if (c < cols) {
-              const float s = c < split ? s0 : s1;
-              const f32x2 ss = pair_of(s, s);
-              uint32_t v[C::kChunk];
-              if constexpr (C::kChunk == 32) {
-                tmem_ld_32cols(at + c, v);
-                tmem_ld_wait(v);
-              } else {
-                tmem_ld_16cols_wait(at + c, v);
-              }
+          for (int c = 0; c < C::kUnit; c += 16) {
+            const float s = C::kCols == kScaleBlock || c0 + c < split ? s0[j] : s1[j];   // 128 columns are a block
+            const f32x2 ss = pair_of(s, s);
 #pragma unroll
-              for (int e = 0; e < C::kChunk; e += 2)
-                sum[(c + e) / 2] = fma2(pair_of(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), ss, sum[(c + e) / 2]);
+            for (int e = 0; e < 16; e += 2) {
+              f32x2& to = sum[(c0 + c + e) / 2];
+              to = fma2(pair_of(__uint_as_float(v[u & 1][c + e]), __uint_as_float(v[u & 1][c + e + 1])), ss, to);
             }
           }
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) sign_pair(lead_tempty + 8 * acc);
-        ++st;
         if (++acc == C::kAccs) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
     }
     if (!ok) break;
-    if (live) {
+    // The warp's rows: their box, the box's shard and row.
+    if constexpr (C::WIDE) {
+      if (p.tma_store) {
+        const int box = row0 / p.box_rows;
+        int shard, row;
+        find_box(p, table.box_begin, (2 * m + static_cast<int>(rank)) * p.boxes + box, shard, row);
+        row += row0 - box * p.box_rows;
+        store_tile<C::kCols>(&p.tmap_y[shard], base + C::kStagingOff + (warp - 4) * 4096, row, col0, p.N,
+                             box < p.boxes && row < table.rows[shard], sum);
+        continue;
+      }
+    }
+    const int box = (row0 + lane) / p.box_rows;
+    int shard, row;
+    find_box(p, table.box_begin, (2 * m + static_cast<int>(rank)) * p.boxes + box, shard, row);
+    row += row0 + lane - box * p.box_rows;
+    if (box < p.boxes && row < table.rows[shard]) {
       uint16_t* y = p.y + static_cast<size_t>(table.row_begin[shard] + row) * p.N + col0;
 #pragma unroll
       for (int c = 0; c < C::kCols; c += 8)
-        if (c < cols && col0 + c < p.N) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = both(sum[c / 2 + e]);
-            w[e] = pack_bf16x2(__float_as_uint(f.x), __float_as_uint(f.y));
-          }
-          *reinterpret_cast<uint4*>(y + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        if (col0 + c < p.N) *reinterpret_cast<uint4*>(y + c) = pack_8(sum + c / 2);
     }
   }
+  // The last copies have read the staging before the shared memory goes away.
+  if (C::WIDE) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 template <class C>
@@ -415,13 +557,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_fp8_kernel(const __grid_co
   uint8_t* base_ptr = smem_raw + (base - raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
-  Table& table = *reinterpret_cast<Table*>(base_ptr + C::kTableOff);
+  Shared<C>& sh = *reinterpret_cast<Shared<C>*>(base_ptr + C::kTableOff);
+  Table& table = sh.table;
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t bars = base + C::kBarsOff;
   if (warp == 0) {
     if (lane < p.k_shards) fetch_descriptor(&p.tmap_w[lane]);
     if (lane < (p.ag ? p.m_shards : p.k_shards)) fetch_descriptor(&p.tmap_x[lane]);
+    if (C::WIDE && p.tma_store && lane < p.m_shards) fetch_descriptor(&p.tmap_y[lane]);
   } else if (warp == 1) {
     if (lane == 0) {
       for (uint32_t i = 0; i < kFp8MaxRing; ++i) {
@@ -433,6 +577,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_fp8_kernel(const __grid_co
         mbar_init(bars + 16 * kFp8MaxRing + 8 * (C::kAccs + i), 2 * C::kEpi / 32);   // read by the pair's warps
       }
       mbar_init(bars + 16 * kFp8MaxRing + 16 * C::kAccs, 1);
+      for (uint32_t i = 0; i < kFp8ScaleRing; ++i) {
+        mbar_init(bars + C::kScaleBarsOff + 8 * i, 32);                                // each lane's copies
+        mbar_init(bars + C::kScaleBarsOff + 8 * (kFp8ScaleRing + i), C::kEpi / 32);   // read by the warps
+      }
       *abort_flag = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -464,9 +612,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_fp8_kernel(const __grid_co
       produce<C>(p, table, base, rank, ctl);
     else if (warp == 1 && rank == 0)
       multiply<C>(p, base, tmem, ctl);
+    else if (warp == 2)
+      copy_scales<C>(p, sh, base, rank, ctl);
   } else {
     if constexpr (C::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
-    finish<C>(p, table, base, tmem, rank, ctl);
+    finish<C>(p, sh, base, tmem, rank, ctl);
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -514,17 +664,36 @@ cudaError_t launch_one(const Fp8Params& p, int ctas, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, gsr_fp8_kernel<C>, p);
 }
 
-}  // namespace
-
-cudaError_t prepare_fp8_kernels() {
-  cudaError_t e = set_limit<Cfg<kFp8Wide>>();
-  if (e == cudaSuccess) e = set_limit<Cfg<kFp8Narrow>>();
+template <int FORM>
+cudaError_t set_limits() {
+  constexpr int n = fp8_max_tile_n(FORM) / 4;
+  cudaError_t e = set_limit<Cfg<FORM, n>>();
+  if (e == cudaSuccess) e = set_limit<Cfg<FORM, 2 * n>>();
+  if (e == cudaSuccess) e = set_limit<Cfg<FORM, 3 * n>>();
+  if (e == cudaSuccess) e = set_limit<Cfg<FORM, 4 * n>>();
   return e;
 }
 
+template <int FORM>
+cudaError_t launch_form(const Fp8Params& p, int ctas, cudaStream_t stream) {
+  constexpr int n = fp8_max_tile_n(FORM) / 4;
+  switch (p.tile_n) {
+    case n: return launch_one<Cfg<FORM, n>>(p, ctas, stream);
+    case 2 * n: return launch_one<Cfg<FORM, 2 * n>>(p, ctas, stream);
+    case 3 * n: return launch_one<Cfg<FORM, 3 * n>>(p, ctas, stream);
+    default: return launch_one<Cfg<FORM, 4 * n>>(p, ctas, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t prepare_fp8_kernels() {
+  const cudaError_t e = set_limits<kFp8Wide>();
+  return e == cudaSuccess ? set_limits<kFp8Narrow>() : e;
+}
+
 cudaError_t launch_fp8(const Fp8Params& p, int form, int ctas, cudaStream_t stream) {
-  return form == kFp8Wide ? launch_one<Cfg<kFp8Wide>>(p, ctas, stream)
-                          : launch_one<Cfg<kFp8Narrow>>(p, ctas, stream);
+  return form == kFp8Wide ? launch_form<kFp8Wide>(p, ctas, stream) : launch_form<kFp8Narrow>(p, ctas, stream);
 }
 
 }  // namespace gsr

@@ -41,6 +41,8 @@ struct Fp8Params {  // 128-byte aligned through its CUtensorMap members
   // (tile_n / 2) rows; with whole_boxes of a stage's k-blocks of them.
   CUtensorMap tmap_x[kMaxShards];
   CUtensorMap tmap_w[kMaxShards];
+  // The rows of Y of M-shard r, in boxes of fp8_store_cols x 32 rows (wide, with tma_store).
+  CUtensorMap tmap_y[kMaxShards];
   const float* sx[kMaxShards];   // scales of X_r / A_r: k-blocks x rows
   const float* sw[kMaxShards];   // of W_r, or [0]: row blocks x k-blocks
   uint16_t* y;
@@ -57,6 +59,7 @@ struct Fp8Params {  // 128-byte aligned through its CUtensorMap members
   int pad_shard;                    // AG: a shard with rows, read out of range (zeros) past the last box
   int ring;                         // stages of the shared-memory ring
   int whole_boxes;
+  int tma_store;                    // every warp's 32 rows are of one box
   int policy_x, policy_w;
   int stages_per_tile;
   int shard_kb[kMaxShards];         // k-blocks of 128 of K-shard r
@@ -66,22 +69,28 @@ struct Fp8Params {  // 128-byte aligned through its CUtensorMap members
   int64_t shard_row_begin[kMaxShards];  // its first row of Y
 };
 
-// The instances. kFp8Wide: 256 token rows per CTA pair, weight tiles of up to 256, one
-// k-block per stage. kFp8Narrow: up to 128 token rows, weight tiles of up to 128, four
-// k-blocks per stage.
+// The instances. kFp8Wide: 256 token rows per CTA pair, weight tiles of 64, 128, 192 or 256
+// rows, one k-block per stage. kFp8Narrow: up to 128 token rows, weight tiles of 32, 64, 96
+// or 128, four k-blocks per stage.
 enum Fp8Form : int { kFp8Wide = 0, kFp8Narrow = 1 };
 constexpr int fp8_kblocks(int form) { return form == kFp8Wide ? 1 : 4; }
 constexpr int fp8_max_tile_n(int form) { return form == kFp8Wide ? 256 : 128; }
 constexpr int fp8_cta_rows(int form) { return form == kFp8Wide ? 128 : 64; }
 constexpr int kFp8MaxRing = 16;
-// Bytes of the ring, at most, and stages that fit: the MMAs read fp8_cta_rows rows of the
-// tokens from a stage whatever it holds, past the last one into a pad.
-constexpr uint32_t kFp8RingBytes = 228 * 1024 - 4096;
+constexpr int kFp8ScaleRing = 4;      // of the scales, four k-blocks a stage
+// Shared memory of the ring, and of what the epilogue stores from (wide: 4 KB per warp).
+constexpr uint32_t fp8_ring_bytes(int form) { return form == kFp8Wide ? 160 * 1024 : 208 * 1024; }
+constexpr uint32_t fp8_staging_bytes(int form) { return form == kFp8Wide ? 8 * 4096 : 0; }
 constexpr uint32_t fp8_stage_bytes(int form, int tile_n, int token_rows) {
   return fp8_kblocks(form) * kScaleBlock * static_cast<uint32_t>(tile_n / 2 + token_rows);
 }
+// Columns of a copy to Y: a warp's are tile_n / 2.
+__host__ __device__ constexpr int fp8_store_cols(int tile_n) { return tile_n / 2 % 64 == 0 ? 64 : 32; }
+// Stages that fit. The MMAs read fp8_cta_rows rows of the tokens from a stage whatever it
+// holds, in the last one past its end.
 constexpr int fp8_ring(int form, int tile_n, int token_rows) {
-  const uint32_t fit = (kFp8RingBytes - fp8_cta_rows(form) * kScaleBlock) / fp8_stage_bytes(form, tile_n, token_rows);
+  const uint32_t past = kScaleBlock * static_cast<uint32_t>(fp8_cta_rows(form) - token_rows);
+  const uint32_t fit = (fp8_ring_bytes(form) - past) / fp8_stage_bytes(form, tile_n, token_rows);
   return static_cast<int>(fit < kFp8MaxRing ? fit : kFp8MaxRing);
 }
 

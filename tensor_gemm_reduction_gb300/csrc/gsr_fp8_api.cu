@@ -42,6 +42,18 @@ CUresult encode(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// Rows of Y in boxes of `width` (64 or 32) columns x 32 rows.
+CUresult encode_y(CUtensorMap* m, void* ptr, int64_t rows, int64_t cols, int width) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(width), 32};
+  cuuint32_t estr[2] = {1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 int64_t pairs_of(const gemm_shard_plan* P) {
   const int cap = P->opt_max_ctas ? std::min(P->opt_max_ctas, P->sm_count) : P->sm_count;
   return std::max<int64_t>(1, std::min<int64_t>(cap / 2, P->pair_clusters));
@@ -177,6 +189,12 @@ gsr_status run_fp8(const gemm_shard_plan* P, bool ag, int64_t N, int R, const in
     p.sx[r] = SX[r];
     if (rows > 0 && cr == CUDA_SUCCESS) cr = encode(&p.tmap_x[r], X[r], rows, ag ? K_r[0] : K_r[r], s.box_rows, x_kb);
   }
+  // A warp's 32 rows lie in one box: the tile's rows are stored by copies, which leave out
+  // what a shard does not have.
+  p.tma_store = s.form == gsr::kFp8Wide && s.box_rows % 32 == 0;
+  if (p.tma_store)
+    for (int r = 0; r < m_shards && cr == CUDA_SUCCESS; ++r)
+      if (M_r[r] > 0) cr = encode_y(&p.tmap_y[r], p.y + p.shard_row_begin[r] * N, M_r[r], N, gsr::fp8_store_cols(s.tile_n));
   if (cr != CUDA_SUCCESS) return fail(GSR_ERR_CUDA, "encoding the operands' descriptors failed (%d)", (int)cr);
   DeviceScope scope(P->device);
   if (scope.err != cudaSuccess) return cuda_fail(scope.err, "selecting the plan's device");

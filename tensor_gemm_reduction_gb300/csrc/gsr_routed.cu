@@ -66,10 +66,6 @@ __device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool real
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0)
                : "memory");
 }
-// Arrives on `bar` when this thread's copies so far have landed.
-__device__ __forceinline__ void sign_copies(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 // 32 TMEM columns of 16 lanes: v[4 g + e] is column 8 g + 2 (lane % 4) + e % 2 of
 // lane (lane / 4) + 8 (e / 2).
 __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* v) {
