@@ -24,8 +24,9 @@
 // short row shards share a tile.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (the pair's leader), warp 2 copies the
-// scales into a ring of their own (loaded by the epilogue itself, even four k-blocks
-// ahead, they cost it 0.4 us a k-block), warps 4 and up epilogue. Every wait is bounded like the other kernels'.
+// scales ahead into a ring of their own and warp 3 multiplies them (loaded by the epilogue
+// itself, even four k-blocks ahead, they cost it 0.4 us a k-block), warps 4 and up
+// epilogue. Every wait is bounded like the other kernels'.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -39,7 +40,7 @@ namespace {
 
 template <int FORM_, int TILE_N_>
 struct Cfg {
-  static constexpr int FORM = FORM_, TILE_N = TILE_N_, KZ = fp8_kblocks(FORM);
+  static constexpr int FORM = FORM_, TILE_N = TILE_N_, KZ = fp8_kblocks(FORM, TILE_N);
   static constexpr bool WIDE = FORM == kFp8Wide;
   static constexpr int kRows = fp8_cta_rows(FORM);          // token rows of a CTA
   static constexpr int kEpi = WIDE ? 256 : 128;
@@ -49,30 +50,42 @@ struct Cfg {
   static constexpr int kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
   static_assert(kRoleRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "more registers than the launch's");
   static constexpr int kCols = TILE_N / 2;                  // columns of an epilogue warp
-  // A stage's sums are read from TMEM in units, one of 32 columns of the stage's k-block or
-  // a k-block's each, the next one while one is added up.
-  static constexpr int kUnit = WIDE ? 32 : kCols, kUnits = WIDE ? kCols / 32 : KZ;
+  // Blocks of weight rows that a tile meets (its first row is a multiple of TILE_N) and
+  // that a warp's columns do.
+  static constexpr int kBlocks = kScaleBlock % TILE_N == 0 ? 1 : 2;
+  static constexpr bool kOneBlock = kBlocks == 1 || kCols == kScaleBlock;
+  // A k-block's sums are read from TMEM in units of 32 columns or of all, the next one while
+  // one is added up.
+  static constexpr int kUnit = !WIDE ? kCols : TILE_N == 256 ? 16 : 32, kPerBlock = kCols / kUnit, kUnits = KZ * kPerBlock;
   // TMEM columns of a k-block's sums, and accumulators (of KZ k-blocks).
-  static constexpr uint32_t kAccCols = WIDE ? 256 : 64;
+  static constexpr uint32_t kAccCols = 256 / KZ;
   static constexpr uint32_t kAccs = 2;
   static constexpr uint32_t kTmemCols = kAccs * KZ * kAccCols;
   static_assert(kTmemCols == 512, "all of the TMEM");
-  // full[16], empty[16], tmem_full[2], tmem_empty[2], drain, scales_full[4], scales_empty[4]
+  // full[16], empty[16], tmem_full[2], tmem_empty[2], drain; the products of the scales: full,
+  // empty; the scales: full, empty
   static constexpr uint32_t kScaleBarsOff = (2 * kFp8MaxRing + 2 * kAccs + 1) * 8;
-  static constexpr uint32_t kBars = kScaleBarsOff + 2 * kFp8ScaleRing * 8;
-  static constexpr uint32_t kStagingOff = fp8_ring_bytes(FORM);
-  static constexpr uint32_t kBarsOff = kStagingOff + fp8_staging_bytes(FORM);
+  static constexpr uint32_t kRawBarsOff = kScaleBarsOff + 2 * kFp8ScaleRing * 8;
+  static constexpr uint32_t kBars = kRawBarsOff + 2 * kFp8RawRing * 8;
+  static constexpr uint32_t kStagingOff = fp8_ring_bytes(FORM, TILE_N);
+  static constexpr uint32_t kBarsOff = kStagingOff + fp8_staging_bytes(FORM, TILE_N);
   static constexpr uint32_t kMiscOff = kBarsOff + kBars;
   static constexpr uint32_t kTableOff = (kMiscOff + 16 + 15) / 16 * 16;
 };
 
-// The scales of four k-blocks: of the CTA's token rows and of the blocks of weight rows
-// that the tile meets (three at most).
+// The products of the scales of four k-blocks, for each of the CTA's token rows and each
+// block of weight rows of the tile.
 template <class C>
 struct GroupScales {
-  float x[4][C::kRows], w[4][4];
+  float4 s[C::kBlocks][C::kRows];
 };
-// The shards as the epilogue reads them (a cold parameter is a memory access).
+
+template <class C>
+struct RawScales {
+  float x[4][C::kRows], w[4][2];
+};
+
+// The shards as the roles read them (a cold parameter is a memory access).
 struct Table {
   const float *sx[kMaxShards], *sw[kMaxShards];
   int64_t row_begin[kMaxShards];
@@ -83,6 +96,7 @@ template <class C>
 struct Shared {
   Table table;
   GroupScales<C> scales[kFp8ScaleRing];
+  RawScales<C> raw[kFp8RawRing];
 };
 template <class C>
 constexpr uint32_t smem_bytes() { return 1024 + C::kTableOff + sizeof(Shared<C>); }
@@ -110,10 +124,10 @@ __device__ __forceinline__ uint32_t make_idesc_e4m3(uint32_t mma_m, uint32_t mma
 }
 
 // The commits of mma_commit_pair by the one thread that issues.
-__device__ __forceinline__ void commit_pair_here(uint32_t bar) {
+__device__ __forceinline__ void commit_pair_here(uint32_t bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(0x3))
+      "h"(mask)
       : "memory");
 }
 
@@ -146,64 +160,75 @@ __device__ void produce(const Fp8Params& p, const Table& table, uint32_t base, u
   const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * kFp8MaxRing;
   const uint32_t lead0 = map_shared_to_rank(full0, 0);
   const uint64_t pol_w = make_l2_policy(p.policy_w), pol_x = make_l2_policy(p.policy_x);
-  const uint32_t w_bytes = C::TILE_N / 2 * kScaleBlock, box_bytes = p.box_rows * kScaleBlock;
-  const uint32_t x_bytes = p.boxes * box_bytes;
-  const uint32_t stage_bytes = C::KZ * (w_bytes + x_bytes);
-  const uint32_t ring = p.ring;
+  constexpr uint32_t w_bytes = C::TILE_N / 2 * kScaleBlock;
+  const uint32_t box_bytes = p.box_rows * kScaleBlock, x_bytes = p.boxes * box_bytes;
+  const uint32_t stage_bytes = C::KZ * (w_bytes + x_bytes), ring = p.ring;
+  const uint32_t lead = rank == 0 ? 1u : 0u;
   const int begins = p.shard_st_begin[lane <= kMaxShards ? lane : kMaxShards];
   const int G = static_cast<int>(gridDim.x) >> 1;
+  // The usual case in a loop of its own: this loop alone feeds the tensor cores, and every
+  // instruction in it costs.
+  const bool simple = p.boxes == 1 && (C::KZ == 1 || p.whole_boxes);
   uint32_t slot = 0, phase = 1, issued = 0;
   bool ok = true;
   for (int id = static_cast<int>(blockIdx.x) >> 1; ok && id < p.tiles; id += G) {
     int m, n0;
     place(p, id, m, n0);
     const int w_row = n0 + static_cast<int>(rank) * (C::TILE_N / 2);
-    const int box0 = (2 * m + static_cast<int>(rank)) * p.boxes;
     // Lane i holds box i of this CTA.
     int shard_x, row_x;
-    find_box(p, table.box_begin, box0 + lane, shard_x, row_x);
-    int shard = 0, begin = 0, end = __shfl_sync(0xffffffffu, begins, 1);
-    for (int st = 0; st < p.stages_per_tile; ++st) {
-      ok = wait_bounded(empty0 + 8 * slot, phase, ctl, (kRoleProducer << 8) | 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      while (end <= st) {
-        begin = end;
-        end = __shfl_sync(0xffffffffu, begins, ++shard + 1);
-      }
-      const int kb = (st - begin) * C::KZ;
-      const uint32_t lead = lead0 + 8 * slot, sw = base + slot * stage_bytes, sx = sw + C::KZ * w_bytes;
-      if (lane == 0) {
-        if (rank == 0) arm(full0 + 8 * slot, 2 * stage_bytes);
-        if (p.whole_boxes) {
-          copy_3d(sw, &p.tmap_w[shard], lead, 0, w_row, kb, pol_w);
+    find_box(p, table.box_begin, (2 * m + static_cast<int>(rank)) * p.boxes + lane, shard_x, row_x);
+    const int shard_0 = __shfl_sync(0xffffffffu, shard_x, 0), row_0 = __shfl_sync(0xffffffffu, row_x, 0);
+    int begin = 0;
+    for (int shard = 0; ok && shard < p.k_shards; ++shard) {
+      const int end = __shfl_sync(0xffffffffu, begins, shard + 1);
+      const CUtensorMap* map_w = &p.tmap_w[shard];
+      const CUtensorMap* map_x = &p.tmap_x[p.ag ? shard_0 : shard];
+      for (int st = begin; st < end; ++st) {
+        ok = wait_bounded(empty0 + 8 * slot, phase, ctl, (kRoleProducer << 8) | 1);
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int kb = (st - begin) * C::KZ;
+        const uint32_t full = full0 + 8 * slot, pair = lead0 + 8 * slot;
+        const uint32_t sw = base + slot * stage_bytes, sx = sw + C::KZ * w_bytes;
+        if (simple) {
+          if constexpr (C::KZ == 1)
+            stage_copies_pair(lead, full, 2 * stage_bytes, pair, sx, map_x, row_0, sw, map_w, w_row, kb * kScaleBlock,
+                              pol_x, pol_w);
+          else
+            stage_copies_pair_3d(lead, full, 2 * stage_bytes, pair, sx, map_x, row_0, sw, map_w, w_row, kb, pol_x, pol_w);
         } else {
+          if (lane == 0) {
+            if (rank == 0) arm(full, 2 * stage_bytes);
+            if (p.whole_boxes) {
+              copy_3d(sw, map_w, pair, 0, w_row, kb, pol_w);
+            } else {
 #pragma unroll
-          for (int j = 0; j < C::KZ; ++j)
-            copy_2d(sw + j * w_bytes, &p.tmap_w[shard], lead, (kb + j) * kScaleBlock, w_row, pol_w);
+              for (int j = 0; j < C::KZ; ++j)
+                copy_2d(sw + j * w_bytes, map_w, pair, (kb + j) * kScaleBlock, w_row, pol_w);
+            }
+          }
+          __syncwarp();
+          if (lane < p.boxes) {
+            const CUtensorMap* map = &p.tmap_x[p.ag ? shard_x : shard];
+            const uint32_t dst = sx + lane * box_bytes;
+#pragma unroll
+            for (int j = 0; j < C::KZ; ++j)
+              if (p.whole_boxes)
+                copy_3d(dst + j * x_bytes, map, pair, 0, row_x, kb + j, pol_x);
+              else
+                copy_2d(dst + j * x_bytes, map, pair, (kb + j) * kScaleBlock, row_x, pol_x);
+          }
+          __syncwarp();
+        }
+        ++issued;
+        if (++slot == ring) {
+          slot = 0;
+          phase ^= 1u;
         }
       }
-      __syncwarp();
-      if (lane < p.boxes) {
-        const CUtensorMap* map = &p.tmap_x[p.ag ? shard_x : shard];
-        const uint32_t dst = sx + lane * box_bytes;
-        if (p.whole_boxes && p.boxes == 1) {
-          copy_3d(dst, map, lead, 0, row_x, kb, pol_x);
-        } else {
-#pragma unroll
-          for (int j = 0; j < C::KZ; ++j)
-            if (p.whole_boxes)
-              copy_3d(dst + j * x_bytes, map, lead, 0, row_x, kb + j, pol_x);
-            else
-              copy_2d(dst + j * x_bytes, map, lead, (kb + j) * kScaleBlock, row_x, pol_x);
-        }
-      }
-      __syncwarp();
-      ++issued;
-      if (++slot == ring) {
-        slot = 0;
-        phase ^= 1u;
-      }
+      begin = end;
     }
   }
   // Let the copies issued land, and the commits that free their slots, before the shared
@@ -220,7 +245,8 @@ __device__ void produce(const Fp8Params& p, const Table& table, uint32_t base, u
   }
 }
 
-// The pair's MMAs (rank 0).
+// The pair's MMAs (rank 0). What it waits for last, the accumulator, is on
+// the way from the epilogue's last read to the next MMA.
 template <class C>
 __device__ void multiply(const Fp8Params& p, uint32_t base, uint32_t tmem, const Ctl& ctl) {
   const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * kFp8MaxRing;
@@ -233,8 +259,8 @@ __device__ void multiply(const Fp8Params& p, uint32_t base, uint32_t tmem, const
   bool ok = true, issued = false;
   for (int id = static_cast<int>(blockIdx.x) >> 1; ok && id < p.tiles; id += G) {
     for (int st = 0; st < p.stages_per_tile; ++st) {
-      ok = wait_bounded(tempty0 + 8 * acc, acc_phase, ctl, (kRoleMma << 8) | 1) &&
-           wait_bounded(full0 + 8 * slot, phase, ctl, (kRoleMma << 8) | 2);
+      ok = wait_bounded(full0 + 8 * slot, phase, ctl, (kRoleMma << 8) | 2) &&
+           wait_bounded(tempty0 + 8 * acc, acc_phase, ctl, (kRoleMma << 8) | 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after_sync();
@@ -244,8 +270,8 @@ __device__ void multiply(const Fp8Params& p, uint32_t base, uint32_t tmem, const
         for (int j = 0; j < C::KZ; ++j)
           mma4_e4m3_pair(tmem + (acc * C::KZ + j) * C::kAccCols, smem_desc_sw128(sx + j * x_bytes),
                          smem_desc_sw128(sw + j * w_bytes), idesc);
-        commit_pair_here(tfull0 + 8 * acc);
-        commit_pair_here(empty0 + 8 * slot);
+        commit_pair_here(tfull0 + 8 * acc, 0x3);
+        commit_pair_here(empty0 + 8 * slot, 0x3);
       }
       __syncwarp();
       issued = true;
@@ -288,14 +314,14 @@ __device__ __forceinline__ void copy_4(uint32_t dst, const float* src, bool real
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
 }
 
-// The scales, by one warp, four k-blocks of the tile's walk over K at a time. Rows that no
+// The scales as they are, by one warp, four k-blocks of the tile's walk over K at a time. Rows that no
 // shard has and positions past the walk's end or that pad a K-shard to whole stages have
 // scale 0 (the sums of the latter are 0).
 template <class C>
 __device__ void copy_scales(const Fp8Params& p, Shared<C>& sh, uint32_t base, uint32_t rank, const Ctl& ctl) {
   constexpr int kPer = C::kRows / 32;   // rows of a lane
   const int lane = static_cast<int>(threadIdx.x) & 31;
-  const uint32_t sfull0 = base + C::kBarsOff + C::kScaleBarsOff, sempty0 = sfull0 + 8 * kFp8ScaleRing;
+  const uint32_t rfull0 = base + C::kBarsOff + C::kRawBarsOff, rempty0 = rfull0 + 8 * kFp8RawRing;
   const int G = static_cast<int>(gridDim.x) >> 1;
   const int last_block = (p.N - 1) / kScaleBlock;
   uint32_t slot = 0, phase = 1;
@@ -312,7 +338,7 @@ __device__ void copy_scales(const Fp8Params& p, Shared<C>& sh, uint32_t base, ui
       row[i] += r - box * p.box_rows;
       live[i] = box < p.boxes && row[i] < sh.table.rows[shard_x[i]];
     }
-    const int block = min(n0 / kScaleBlock + lane, last_block);   // of lanes 0..3
+    const int block = min(n0 / kScaleBlock + lane, last_block);   // (of the first lanes)
     int shard = 0, n = sh.table.kb[0], kb = 0;
     const float *x[kPer], *w = nullptr;
     int64_t step[kPer];
@@ -325,16 +351,16 @@ __device__ void copy_scales(const Fp8Params& p, Shared<C>& sh, uint32_t base, ui
     for (int i = 0; i < kPer; ++i) step[i] = live[i] ? sh.table.rows[shard_x[i]] : 0;
     enter();
     while (shard < p.k_shards) {
-      ok = wait_bounded(sempty0 + 8 * slot, phase, ctl, (kRoleProducer << 8) | 3);
+      ok = wait_bounded(rempty0 + 8 * slot, phase, ctl, (kRoleProducer << 8) | 3);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const GroupScales<C>& to = sh.scales[slot];
+      const RawScales<C>& to = sh.raw[slot];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool real = shard < p.k_shards && kb < n;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) copy_4(smem_u32(&to.x[j][lane + 32 * i]), x[i], real && live[i]);
-        if (lane < 4) copy_4(smem_u32(&to.w[j][lane]), w, real);
+        if (lane < C::kBlocks) copy_4(smem_u32(&to.w[j][lane]), w, real);
         if (real && kb + 1 < n) {   // (never past the last one's address)
 #pragma unroll
           for (int i = 0; i < kPer; ++i) x[i] += step[i];
@@ -348,14 +374,48 @@ __device__ void copy_scales(const Fp8Params& p, Shared<C>& sh, uint32_t base, ui
           }
         }
       }
-      sign_copies(sfull0 + 8 * slot);
-      if (++slot == kFp8ScaleRing) {
+      sign_copies(rfull0 + 8 * slot);
+      if (++slot == kFp8RawRing) {
         slot = 0;
         phase ^= 1u;
       }
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Their products, by another warp.
+template <class C>
+__device__ void multiply_scales(const Fp8Params& p, Shared<C>& sh, uint32_t base, const Ctl& ctl) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const uint32_t sfull0 = base + C::kBarsOff + C::kScaleBarsOff, sempty0 = sfull0 + 8 * kFp8ScaleRing;
+  const uint32_t rfull0 = base + C::kBarsOff + C::kRawBarsOff, rempty0 = rfull0 + 8 * kFp8RawRing;
+  const int G = static_cast<int>(gridDim.x) >> 1;
+  const int groups = (p.stages_per_tile * C::KZ + 3) / 4;
+  uint32_t group = 0;
+  for (int id = static_cast<int>(blockIdx.x) >> 1; id < p.tiles; id += G)
+    for (int i = 0; i < groups; ++i, ++group) {
+      const uint32_t in = group % kFp8RawRing, out = group % kFp8ScaleRing;
+      const bool ok = wait_bounded(rfull0 + 8 * in, (group / kFp8RawRing) & 1u, ctl, (kRoleMma << 8) | 3) &&
+                      wait_bounded(sempty0 + 8 * out, ((group / kFp8ScaleRing) & 1u) ^ 1u, ctl, (kRoleMma << 8) | 4);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      const RawScales<C>& from = sh.raw[in];
+#pragma unroll
+      for (int r = lane; r < C::kRows; r += 32) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = from.x[j][r];
+#pragma unroll
+        for (int b = 0; b < C::kBlocks; ++b)
+          sh.scales[out].s[b][r] =
+              make_float4(x[0] * from.w[0][b], x[1] * from.w[1][b], x[2] * from.w[2][b], x[3] * from.w[3][b]);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(sfull0 + 8 * out);
+        mbar_arrive(rempty0 + 8 * in);
+      }
+    }
 }
 
 // wait_bounded without its call, across which the epilogue's registers would be saved.
@@ -395,6 +455,13 @@ __device__ __forceinline__ void wait_sums(uint32_t (&v)[N]) {
                       "+r"(v[i + 6]), "+r"(v[i + 7]));
 }
 
+__device__ __forceinline__ void load_scales(uint32_t at, float (&s)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(s[0]), "=f"(s[1]), "=f"(s[2]), "=f"(s[3])
+               : "r"(at)
+               : "memory");
+}
+
 __device__ __forceinline__ uint4 pack_8(const f32x2* sum) {
   uint32_t w[4];
 #pragma unroll
@@ -405,35 +472,42 @@ __device__ __forceinline__ uint4 pack_8(const f32x2* sum) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A warp's 32 rows x COLS columns through its 4 KB of staging: 64 or 32 columns at a time
+// A warp's 32 rows x COLS columns through its staging, 64 or 32 columns at a time
 // in the swizzled layout of the copy (128 or 64 bytes a row: 8 lanes' 16-byte stores meet
-// in no bank), then one copy, which leaves out what lies past the shard's rows and N.
-// Stored straight from the registers, a row per lane, a tile took 2.6 us.
+// in no bank), then a copy each, which leave out what lies past the shard's rows and N. They
+// read the staging while the next tile is under way. (Stored straight from the registers,
+// a row per lane, a tile took 2.6 us; with staging for 32 columns alone, 2.)
 template <int COLS>
 __device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t staging, int row, int col, int N, bool rows,
                                            const f32x2* sum) {
-  const int lane = static_cast<int>(threadIdx.x) & 31;
   constexpr int kWidth = fp8_store_cols(2 * COLS);
+  const int lane = static_cast<int>(threadIdx.x) & 31;
   const uint32_t at = staging + lane * (2 * kWidth);
   const int turn = kWidth == 64 ? lane & 7 : lane >> 1 & 3;
+  constexpr int kStaged = fp8_staged_cols(2 * COLS);
 #pragma unroll
-  for (int c = 0; c < COLS; c += kWidth) {
+  for (int c0 = 0; c0 < COLS; c0 += kStaged) {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // (lane 0's: the others have none)
     __syncwarp();
 #pragma unroll
-    for (int e = 0; e < kWidth; e += 8) {
-      const uint4 w = pack_8(sum + (c + e) / 2);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((e >> 3) ^ turn) << 4)), "r"(w.x),
-                   "r"(w.y), "r"(w.z), "r"(w.w)
+    for (int c = 0; c < kStaged; c += 8) {
+      const uint4 w = pack_8(sum + (c0 + c) / 2);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::
+                   "r"(at + c / kWidth * (64 * kWidth) + (((c % kWidth >> 3) ^ turn) << 4)), "r"(w.x), "r"(w.y), "r"(w.z),
+                   "r"(w.w)
                    : "memory");
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
-    if (lane == 0 && rows && col + c < N) {
-      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
-                   "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
-                   "r"(col + c), "r"(row), "r"(staging)
-                   : "memory");
+    if (lane == 0 && rows) {
+#pragma unroll
+      for (int c = 0; c < kStaged; c += kWidth)
+        if (col + c0 + c < N)
+          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::
+                       "l"(reinterpret_cast<uint64_t>(map)), "r"(col + c0 + c), "r"(row),
+                       "r"(staging + c / kWidth * (64 * kWidth))
+                       : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   }
 }
@@ -451,6 +525,7 @@ __device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, u
   const int half = C::WIDE ? (warp - 4) >> 2 : quad >> 1;   // of the tile's columns
   const int row0 = C::WIDE ? quad * 32 : (quad & 1) * 32;   // first token row of the CTA
   const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (C::WIDE ? half * C::kCols : 0);
+  const uint32_t scales0 = smem_u32(&sh.scales[0].s[0][row0 + lane]);
   const int G = static_cast<int>(gridDim.x) >> 1;
   uint32_t acc = 0, acc_phase = 0, slot = 0, phase = 0;
   bool ok = true;
@@ -458,35 +533,34 @@ __device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, u
     int m, n0;
     place(p, id, m, n0);
     const int col0 = n0 + half * C::kCols;
-    // The warp's blocks of weight rows among the tile's, and its columns before the second.
-    const int first = col0 / kScaleBlock, b0 = first - n0 / kScaleBlock, b1 = min(b0 + 1, 3);
-    const int split = (first + 1) * kScaleBlock - col0;
+    // The warp's block of weight rows among the tile's, if it has one, or its columns before
+    // the tile's second block.
+    const int b0 = col0 / kScaleBlock - n0 / kScaleBlock;
+    const int split = (n0 / kScaleBlock + 1) * kScaleBlock - col0;
     f32x2 sum[C::kCols / 2];
 #pragma unroll
     for (int i = 0; i < C::kCols / 2; ++i) sum[i] = 0;
-    for (int st = 0; ok && st < p.stages_per_tile;) {
-      // Four k-blocks' scales, then their sums.
-      ok = wait_here(sfull0 + 8 * slot, phase, ctl, (kRoleEpilogue << 8) | 2);
-      const GroupScales<C>& scales = sh.scales[slot];
-      float s0[4], s1[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = scales.x[j][row0 + lane];
-        s0[j] = x * scales.w[j][b0];
-        s1[j] = x * scales.w[j][b1];
-      }
-      __syncwarp();
+    float s0[4], s1[4];
+    auto next_scales = [&]() {   // four k-blocks'
+      ok = wait_here(sfull0 + 8 * slot, phase, ctl, (kRoleEpilogue << 8) | 2) && ok;
+      const uint32_t at = scales0 + slot * static_cast<uint32_t>(sizeof(GroupScales<C>));
+      load_scales(at + (C::kOneBlock ? b0 : 0) * (16 * C::kRows), s0);
+      if constexpr (!C::kOneBlock) load_scales(at + 16 * C::kRows, s1);
+      __syncwarp();   // read by every lane
       if (lane == 0) mbar_arrive(sempty0 + 8 * slot);
       if (++slot == kFp8ScaleRing) {
         slot = 0;
         phase ^= 1u;
       }
+    };
+    for (int st = 0; ok && st < p.stages_per_tile;) {
+      next_scales();
 #pragma unroll
       for (int i = 0; i < 4 / C::KZ; ++i) {
         if (st >= p.stages_per_tile) break;
         ++st;
         ok = ok && wait_here(tfull0 + 8 * acc, acc_phase, ctl, (kRoleEpilogue << 8) | 1);
-        // Every lane together, also after a wait that ran out.
+        // Every lane together, also after a wait that ran out (the vote is below).
         __syncwarp();
         tc_fence_after_sync();
         const uint32_t at = taddr + acc * C::KZ * C::kAccCols;
@@ -496,16 +570,17 @@ __device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, u
         for (int u = 0; u < C::kUnits; ++u) {
           wait_sums<C::kUnit>(v[u & 1]);
           if (u + 1 < C::kUnits) {
-            read_sums<C::kUnit>(at + (u + 1) * (C::WIDE ? 32 : C::kAccCols), v[(u + 1) & 1]);
+            read_sums<C::kUnit>(at + (u + 1) / C::kPerBlock * C::kAccCols + (u + 1) % C::kPerBlock * C::kUnit,
+                                v[(u + 1) & 1]);
           } else {
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) sign_pair(lead_tempty + 8 * acc);
           }
-          const int j = C::WIDE ? i : u, c0 = C::WIDE ? 32 * u : 0;
+          const int j = i * C::KZ + u / C::kPerBlock, c0 = u % C::kPerBlock * C::kUnit;
 #pragma unroll
           for (int c = 0; c < C::kUnit; c += 16) {
-            const float s = C::kCols == kScaleBlock || c0 + c < split ? s0[j] : s1[j];   // 128 columns are a block
+            const float s = C::kOneBlock || c0 + c < split ? s0[j] : s1[j];
             const f32x2 ss = pair_of(s, s);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
@@ -529,7 +604,7 @@ __device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, u
         int shard, row;
         find_box(p, table.box_begin, (2 * m + static_cast<int>(rank)) * p.boxes + box, shard, row);
         row += row0 - box * p.box_rows;
-        store_tile<C::kCols>(&p.tmap_y[shard], base + C::kStagingOff + (warp - 4) * 4096, row, col0, p.N,
+        store_tile<C::kCols>(&p.tmap_y[shard], base + C::kStagingOff + (warp - 4) * (64 * fp8_staged_cols(C::TILE_N)), row, col0, p.N,
                              box < p.boxes && row < table.rows[shard], sum);
         continue;
       }
@@ -578,8 +653,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_fp8_kernel(const __grid_co
       }
       mbar_init(bars + 16 * kFp8MaxRing + 16 * C::kAccs, 1);
       for (uint32_t i = 0; i < kFp8ScaleRing; ++i) {
-        mbar_init(bars + C::kScaleBarsOff + 8 * i, 32);                                // each lane's copies
+        mbar_init(bars + C::kScaleBarsOff + 8 * i, 1);
         mbar_init(bars + C::kScaleBarsOff + 8 * (kFp8ScaleRing + i), C::kEpi / 32);   // read by the warps
+      }
+      for (uint32_t i = 0; i < kFp8RawRing; ++i) {
+        mbar_init(bars + C::kRawBarsOff + 8 * i, 32);   // each lane's copies
+        mbar_init(bars + C::kRawBarsOff + 8 * (kFp8RawRing + i), 1);
       }
       *abort_flag = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -614,6 +693,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) gsr_fp8_kernel(const __grid_co
       multiply<C>(p, base, tmem, ctl);
     else if (warp == 2)
       copy_scales<C>(p, sh, base, rank, ctl);
+    else if (warp == 3)
+      multiply_scales<C>(p, sh, base, ctl);
   } else {
     if constexpr (C::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
     finish<C>(p, sh, base, tmem, rank, ctl);

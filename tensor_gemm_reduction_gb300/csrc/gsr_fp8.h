@@ -70,27 +70,37 @@ struct Fp8Params {  // 128-byte aligned through its CUtensorMap members
 };
 
 // The instances. kFp8Wide: 256 token rows per CTA pair, weight tiles of 64, 128, 192 or 256
-// rows, one k-block per stage. kFp8Narrow: up to 128 token rows, weight tiles of 32, 64, 96
-// or 128, four k-blocks per stage.
+// rows; kFp8Narrow: up to 128 token rows, weight tiles of 32, 64, 96 or 128. k-blocks of a
+// ring stage: a stage costs the barriers' fixed time, so as many as have an accumulator
+// each, twice.
 enum Fp8Form : int { kFp8Wide = 0, kFp8Narrow = 1 };
-constexpr int fp8_kblocks(int form) { return form == kFp8Wide ? 1 : 4; }
+__host__ __device__ constexpr int fp8_kblocks(int form, int tile_n) {
+  return form == kFp8Narrow ? 4 : tile_n <= 128 ? 2 : 1;
+}
 constexpr int fp8_max_tile_n(int form) { return form == kFp8Wide ? 256 : 128; }
 constexpr int fp8_cta_rows(int form) { return form == kFp8Wide ? 128 : 64; }
 constexpr int kFp8MaxRing = 16;
-constexpr int kFp8ScaleRing = 4;      // of the scales, four k-blocks a stage
-// Shared memory of the ring, and of what the epilogue stores from (wide: 4 KB per warp).
-constexpr uint32_t fp8_ring_bytes(int form) { return form == kFp8Wide ? 160 * 1024 : 208 * 1024; }
-constexpr uint32_t fp8_staging_bytes(int form) { return form == kFp8Wide ? 8 * 4096 : 0; }
-constexpr uint32_t fp8_stage_bytes(int form, int tile_n, int token_rows) {
-  return fp8_kblocks(form) * kScaleBlock * static_cast<uint32_t>(tile_n / 2 + token_rows);
+constexpr int kFp8ScaleRing = 2;      // of the scales' products, four k-blocks a stage
+constexpr int kFp8RawRing = 4;        // of the scales
+// Shared memory of what the epilogue stores from (wide: 32 rows of a warp's tile_n / 2 columns,
+// or of 64 at a time), and of the ring.
+__host__ __device__ constexpr int fp8_staged_cols(int tile_n) { return tile_n == 256 ? 64 : tile_n / 2; }
+__host__ __device__ constexpr uint32_t fp8_staging_bytes(int form, int tile_n) {
+  return form == kFp8Wide ? 8 * 32 * 2 * static_cast<uint32_t>(fp8_staged_cols(tile_n)) : 0;
 }
-// Columns of a copy to Y: a warp's are tile_n / 2.
+__host__ __device__ constexpr uint32_t fp8_ring_bytes(int form, int tile_n) {
+  return 206 * 1024 - fp8_staging_bytes(form, tile_n);
+}
+// Columns of a copy to Y (a warp's are tile_n / 2).
 __host__ __device__ constexpr int fp8_store_cols(int tile_n) { return tile_n / 2 % 64 == 0 ? 64 : 32; }
+constexpr uint32_t fp8_stage_bytes(int form, int tile_n, int token_rows) {
+  return fp8_kblocks(form, tile_n) * kScaleBlock * static_cast<uint32_t>(tile_n / 2 + token_rows);
+}
 // Stages that fit. The MMAs read fp8_cta_rows rows of the tokens from a stage whatever it
 // holds, in the last one past its end.
 constexpr int fp8_ring(int form, int tile_n, int token_rows) {
   const uint32_t past = kScaleBlock * static_cast<uint32_t>(fp8_cta_rows(form) - token_rows);
-  const uint32_t fit = (fp8_ring_bytes(form) - past) / fp8_stage_bytes(form, tile_n, token_rows);
+  const uint32_t fit = (fp8_ring_bytes(form, tile_n) - past) / fp8_stage_bytes(form, tile_n, token_rows);
   return static_cast<int>(fit < kFp8MaxRing ? fit : kFp8MaxRing);
 }
 

@@ -50,8 +50,8 @@ CUresult encode_y(CUtensorMap* m, void* ptr, int64_t rows, int64_t cols, int wid
   cuuint32_t estr[2] = {1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                     width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 int64_t pairs_of(const gemm_shard_plan* P) {
@@ -84,7 +84,7 @@ int64_t best_box(int cta_rows, int shards, const int64_t* rows, int* box) {
   return best;
 }
 
-Shape choose(const gemm_shard_plan* P, int64_t N, int shards, const int64_t* rows) {
+Shape choose(const gemm_shard_plan* P, int64_t N, int64_t kblocks, int shards, const int64_t* rows) {
   Shape s;
   const int64_t pairs = pairs_of(P);
   const int narrow = gsr::fp8_cta_rows(gsr::kFp8Narrow), wide = gsr::fp8_cta_rows(gsr::kFp8Wide);
@@ -103,9 +103,15 @@ Shape choose(const gemm_shard_plan* P, int64_t N, int shards, const int64_t* row
   s.form = gsr::kFp8Wide;
   s.m_tiles = best_box(wide, shards, rows, &s.box_rows);
   s.boxes = wide / s.box_rows;
+  // The tile width by the cycles that its waves take: a k-block of 256, 192, 128 or 64 weight
+  // rows takes 880, 720, 500 and 425 (the epilogue's chain of waits and reads, and for the
+  // narrower ones the copies), a tile's start and store some 2500. Measured with all tiles
+  // of 256 / 192 / 128 / 64 (us, N = K = 7168): M = 256 31 / 26 / 21 / 30, 512 32 / 27 / 33 /
+  // 43, 1000 58 / 48 / 50 / 80, 4096 165 / 172 / 176 / 298.
+  constexpr int kCycles[4] = {425, 500, 720, 880};
   int64_t best = INT64_MAX;
   for (int n = 256; n >= 64; n -= 64) {
-    const int64_t tiles = s.m_tiles * cdiv(N, n), cost = cdiv(tiles, pairs) * (std::max(n, 128) + 16);
+    const int64_t cost = cdiv(s.m_tiles * cdiv(N, n), pairs) * (kblocks * kCycles[n / 64 - 1] + 2500);
     if (cost < best) {
       best = cost;
       s.tile_n = n;
@@ -120,8 +126,10 @@ gsr_status run_fp8(const gemm_shard_plan* P, bool ag, int64_t N, int R, const in
                    const void* const* X, const float* const* SX, const void* const* W, const float* const* SW,
                    void* Y, void* ws, gsr_stream_t stream) {
   const int m_shards = ag ? R : 1, k_shards = ag ? 1 : R;
-  const Shape s = choose(P, N, m_shards, M_r);
-  const int kz = gsr::fp8_kblocks(s.form);
+  int64_t kblocks = 0;
+  for (int r = 0; r < k_shards; ++r) kblocks += cdiv(K_r[r], kScaleBlock);
+  const Shape s = choose(P, N, kblocks, m_shards, M_r);
+  const int kz = gsr::fp8_kblocks(s.form, s.tile_n);
   int64_t stages = 0, k_total = 0;
   for (int r = 0; r < k_shards; ++r) {
     stages += cdiv(cdiv(K_r[r], kScaleBlock), kz);
