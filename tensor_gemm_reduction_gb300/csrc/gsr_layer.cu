@@ -40,17 +40,22 @@ namespace {
 constexpr int kThreadsL = 256, kWarpsL = kThreadsL / 32;
 constexpr int kResident = 3;      // CTAs per SM
 constexpr int kMaxCluster = 8;
-constexpr int kGroupsAtOnce = 8;  // groups of 8 entries that share one read of the weights, at most
+// Groups of 8 entries that share one read of the weights, at most. (8 of them leave no
+// registers for their loads: one after the other, an expert of 51 entries took three times
+// as long.)
+constexpr int kGroupsAtOnce = 4;
 
 // The entries by expert: expert[a] names entry[begin[a]] .. entry[begin[a + 1] - 1],
 // ascending, of the a-th expert that has any.
 struct Sorted {
   uint16_t expert[kLayerEntries], begin[kLayerEntries + 1], entry[kLayerEntries];
+  uint8_t token[kLayerEntries];    // of entry[i]
   int active;
 };
 
-// Sorted entries, built in scratch of kMaxGroups + kLayerEntries ints. By all threads.
-__device__ void sort_entries(const LayerParams& p, Sorted& s, int* scratch) {
+// Sorted entries, and their weights where asked for, built in scratch of kMaxGroups +
+// kLayerEntries ints. By all threads.
+__device__ void sort_entries(const LayerParams& p, Sorted& s, float* weights, int* scratch) {
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   int* count = scratch;                                             // per expert, then its begin
   int16_t* id = reinterpret_cast<int16_t*>(scratch + kMaxGroups);   // per entry, -1: dropped
@@ -111,7 +116,12 @@ __device__ void sort_entries(const LayerParams& p, Sorted& s, int* scratch) {
   }
   __syncthreads();
   for (int i = tid; i < n; i += kThreadsL)
-    if (id[i] >= 0) s.entry[count[id[i]] + place[i]] = static_cast<uint16_t>(i);
+    if (id[i] >= 0) {
+      const int to = count[id[i]] + place[i];
+      s.entry[to] = static_cast<uint16_t>(i);
+      s.token[to] = static_cast<uint8_t>(i / p.topk);
+      if (weights) weights[to] = p.weights[i];
+    }
   __syncthreads();
 }
 
@@ -163,7 +173,8 @@ __device__ __forceinline__ float remote_float(const float* p, uint32_t rank) {
 
 // ------------------------------------------------------------ up
 
-constexpr int kPartFloats = kWarpsL * 32 * 32;   // fragments of a pass: 8 warps x 32 values x 32 lanes
+constexpr int kPartValues = 16;   // of a lane's fragments in a pass, at most
+constexpr int kPartFloats = kWarpsL * kPartValues * 32;
 
 // MT strips from column n0 on of expert e against NG groups of 8 entries: this CTA's
 // share of k, the warps' sums added up, and h.
@@ -178,31 +189,28 @@ __device__ void up_pass(const LayerParams& p, const Sorted& s, int e, int n0, in
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
     const int at = 8 * i + g;
-    x[i] = at < count ? p.x + static_cast<size_t>(s.entry[first + at] / p.topk) * K : nullptr;
+    x[i] = at < count ? p.x + static_cast<size_t>(s.token[first + at]) * K : nullptr;
   }
   float c[MT][NG][4] = {};
   for (int k0 = static_cast<int>(rank * kWarpsL + warp) * 64; k0 < p.K; k0 += static_cast<int>(ctas) * kWarpsL * 64) {
-    constexpr int kAtOnce = NG <= 4 ? 2 : 1;   // steps of 32 k whose loads are in flight together
-#pragma unroll 1
-    for (int k = k0 + 8 * t; k < k0 + 64; k += 32 * kAtOnce) {
-      uint4 lo[MT][kAtOnce], hi[MT][kAtOnce];
+    const int k = k0 + 8 * t;
+    uint4 lo[MT][2], hi[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        lo[m][j] = stream(gate + 8 * m * K + k + 32 * j, k + 32 * j < p.K);
+        hi[m][j] = stream(up + 8 * m * K + k + 32 * j, k + 32 * j < p.K);
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint4 b[NG];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) b[i] = fetch(x[i] + k + 32 * j, x[i] && k + 32 * j < p.K);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          lo[m][j] = stream(gate + 8 * m * K + k + 32 * j, k + 32 * j < p.K);
-          hi[m][j] = stream(up + 8 * m * K + k + 32 * j, k + 32 * j < p.K);
-        }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        uint4 b[NG];
-#pragma unroll
-        for (int i = 0; i < NG; ++i) b[i] = fetch(x[i] + k + 32 * j, x[i] && k + 32 * j < p.K);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < NG; ++i) multiply_32(c[m][i], lo[m][j], hi[m][j], b[i]);
-      }
+        for (int i = 0; i < NG; ++i) multiply_32(c[m][i], lo[m][j], hi[m][j], b[i]);
     }
   }
 #pragma unroll
@@ -210,13 +218,13 @@ __device__ void up_pass(const LayerParams& p, const Sorted& s, int e, int n0, in
 #pragma unroll
     for (int i = 0; i < NG; ++i)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) part[(warp * 32 + (m * NG + i) * 4 + v) * 32 + lane] = c[m][i][v];
+      for (int v = 0; v < 4; ++v) part[(warp * kPartValues + (m * NG + i) * 4 + v) * 32 + lane] = c[m][i][v];
   __syncthreads();
   if (ctas > 1) {
     for (int i = tid; i < MT * NG * 4 * 32; i += kThreadsL) {
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarpsL; ++w) sum += part[w * 32 * 32 + i];
+      for (int w = 0; w < kWarpsL; ++w) sum += part[w * (kPartValues * 32) + i];
       total[i] = sum;
     }
     cluster_sync();
@@ -230,8 +238,8 @@ __device__ void up_pass(const LayerParams& p, const Sorted& s, int e, int n0, in
       if (ctas == 1) {
 #pragma unroll
         for (int w = 0; w < kWarpsL; ++w) {
-          gv += part[w * 32 * 32 + at];
-          uv += part[w * 32 * 32 + at + 64];
+          gv += part[w * (kPartValues * 32) + at];
+          uv += part[w * (kPartValues * 32) + at + 64];
         }
       } else {
         for (uint32_t r = 0; r < ctas; ++r) {
@@ -251,11 +259,11 @@ __device__ void up_pass(const LayerParams& p, const Sorted& s, int e, int n0, in
 __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_up_kernel(const __grid_constant__ LayerParams p) {
   __shared__ Sorted s;
   __shared__ float part[kPartFloats];
-  __shared__ float total[32 * 32];
+  __shared__ float total[kPartValues * 32];
   const uint32_t rank = cluster_rank(), ctas = cluster_ctas();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  sort_entries(p, s, reinterpret_cast<int*>(part));
+  sort_entries(p, s, nullptr, reinterpret_cast<int*>(part));
   const int strips = p.N / 8, G = static_cast<int>(gridDim.x / ctas), me = static_cast<int>(blockIdx.x / ctas);
   const long long all = static_cast<long long>(s.active) * strips;
   const int end = static_cast<int>(all * (me + 1) / G);
@@ -269,8 +277,7 @@ __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_up_kernel(cons
       else if (two) up_pass<2, 2>(p, s, e, 8 * strip, at, n, part, total, rank, ctas);
       else if (n <= 8) up_pass<1, 1>(p, s, e, 8 * strip, at, n, part, total, rank, ctas);
       else if (n <= 16) up_pass<1, 2>(p, s, e, 8 * strip, at, n, part, total, rank, ctas);
-      else if (n <= 32) up_pass<1, 4>(p, s, e, 8 * strip, at, n, part, total, rank, ctas);
-      else up_pass<1, 8>(p, s, e, 8 * strip, at, n, part, total, rank, ctas);
+      else up_pass<1, 4>(p, s, e, 8 * strip, at, n, part, total, rank, ctas);
     }
     i += two ? 2 : 1;
   }
@@ -284,7 +291,7 @@ constexpr int kPieceK = 128;   // k of a warp's turn
 // weighted and added to this warp's sums (tokens x 16).
 template <int NG>
 __device__ void down_pass(const LayerParams& p, const Sorted& s, int e, int o0, int from, int to, int first, int count,
-                          float* sums) {
+                          const float* weights, float* sums) {
   const int lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, t = lane & 3;
   const size_t N = p.N;
   const bool in_lo = o0 + g < p.K, in_hi = o0 + 8 + g < p.K;
@@ -298,7 +305,7 @@ __device__ void down_pass(const LayerParams& p, const Sorted& s, int e, int o0, 
   }
   float c[NG][4] = {};
   for (int piece = from; piece < to; ++piece) {
-    constexpr int kAtOnce = NG <= 2 ? 4 : NG <= 4 ? 2 : 1;   // as in up_pass
+    constexpr int kAtOnce = NG <= 2 ? 4 : 2;   // steps of 32 k whose loads are in flight together
 #pragma unroll 1
     for (int k = piece * kPieceK + 8 * t; k < (piece + 1) * kPieceK; k += 32 * kAtOnce) {
       uint4 lo[kAtOnce], hi[kAtOnce];
@@ -329,9 +336,8 @@ __device__ void down_pass(const LayerParams& p, const Sorted& s, int e, int o0, 
         for (int v = 0; v < 2; ++v) {
           const int at = 8 * i + 2 * t + v;
           if (at < count) {
-            const int entry = s.entry[first + at];
-            const float w = p.weights[entry];
-            float* y = sums + entry / p.topk * 16 + g;
+            const float w = weights[first + at];
+            float* y = sums + s.token[first + at] * 16 + g;
             y[0] = fmaf(w, c[i][v], y[0]);
             y[8] = fmaf(w, c[i][v + 2], y[8]);
           }
@@ -344,11 +350,12 @@ __device__ void down_pass(const LayerParams& p, const Sorted& s, int e, int o0, 
 __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_down_kernel(const __grid_constant__ LayerParams p) {
   __shared__ Sorted s;
   __shared__ float sums[kWarpsL][kLayerTokens * 16];
+  __shared__ float weights[kLayerEntries];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_ctas();
   // The first kernel let this one start after it had waited for all before it, so the
   // call's inputs may be read; only h has to be waited for.
-  sort_entries(p, s, reinterpret_cast<int*>(sums));
+  sort_entries(p, s, weights, reinterpret_cast<int*>(sums));
   const int pieces = (p.N + kPieceK - 1) / kPieceK, tiles = (p.K + 15) / 16;
   const int G = static_cast<int>(gridDim.x / ctas), workers = static_cast<int>(ctas) * kWarpsL;
   const int worker = static_cast<int>(rank) * kWarpsL + warp;
@@ -362,7 +369,6 @@ __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_down_kernel(co
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.down + (static_cast<size_t>(s.expert[a]) * p.K + row) * p.N + k));
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (; tile < tiles; tile += G) {
     __syncthreads();
     for (int i = lane; i < p.T * 16; i += 32) sums[warp][i] = 0.f;
@@ -373,10 +379,9 @@ __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_down_kernel(co
       const int first = s.begin[a], count = s.begin[a + 1] - first;
       for (int f = 0; f < count; f += 8 * kGroupsAtOnce) {
         const int n = min(count - f, 8 * kGroupsAtOnce), at = first + f;
-        if (n <= 8) down_pass<1>(p, s, e, o0, from, to, at, n, sums[warp]);
-        else if (n <= 16) down_pass<2>(p, s, e, o0, from, to, at, n, sums[warp]);
-        else if (n <= 32) down_pass<4>(p, s, e, o0, from, to, at, n, sums[warp]);
-        else down_pass<8>(p, s, e, o0, from, to, at, n, sums[warp]);
+        if (n <= 8) down_pass<1>(p, s, e, o0, from, to, at, n, weights, sums[warp]);
+        else if (n <= 16) down_pass<2>(p, s, e, o0, from, to, at, n, weights, sums[warp]);
+        else down_pass<4>(p, s, e, o0, from, to, at, n, weights, sums[warp]);
       }
       i += to - from;
     }
@@ -407,6 +412,9 @@ __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_down_kernel(co
       }
     if (ctas > 1) cluster_sync();   // read by the first CTA before the next tile
   }
+  // Not earlier: with the next call's first kernel resident and waiting beside this one, 16
+  // tokens took 395 us, and 324 without.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // A grid of clusters: as many CTAs per unit of work as fill the GPU, up to 8.
