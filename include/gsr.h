@@ -490,14 +490,14 @@ gsr_status gemm_group_combine(const gemm_shard_plan *plan, int64_t T, int topk, 
 
 /*
  * Expert layer of a few tokens: what gemm_group_route, gemm_grouped_gated,
- * gemm_grouped and gemm_group_combine do together, in two launches:
+ * gemm_grouped and gemm_group_combine do together, in one call:
  *     Y[t] = base[t] + sum_j weights[t, j] * W_down[e] . h_tj,
  *     h_tj = silu(G[e] . X[t]) * (U[e] . X[t]),  e = ids[t, j],
  * G[e] and U[e] the first and the last N rows of W_up[e].
  *   T, topk   tokens and entries of each: T <= GSR_MAX_LAYER_TOKENS, T * topk <=
  *             GSR_MAX_LAYER_ENTRIES and max_M; T == 0 returns GSR_OK with no launch
- *   E, N, K   experts, their inner and the outer width: multiples of 8, N <= max_N, K <=
- *             max_N and max_K
+ *   E, N, K   experts, their inner and the outer width: multiples of 8, at most max_N and
+ *             max_K
  *   ids       device, T x topk integers of id_bytes (4 or 8) bytes; a value outside
  *             0..E-1 drops the entry, whatever its weight holds. A token may name an
  *             expert twice.
@@ -505,10 +505,12 @@ gsr_status gemm_group_combine(const gemm_shard_plan *plan, int64_t T, int topk, 
  *   X, base   device, T x K bf16; base may be NULL (0)
  *   W_up      device, E x 2N x K bf16; W_down: E x K x N bf16
  *   Y         device, T x K bf16; may be base or X
- * The products accumulate in fp32, h is rounded to bf16 between them, the weighted sum is
- * fp32 (experts ascending, and the entries of one expert in order, in parts of k whose
- * number depends on the shapes) and Y is rounded once. Only the weights of named experts
- * are read.
+ * Up to 64 entries (T * topk), and up to 8 E, run in two kernels of their own, whose
+ * weighted sum is fp32 (experts ascending, the entries of one in order, in parts of k whose
+ * number depends on the shapes); more run in the kernels of the calls named above,
+ * with the down products rounded to bf16 before they are weighted, as there. In both the
+ * products accumulate in fp32, h is rounded to bf16 between them and Y once. Only the
+ * weights of named experts are read.
  */
 gsr_status gemm_expert_layer(const gemm_shard_plan *plan, int64_t T, int topk, int E, int64_t N,
                              int64_t K, const void *ids, int id_bytes, const float *weights,

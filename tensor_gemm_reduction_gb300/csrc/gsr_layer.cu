@@ -11,7 +11,7 @@
 // work. A thread loads 16 bytes of a weight row (8 k), and the same k of a token: which k
 // an MMA calls its first is the same for both operands.
 //
-// Every CTA sorts the T * topk entries by expert itself (a stable order, so that sums
+// Every CTA sorts the T * topk entries by expert itself (in a stable order, so that sums
 // do not depend on timing).
 // - Up: a strip is 8 columns of one expert, gate and up rows as the two halves of A, so
 //   that a thread ends with both of the same element. Strips are dealt evenly to the
@@ -48,81 +48,62 @@ constexpr int kGroupsAtOnce = 4;
 // The entries by expert: expert[a] names entry[begin[a]] .. entry[begin[a + 1] - 1],
 // ascending, of the a-th expert that has any.
 struct Sorted {
-  uint16_t expert[kLayerEntries], begin[kLayerEntries + 1], entry[kLayerEntries];
-  uint8_t token[kLayerEntries];    // of entry[i]
-  int active;
+  alignas(16) int id[kLayerEntries];      // of the sort, read four at a time; past every
+  alignas(16) int first[kLayerEntries];   // expert: none
+  int expert[kLayerEntries], begin[kLayerEntries + 1];
+  int entry[kLayerEntries], token[kLayerEntries];
+  float weight[kLayerEntries];
 };
 
-// Sorted entries, and their weights where asked for, built in scratch of kMaxGroups +
-// kLayerEntries ints. By all threads.
-__device__ void sort_entries(const LayerParams& p, Sorted& s, float* weights, int* scratch) {
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  int* count = scratch;                                             // per expert, then its begin
-  int16_t* id = reinterpret_cast<int16_t*>(scratch + kMaxGroups);   // per entry, -1: dropped
-  int16_t* place = id + kLayerEntries;                              // among its expert's entries
-  __shared__ int sums[kWarpsL];
-  const int n = p.T * p.topk;
-  for (int e = tid; e < p.E; e += kThreadsL) count[e] = 0;
-  for (int i = tid; i < n; i += kThreadsL) {
+// Sorts the entries; their number of experts. By all threads, the first of which own an
+// entry each and compare it with all.
+__device__ int sort_entries(const LayerParams& p, Sorted& s) {
+  static_assert(kLayerEntries <= kThreadsL && kLayerEntries % 4 == 0, "an entry per thread");
+  constexpr int kNone = 1 << 30;
+  const int i = static_cast<int>(threadIdx.x), n = p.T * p.topk;
+  int mine = kNone;
+  float weight = 0.f;
+  if (i < n) {
     const long long v = p.wide ? reinterpret_cast<const long long*>(p.ids)[i] : reinterpret_cast<const int*>(p.ids)[i];
-    id[i] = static_cast<int16_t>(v >= 0 && v < p.E ? v : -1);
+    weight = p.weights[i];
+    if (v >= 0 && v < p.E) mine = static_cast<int>(v);
   }
+  if (i < kLayerEntries) s.id[i] = mine;
   __syncthreads();
-  if (warp == 0) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int mine = i0 + lane < n ? id[i0 + lane] : -1;
-      const uint32_t same = __match_any_sync(0xffffffffu, mine);
-      const uint32_t before = same & ((1u << lane) - 1u);
-      const int first = mine >= 0 ? count[mine] : 0;
-      __syncwarp();
-      if (mine >= 0) {
-        place[i0 + lane] = static_cast<int16_t>(first + __popc(before));
-        if (before == 0) count[mine] = first + __popc(same);
+  const int quads = (n + 3) / 4;
+  int place = 0;
+  bool first = mine != kNone;
+  if (first)
+    for (int q = 0; q < quads; ++q) {
+      const int4 o = reinterpret_cast<const int4*>(s.id)[q];
+      const int id[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool before = id[j] == mine && 4 * q + j < i;
+        place += id[j] < mine || before ? 1 : 0;
+        first = first && !before;
       }
-      __syncwarp();
+    }
+  if (i < kLayerEntries) s.first[i] = first ? mine : kNone;
+  const int kept = __syncthreads_count(mine != kNone);
+  if (mine != kNone) {
+    s.entry[place] = i;
+    s.token[place] = i / p.topk;
+    s.weight[place] = weight;
+    if (first) {
+      int a = 0;
+      for (int q = 0; q < quads; ++q) {
+        const int4 o = reinterpret_cast<const int4*>(s.first)[q];
+        a += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
+      }
+      s.expert[a] = mine;
+      s.begin[a] = place;
     }
   }
+  const int active = __syncthreads_count(first);
+  if (i == 0) s.begin[active] = kept;
   __syncthreads();
-  // Prefix sums of entries (low half) and of experts that have any (high half).
-  const int per = (p.E + kThreadsL - 1) / kThreadsL, e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
-  int mine = 0;
-  for (int e = e0; e < e1; ++e) mine += count[e] + (count[e] > 0 ? 1 << 16 : 0);
-  int incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  if (lane == 31) sums[warp] = incl;
-  __syncthreads();
-  int at = incl - mine, total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarpsL; ++i) {
-    if (i < warp) at += sums[i];
-    total += sums[i];
-  }
-  for (int e = e0; e < e1; ++e) {
-    const int c = count[e];
-    count[e] = at & 0xffff;
-    if (c > 0) {
-      s.expert[at >> 16] = static_cast<uint16_t>(e);
-      s.begin[at >> 16] = static_cast<uint16_t>(at & 0xffff);
-      at += c + (1 << 16);
-    }
-  }
-  if (tid == 0) {
-    s.active = total >> 16;
-    s.begin[total >> 16] = static_cast<uint16_t>(total & 0xffff);
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += kThreadsL)
-    if (id[i] >= 0) {
-      const int to = count[id[i]] + place[i];
-      s.entry[to] = static_cast<uint16_t>(i);
-      s.token[to] = static_cast<uint8_t>(i / p.topk);
-      if (weights) weights[to] = p.weights[i];
-    }
-  __syncthreads();
+  return active;
 }
 
 __device__ __forceinline__ uint4 stream(const uint16_t* p, bool real) {
@@ -263,9 +244,9 @@ __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_up_kernel(cons
   const uint32_t rank = cluster_rank(), ctas = cluster_ctas();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  sort_entries(p, s, nullptr, reinterpret_cast<int*>(part));
+  const int active = sort_entries(p, s);
   const int strips = p.N / 8, G = static_cast<int>(gridDim.x / ctas), me = static_cast<int>(blockIdx.x / ctas);
-  const long long all = static_cast<long long>(s.active) * strips;
+  const long long all = static_cast<long long>(active) * strips;
   const int end = static_cast<int>(all * (me + 1) / G);
   for (int i = static_cast<int>(all * me / G); i < end;) {
     const int a = i / strips, strip = i - a * strips, e = s.expert[a];
@@ -291,7 +272,7 @@ constexpr int kPieceK = 128;   // k of a warp's turn
 // weighted and added to this warp's sums (tokens x 16).
 template <int NG>
 __device__ void down_pass(const LayerParams& p, const Sorted& s, int e, int o0, int from, int to, int first, int count,
-                          const float* weights, float* sums) {
+                          float* sums) {
   const int lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, t = lane & 3;
   const size_t N = p.N;
   const bool in_lo = o0 + g < p.K, in_hi = o0 + 8 + g < p.K;
@@ -336,7 +317,7 @@ __device__ void down_pass(const LayerParams& p, const Sorted& s, int e, int o0, 
         for (int v = 0; v < 2; ++v) {
           const int at = 8 * i + 2 * t + v;
           if (at < count) {
-            const float w = weights[first + at];
+            const float w = s.weight[first + at];
             float* y = sums + s.token[first + at] * 16 + g;
             y[0] = fmaf(w, c[i][v], y[0]);
             y[8] = fmaf(w, c[i][v + 2], y[8]);
@@ -350,16 +331,15 @@ __device__ void down_pass(const LayerParams& p, const Sorted& s, int e, int o0, 
 __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_down_kernel(const __grid_constant__ LayerParams p) {
   __shared__ Sorted s;
   __shared__ float sums[kWarpsL][kLayerTokens * 16];
-  __shared__ float weights[kLayerEntries];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_ctas();
   // The first kernel let this one start after it had waited for all before it, so the
   // call's inputs may be read; only h has to be waited for.
-  sort_entries(p, s, weights, reinterpret_cast<int*>(sums));
+  const int active = sort_entries(p, s);
   const int pieces = (p.N + kPieceK - 1) / kPieceK, tiles = (p.K + 15) / 16;
   const int G = static_cast<int>(gridDim.x / ctas), workers = static_cast<int>(ctas) * kWarpsL;
   const int worker = static_cast<int>(rank) * kWarpsL + warp;
-  const long long all = static_cast<long long>(s.active) * pieces;
+  const long long all = static_cast<long long>(active) * pieces;
   const int begin = static_cast<int>(all * worker / workers), end = static_cast<int>(all * (worker + 1) / workers);
   int tile = static_cast<int>(blockIdx.x / ctas);
   // The first weights of this warp: 16 rows x 256 bytes a piece, a line per lane.
@@ -379,9 +359,9 @@ __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_down_kernel(co
       const int first = s.begin[a], count = s.begin[a + 1] - first;
       for (int f = 0; f < count; f += 8 * kGroupsAtOnce) {
         const int n = min(count - f, 8 * kGroupsAtOnce), at = first + f;
-        if (n <= 8) down_pass<1>(p, s, e, o0, from, to, at, n, weights, sums[warp]);
-        else if (n <= 16) down_pass<2>(p, s, e, o0, from, to, at, n, weights, sums[warp]);
-        else down_pass<4>(p, s, e, o0, from, to, at, n, weights, sums[warp]);
+        if (n <= 8) down_pass<1>(p, s, e, o0, from, to, at, n, sums[warp]);
+        else if (n <= 16) down_pass<2>(p, s, e, o0, from, to, at, n, sums[warp]);
+        else down_pass<4>(p, s, e, o0, from, to, at, n, sums[warp]);
       }
       i += to - from;
     }

@@ -7,8 +7,19 @@
 
 namespace gsr {
 
-constexpr int kLayerTokens = 64;      // T, at most
-constexpr int kLayerEntries = 1024;   // T * topk, at most
+constexpr int kLayerTokens = 64;        // T, at most
+constexpr int kLayerMost = 1024;        // T * topk, at most
+// T * topk up to which the two kernels run, and the same per expert. Beyond them the entries'
+// rows, which are read for every 8 or 16 columns, are the traffic, and the routed
+// products, with up to 256 tokens a tile, are faster. Measured, the two kernels / the four
+// routed ones (us): one entry of one expert, N = 896, K = 7168, 18 / 29; 4 of 128, N = 256, K =
+// 7168, 17 / 31; 8 of 64, N = 896, K = 7168, 50 / 65, 128 325 / 323, 256 452 / 358, 512 604 / 365;
+// 64 of 8, same widths, 58 / 66, N = 1024, K = 4096, 53 / 50; 64 of 16, 78 / 79; 64 of 4, N =
+// K = 2048, 46 / 34; 128 of 32, N = 512, K = 2048, 61 / 49; 183 of 7, N = 1000, K = 1832, 47 / 34.
+constexpr int kLayerEntries = 64, kLayerPerExpert = 8;
+inline bool layer_in_two(int64_t entries, int E) {
+  return entries <= kLayerEntries && entries <= static_cast<int64_t>(kLayerPerExpert) * E;
+}
 
 struct LayerParams {
   const void* ids;          // T x topk

@@ -48,10 +48,12 @@ int64_t max_lists(const gemm_shard_plan* P) { return P->max_M / 128 + 2; }
 size_t list_bytes(const gemm_shard_plan* P) {
   return round256(static_cast<size_t>(max_lists(P)) * gsr::kAdapterListStride * sizeof(int32_t));
 }
-// The expert layer's rows between its products.
-size_t layer_bytes(const gemm_shard_plan* P) {
-  return round256(static_cast<size_t>(std::min<int64_t>(P->max_M, gsr::kLayerEntries)) * P->max_N * 2);
+// The expert layer's rows between its products and after them, and its route.
+size_t layer_rows_bytes(const gemm_shard_plan* P) {
+  return round256(static_cast<size_t>(std::min<int64_t>(P->max_M, gsr::kLayerMost)) * P->max_N * 2);
 }
+constexpr size_t kLayerRouteBytes = 4 * (gsr::kMaxGroups + 64 + 2 * gsr::kLayerMost);
+size_t layer_bytes(const gemm_shard_plan* P) { return 2 * layer_rows_bytes(P) + kLayerRouteBytes; }
 constexpr size_t kPartialsAt = gsr::kWsHeader + gsr::kRoutedCounterBytes;
 
 size_t workspace_bytes(const gemm_shard_plan* P) {
@@ -356,15 +358,17 @@ gsr_status gemm_expert_layer(const gemm_shard_plan* P, int64_t T, int topk, int 
     return fail(GSR_ERR_INVALID_VALUE, "E=%d outside 1..%d", E, gsr::kMaxGroups);
   if (topk < 1 || topk > gsr::kMaxTopk)
     return fail(GSR_ERR_INVALID_VALUE, "topk=%d outside 1..%d", topk, gsr::kMaxTopk);
-  if (T < 0 || T > gsr::kLayerTokens || T * topk > gsr::kLayerEntries || T * topk > P->max_M)
+  if (T < 0 || T > gsr::kLayerTokens || T * topk > gsr::kLayerMost || T * topk > P->max_M)
     return fail(GSR_ERR_INVALID_VALUE, "T=%lld outside 0..%d, or T * topk above %d or the plan's max_M=%lld",
-                (long long)T, gsr::kLayerTokens, gsr::kLayerEntries, (long long)P->max_M);
-  if (N < 8 || N % 8 || N > P->max_N || N > INT32_MAX / 2048)
-    return fail(GSR_ERR_INVALID_VALUE, "N=%lld must be a positive multiple of 8, at most the plan's max_N=%lld",
-                (long long)N, (long long)P->max_N);
-  if (K < 8 || K % 8 || K > P->max_K || K > P->max_N || K > INT32_MAX / 2048)
-    return fail(GSR_ERR_INVALID_VALUE, "K=%lld must be a positive multiple of 8, at most the plan's max_K=%lld and max_N=%lld",
-                (long long)K, (long long)P->max_K, (long long)P->max_N);
+                (long long)T, gsr::kLayerTokens, gsr::kLayerMost, (long long)P->max_M);
+  // Either width is an output's and a reduction's.
+  const int64_t widest = std::min<int64_t>(std::min(P->max_N, P->max_K), 1 << 20);
+  if (N < 8 || N % 8 || N > widest)
+    return fail(GSR_ERR_INVALID_VALUE, "N=%lld must be a positive multiple of 8, at most the plan's max_N and max_K (%lld)",
+                (long long)N, (long long)widest);
+  if (K < 8 || K % 8 || K > widest)
+    return fail(GSR_ERR_INVALID_VALUE, "K=%lld must be a positive multiple of 8, at most the plan's max_N and max_K (%lld)",
+                (long long)K, (long long)widest);
   if (id_bytes != 4 && id_bytes != 8)
     return fail(GSR_ERR_INVALID_VALUE, "id_bytes must be 4 or 8 (got %d)", id_bytes);
   if (T > 0 && (!ids || !weights || !X || !Y))
@@ -379,9 +383,21 @@ gsr_status gemm_expert_layer(const gemm_shard_plan* P, int64_t T, int topk, int 
   if (s) return s;
   if (T == 0) return ok();
   if (gsr::log_config_enabled())
-    std::fprintf(stderr, "gsr: expert_layer T=%lld topk=%d E=%d N=%lld K=%lld kernel=layer\n", (long long)T, topk, E,
-                 (long long)N, (long long)K);
+    std::fprintf(stderr, "gsr: expert_layer T=%lld topk=%d E=%d N=%lld K=%lld kernel=%s\n", (long long)T, topk, E,
+                 (long long)N, (long long)K, gsr::layer_in_two(T * topk, E) ? "layer" : "routed");
   if (P->device < 0) return fail(GSR_ERR_UNSUPPORTED, "host plan: arguments are valid, nothing launched");
+  uint8_t* rows = static_cast<uint8_t*>(ws) + workspace_bytes(P) - layer_bytes(P);
+  if (!gsr::layer_in_two(T * topk, E)) {
+    void* z = rows + layer_rows_bytes(P);
+    int32_t* offsets = reinterpret_cast<int32_t*>(rows + 2 * layer_rows_bytes(P));
+    int32_t *source = offsets + gsr::kMaxGroups + 64, *position = source + gsr::kLayerMost;
+    const int64_t M = T * topk;
+    s = gemm_group_route(P, T, topk, E, ids, id_bytes, offsets, source, position, stream);
+    if (!s) s = run_grouped(P, gsr::kGated, E, M, N, K, offsets, T, X, source, W_up, rows, ws, ws_bytes, stream);
+    if (!s) s = run_grouped(P, gsr::kGrouped, E, M, K, N, offsets, M, rows, nullptr, W_down, z, ws, ws_bytes, stream);
+    if (!s) s = gemm_group_combine(P, T, topk, K, M, z, position, weights, base, Y, stream);
+    return s;
+  }
   gsr::LayerParams p = {};
   p.ids = ids;
   p.weights = weights;
@@ -389,7 +405,7 @@ gsr_status gemm_expert_layer(const gemm_shard_plan* P, int64_t T, int topk, int 
   p.up = static_cast<const uint16_t*>(W_up);
   p.down = static_cast<const uint16_t*>(W_down);
   p.base = static_cast<const uint16_t*>(base);
-  p.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + workspace_bytes(P) - layer_bytes(P));
+  p.h = reinterpret_cast<uint16_t*>(rows);
   p.y = static_cast<uint16_t*>(Y);
   p.T = static_cast<int>(T);
   p.topk = topk;

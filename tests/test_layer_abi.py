@@ -50,16 +50,18 @@ def test_refusals(host):
     assert call(T=0, ids=0, weights=0, X=0, Y=0) == B.GSR_OK
     small = B.gemm_shard_plan_create_host(152, 39, 8192, 8192, 1)
     refused(call(plan=small.handle), B.GSR_ERR_INVALID_VALUE, "max_M=39")
-    # the width that comes back is an output's as well as a reduction's
+    # either width is an output's as well as a reduction's
     narrow = B.gemm_shard_plan_create_host(152, 64, 64, 8192, 1)
-    refused(call(plan=narrow.handle), B.GSR_ERR_INVALID_VALUE, "max_N=64")
+    refused(call(plan=narrow.handle), B.GSR_ERR_INVALID_VALUE, "K=128")
+    short = B.gemm_shard_plan_create_host(152, 64, 8192, 56, 1)
+    refused(call(plan=short.handle, K=56), B.GSR_ERR_INVALID_VALUE, "N=64")
 
 
 def test_workspace_holds_the_rows_between_the_products(host):
     _, plan = host
     few = B.gemm_shard_plan_create_host(152, 1024, 8192, 8192, 16)
     wide = B.gemm_shard_plan_create_host(152, 1024, 16384, 8192, 16)
-    assert B.gemm_routed_workspace_size(wide) - B.gemm_routed_workspace_size(few) == 1024 * 8192 * 2
+    assert B.gemm_routed_workspace_size(wide) - B.gemm_routed_workspace_size(few) == 2 * 1024 * 8192 * 2
 
 
 def test_binding_refuses_wrong_tensors(host):
