@@ -107,6 +107,6 @@ constexpr int fp8_ring(int form, int tile_n, int token_rows) {
 cudaError_t prepare_fp8_kernels();
 cudaError_t launch_fp8(const Fp8Params& p, int form, int ctas, cudaStream_t stream);
 cudaError_t launch_norm(const NormParams& p, int sm_count, cudaStream_t stream);
-cudaError_t launch_quantize(const QuantParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_quantize(const QuantParams& p, cudaStream_t stream);
 
 }  // namespace gsr

@@ -279,8 +279,8 @@ gsr_status gemm_shard_quantize(const gemm_shard_plan* P, int64_t rows, int64_t c
   if (cols < 16 || cols % 16 || cols > P->max_K || cols > INT32_MAX - 256)
     return fail(GSR_ERR_INVALID_VALUE, "cols=%lld must be a positive multiple of 16, at most the plan's max_K=%lld",
                 (long long)cols, (long long)P->max_K);
-  if (block_rows != 1 && cdiv(rows, kScaleBlock) * cdiv(cols, kScaleBlock) > INT32_MAX)
-    return fail(GSR_ERR_INVALID_VALUE, "rows and cols give too many blocks");
+  if (cdiv(rows, 16) * cdiv(cols, kScaleBlock) > INT32_MAX)   // (a grid of fewer CTAs in either form)
+    return fail(GSR_ERR_INVALID_VALUE, "rows and cols give too many groups");
   if (rows > 0 && (!X || !Q || !scale)) return fail(GSR_ERR_INVALID_VALUE, "X, Q and scale must not be NULL");
   if (!aligned16(X) || !aligned16(Q) || !aligned4(scale))
     return fail(GSR_ERR_INVALID_VALUE, "X and Q must be 16-byte aligned, scale 4-byte aligned");
@@ -295,7 +295,7 @@ gsr_status gemm_shard_quantize(const gemm_shard_plan* P, int64_t rows, int64_t c
   p.block_rows = block_rows;
   DeviceScope scope(P->device);
   if (scope.err != cudaSuccess) return cuda_fail(scope.err, "selecting the plan's device");
-  const cudaError_t e = gsr::launch_quantize(p, P->sm_count, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = gsr::launch_quantize(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
   return ok();
 }
