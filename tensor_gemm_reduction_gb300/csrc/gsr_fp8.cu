@@ -54,9 +54,9 @@ struct Cfg {
   // that a warp's columns do.
   static constexpr int kBlocks = kScaleBlock % TILE_N == 0 ? 1 : 2;
   static constexpr bool kOneBlock = kBlocks == 1 || kCols == kScaleBlock;
-  // A k-block's sums are read from TMEM in units of 32 columns or of all, the next one while
-  // one is added up.
-  static constexpr int kUnit = !WIDE ? kCols : TILE_N == 256 ? 16 : 32, kPerBlock = kCols / kUnit, kUnits = KZ * kPerBlock;
+  // A k-block's sums are read from TMEM in units, the next one while one is added up: as
+  // wide ones as there are registers for (a read takes about 100 cycles whatever it reads).
+  static constexpr int kUnit = kCols <= 64 ? kCols : kCols == 96 ? 48 : 32, kPerBlock = kCols / kUnit, kUnits = KZ * kPerBlock;
   // TMEM columns of a k-block's sums, and accumulators (of KZ k-blocks).
   static constexpr uint32_t kAccCols = 256 / KZ;
   static constexpr uint32_t kAccs = 2;
@@ -292,21 +292,49 @@ __device__ void multiply(const Fp8Params& p, uint32_t base, uint32_t tmem, const
   }
 }
 
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pair_of(float a, float b) {
-  f32x2 v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  return v;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 v;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
-  return v;
-}
-__device__ __forceinline__ float2 both(f32x2 v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
+// An epilogue thread's N sums. PAIRS: two by two in 64-bit registers, whose operands the
+// compiler has to place in pairs; with 128 sums it has no room to (tiles of 256 at M = 4096,
+// N = K = 7168: 165 us in pairs, 150 alone; of 192 169 and 175).
+template <bool PAIRS, int N>
+struct Sums {
+  float v[N];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.f;
+  }
+  // 16 columns from c on += s * x.
+  __device__ __forceinline__ void add(int c, const uint32_t* x, float s) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[c + e] = fmaf(__uint_as_float(x[e]), s, v[c + e]);
+  }
+  __device__ __forceinline__ uint32_t two(int c) const { return pack_bf16x2(__float_as_uint(v[c]), __float_as_uint(v[c + 1])); }
+};
+template <int N>
+struct Sums<true, N> {
+  unsigned long long v[N / 2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) v[i] = 0;
+  }
+  __device__ __forceinline__ void add(int c, const uint32_t* x, float s) {
+    unsigned long long ss, xx;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      asm("mov.b64 %0, {%1, %2};" : "=l"(xx) : "r"(x[e]), "r"(x[e + 1]));
+      asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v[(c + e) / 2]) : "l"(xx), "l"(ss));
+    }
+  }
+  __device__ __forceinline__ uint32_t two(int c) const {
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v[c / 2]));
+    return pack_bf16x2(a, b);
+  }
+};
+// 8 sums from c on in bf16.
+template <class S>
+__device__ __forceinline__ uint4 pack_8(const S& sums, int c) {
+  return make_uint4(sums.two(c), sums.two(c + 2), sums.two(c + 4), sums.two(c + 6));
 }
 
 // 4 bytes to shared memory, or zeros; asynchronous.
@@ -462,24 +490,14 @@ __device__ __forceinline__ void load_scales(uint32_t at, float (&s)[4]) {
                : "memory");
 }
 
-__device__ __forceinline__ uint4 pack_8(const f32x2* sum) {
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = both(sum[e]);
-    w[e] = pack_bf16x2(__float_as_uint(f.x), __float_as_uint(f.y));
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // A warp's 32 rows x COLS columns through its staging, 64 or 32 columns at a time
 // in the swizzled layout of the copy (128 or 64 bytes a row: 8 lanes' 16-byte stores meet
 // in no bank), then a copy each, which leave out what lies past the shard's rows and N. They
 // read the staging while the next tile is under way. (Stored straight from the registers,
 // a row per lane, a tile took 2.6 us; with staging for 32 columns alone, 2.)
-template <int COLS>
+template <int COLS, class S>
 __device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t staging, int row, int col, int N, bool rows,
-                                           const f32x2* sum) {
+                                           const S& sums) {
   constexpr int kWidth = fp8_store_cols(2 * COLS);
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const uint32_t at = staging + lane * (2 * kWidth);
@@ -491,7 +509,7 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t stag
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < kStaged; c += 8) {
-      const uint4 w = pack_8(sum + (c0 + c) / 2);
+      const uint4 w = pack_8(sums, c0 + c);
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::
                    "r"(at + c / kWidth * (64 * kWidth) + (((c % kWidth >> 3) ^ turn) << 4)), "r"(w.x), "r"(w.y), "r"(w.z),
                    "r"(w.w)
@@ -537,9 +555,8 @@ __device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, u
     // the tile's second block.
     const int b0 = col0 / kScaleBlock - n0 / kScaleBlock;
     const int split = (n0 / kScaleBlock + 1) * kScaleBlock - col0;
-    f32x2 sum[C::kCols / 2];
-#pragma unroll
-    for (int i = 0; i < C::kCols / 2; ++i) sum[i] = 0;
+    Sums<C::TILE_N != 256, C::kCols> sums;
+    sums.clear();
     float s0[4], s1[4];
     auto next_scales = [&]() {   // four k-blocks'
       ok = wait_here(sfull0 + 8 * slot, phase, ctl, (kRoleEpilogue << 8) | 2) && ok;
@@ -579,15 +596,8 @@ __device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, u
           }
           const int j = i * C::KZ + u / C::kPerBlock, c0 = u % C::kPerBlock * C::kUnit;
 #pragma unroll
-          for (int c = 0; c < C::kUnit; c += 16) {
-            const float s = C::kOneBlock || c0 + c < split ? s0[j] : s1[j];
-            const f32x2 ss = pair_of(s, s);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              f32x2& to = sum[(c0 + c + e) / 2];
-              to = fma2(pair_of(__uint_as_float(v[u & 1][c + e]), __uint_as_float(v[u & 1][c + e + 1])), ss, to);
-            }
-          }
+          for (int c = 0; c < C::kUnit; c += 16)
+            sums.add(c0 + c, v[u & 1] + c, C::kOneBlock || c0 + c < split ? s0[j] : s1[j]);
         }
         if (++acc == C::kAccs) {
           acc = 0;
@@ -605,7 +615,7 @@ __device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, u
         find_box(p, table.box_begin, (2 * m + static_cast<int>(rank)) * p.boxes + box, shard, row);
         row += row0 - box * p.box_rows;
         store_tile<C::kCols>(&p.tmap_y[shard], base + C::kStagingOff + (warp - 4) * (64 * fp8_staged_cols(C::TILE_N)), row, col0, p.N,
-                             box < p.boxes && row < table.rows[shard], sum);
+                             box < p.boxes && row < table.rows[shard], sums);
         continue;
       }
     }
@@ -617,7 +627,7 @@ __device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, u
       uint16_t* y = p.y + static_cast<size_t>(table.row_begin[shard] + row) * p.N + col0;
 #pragma unroll
       for (int c = 0; c < C::kCols; c += 8)
-        if (col0 + c < p.N) *reinterpret_cast<uint4*>(y + c) = pack_8(sum + c / 2);
+        if (col0 + c < p.N) *reinterpret_cast<uint4*>(y + c) = pack_8(sums, c);
     }
   }
   // The last copies have read the staging before the shared memory goes away.

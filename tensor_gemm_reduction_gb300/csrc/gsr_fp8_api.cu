@@ -104,11 +104,11 @@ Shape choose(const gemm_shard_plan* P, int64_t N, int64_t kblocks, int shards, c
   s.m_tiles = best_box(wide, shards, rows, &s.box_rows);
   s.boxes = wide / s.box_rows;
   // The tile width by the cycles that its waves take: a k-block of 256, 192, 128 or 64 weight
-  // rows takes 880, 720, 500 and 425 (the epilogue's chain of waits and reads, and for the
+  // rows takes 800, 680, 450 and 320 (the epilogue's chain of waits and reads, and for the
   // narrower ones the copies), a tile's start and store some 2500. Measured with all tiles
-  // of 256 / 192 / 128 / 64 (us, N = K = 7168): M = 256 31 / 26 / 21 / 30, 512 32 / 27 / 33 /
-  // 43, 1000 58 / 48 / 50 / 80, 4096 165 / 172 / 176 / 298.
-  constexpr int kCycles[4] = {425, 500, 720, 880};
+  // of 256 / 192 / 128 / 64 (us, N = K = 7168): M = 256 28 / 26 / 20 / 26, 512 29 / 27 / 31 /
+  // 37, 1000 51 / 47 / 49 / 68, 4096 148 / 168 / 173 / 253.
+  constexpr int kCycles[4] = {320, 450, 680, 800};
   int64_t best = INT64_MAX;
   for (int n = 256; n >= 64; n -= 64) {
     const int64_t cost = cdiv(s.m_tiles * cdiv(N, n), pairs) * (kblocks * kCycles[n / 64 - 1] + 2500);
