@@ -103,6 +103,10 @@ Shape choose(const gemm_shard_plan* P, int64_t N, int64_t kblocks, int shards, c
   s.form = gsr::kFp8Wide;
   s.m_tiles = best_box(wide, shards, rows, &s.box_rows);
   s.boxes = wide / s.box_rows;
+  // One row shard in one tile is split evenly here too, in whole warps' rows. (Boxes that hold
+  // a few rows of 128 and end inside a shard's k-blocks are slow to copy: 136 rows, 8 K-shards
+  // of 7 k-blocks, 25 us against 19.)
+  if (shards == 1 && s.m_tiles == 1) s.box_rows = static_cast<int>(cdiv(cdiv(rows[0], 2), 32) * 32);
   // The tile width by the cycles that its waves take: a k-block of 256, 192, 128 or 64 weight
   // rows takes 800, 680, 450 and 320 (the epilogue's chain of waits and reads, and for the
   // narrower ones the copies), a tile's start and store some 2500. Measured with all tiles
