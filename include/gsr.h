@@ -398,7 +398,8 @@ gsr_status gemm_shard_pack_gather(const gemm_shard_plan *plan, int R, const int6
  *     call. gemm_shard_check_status reads its status word. gemm_group_route and
  *     gemm_group_combine need none.
  *   - Options: GSR_OPT_TIMEOUT_NS and GSR_OPT_MAX_CTAS (in whole CTA pairs, one at
- *     least) apply to the products; the others do not.
+ *     least) apply to the products (not to gemm_expert_layer's own two kernels); the
+ *     others do not.
  *   - Results are reproducible: sums run in an order that depends on the shapes
  *     and the group sizes alone.
  *   - Graphs: the calls may be recorded in a CUDA graph; a replay reads the

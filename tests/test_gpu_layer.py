@@ -248,3 +248,14 @@ def test_a_block_in_a_graph(setup):
         for b, (out, Z) in zip(blocks, want):
             assert torch.equal(b.out, out) and torch.equal(b.Z, Z)
             B.gemm_shard_check_status(b.plan, b.ws)
+
+
+@pytest.mark.parametrize("tokens,graph", [(1, False), (4, True), (37, True)])
+def test_the_example_runs_a_decode_step(tokens, graph):
+    import importlib.util
+    import os
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_block.py")
+    spec = importlib.util.spec_from_file_location("decode_block", at)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    assert mod.main(["--tokens", str(tokens)] + (["--graph"] if graph else [])) == 0
