@@ -32,7 +32,9 @@
 // Measured and dropped: the next k-block's wait and first read before the last sums of this
 // one (no gain with 192 columns, spills with 256); the MMAs issued by one thread for the
 // whole loop (M = 1 13 -> 19 us); a ring of four stages of 256 x 256 (M = 4096 258 us,
-// against 165 with five).
+// against 165 with five); weight tiles of 96 for one tile of up to 256 tokens (M = 256 20.2
+// us, with 128 19.4); the producer's start before the TMEM allocation and the cluster's
+// barrier (M = 512 27 -> 31 us).
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (the pair's leader), warp 2 copies the
 // scales ahead into a ring of their own and warp 3 multiplies them (loaded by the epilogue
@@ -256,8 +258,8 @@ __device__ void produce(const Fp8Params& p, const Table& table, uint32_t base, u
   }
 }
 
-// The pair's MMAs (rank 0). What it waits for last, the accumulator, is on
-// the way from the epilogue's last read to the next MMA.
+// The pair's MMAs (rank 0). What it waits for last, the accumulator, is on the way from the
+// epilogue's last read to the next MMA.
 template <class C>
 __device__ void multiply(const Fp8Params& p, uint32_t base, uint32_t tmem, const Ctl& ctl) {
   const uint32_t full0 = base + C::kBarsOff, empty0 = full0 + 8 * kFp8MaxRing;
@@ -353,9 +355,9 @@ __device__ __forceinline__ void copy_4(uint32_t dst, const float* src, bool real
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
 }
 
-// The scales as they are, by one warp, four k-blocks of the tile's walk over K at a time. Rows that no
-// shard has and positions past the walk's end or that pad a K-shard to whole stages have
-// scale 0 (the sums of the latter are 0).
+// The scales as they are, by one warp, four k-blocks of the tile's walk over K at a time.
+// Rows that no shard has and positions past the walk's end or that pad a K-shard to whole
+// stages have scale 0 (the sums of the latter are 0).
 template <class C>
 __device__ void copy_scales(const Fp8Params& p, Shared<C>& sh, uint32_t base, uint32_t rank, const Ctl& ctl) {
   constexpr int kPer = C::kRows / 32;   // rows of a lane
@@ -501,9 +503,9 @@ __device__ __forceinline__ void load_scales(uint32_t at, float (&s)[4]) {
                : "memory");
 }
 
-// A warp's 32 rows x COLS columns through its staging, 64 or 32 columns at a time
-// in the swizzled layout of the copy (128 or 64 bytes a row: 8 lanes' 16-byte stores meet
-// in no bank), then a copy each, which leave out what lies past the shard's rows and N. They
+// A warp's 32 rows x COLS columns through its staging, 64 or 32 columns at a time in the
+// swizzled layout of the copy (128 or 64 bytes a row: 8 lanes' 16-byte stores meet in no
+// bank), then a copy each, which leave out what lies past the shard's rows and N. They
 // read the staging while the next tile is under way. (Stored straight from the registers,
 // a row per lane, a tile took 2.6 us; with staging for 32 columns alone, 2.)
 template <int COLS, class S>
@@ -625,8 +627,8 @@ __device__ void finish(const Fp8Params& p, const Shared<C>& sh, uint32_t base, u
         int shard, row;
         find_box(p, table.box_begin, (2 * m + static_cast<int>(rank)) * p.boxes + box, shard, row);
         row += row0 - box * p.box_rows;
-        store_tile<C::kCols>(&p.tmap_y[shard], base + C::kStagingOff + (warp - 4) * (64 * fp8_staged_cols(C::TILE_N)), row, col0, p.N,
-                             box < p.boxes && row < table.rows[shard], sums);
+        const uint32_t staging = base + C::kStagingOff + (warp - 4) * (64 * fp8_staged_cols(C::TILE_N));
+        store_tile<C::kCols>(&p.tmap_y[shard], staging, row, col0, p.N, box < p.boxes && row < table.rows[shard], sums);
         continue;
       }
     }

@@ -59,6 +59,9 @@ int64_t pairs_of(const gemm_shard_plan* P) {
   return std::max<int64_t>(1, std::min<int64_t>(cap / 2, P->pair_clusters));
 }
 
+// Of rows and columns: 32-bit coordinates, and one past every shard's rows.
+constexpr int64_t kMostRows = (int64_t(1) << 30) - 256;
+
 struct Shape {
   int form, box_rows, boxes, tile_n;
   int64_t m_tiles, n_tiles;
@@ -71,17 +74,22 @@ int64_t token_tiles(int cta_rows, int box, int shards, const int64_t* rows) {
   return cdiv(boxes, 2 * (cta_rows / box));
 }
 
-// The box that gives the fewest token tiles, of those the largest.
-int64_t best_box(int cta_rows, int shards, const int64_t* rows, int* box) {
-  int64_t best = INT64_MAX;
+// The token tiles of the best box: the fewest, where a box more in a CTA counts as 5 % of a
+// tile (a copy more per k-block) and, in the wide form, boxes that are not of whole warps'
+// rows as 12 % (their tiles are not stored by copies); of equal ones the largest.
+int64_t best_box(int form, int shards, const int64_t* rows, int* box) {
+  const int cta_rows = gsr::fp8_cta_rows(form);
+  int64_t best = INT64_MAX, tiles = 0;
   for (int b = cta_rows; b >= 8; b -= 8) {
     const int64_t t = token_tiles(cta_rows, b, shards, rows);
-    if (t < best) {
-      best = t;
+    const int64_t cost = t * (100 + 5 * (cta_rows / b - 1) + (form == gsr::kFp8Wide && b % 32 ? 12 : 0));
+    if (cost < best) {
+      best = cost;
+      tiles = t;
       *box = b;
     }
   }
-  return best;
+  return tiles;
 }
 
 Shape choose(const gemm_shard_plan* P, int64_t N, int64_t kblocks, int shards, const int64_t* rows) {
@@ -89,7 +97,7 @@ Shape choose(const gemm_shard_plan* P, int64_t N, int64_t kblocks, int shards, c
   const int64_t pairs = pairs_of(P);
   const int narrow = gsr::fp8_cta_rows(gsr::kFp8Narrow), wide = gsr::fp8_cta_rows(gsr::kFp8Wide);
   s.form = gsr::kFp8Narrow;
-  s.m_tiles = best_box(narrow, shards, rows, &s.box_rows);
+  s.m_tiles = best_box(s.form, shards, rows, &s.box_rows);
   if (s.m_tiles == 1) {
     // One row shard is split evenly over the pair.
     if (shards == 1) s.box_rows = static_cast<int>(cdiv(cdiv(rows[0], 2), 8) * 8);
@@ -101,7 +109,7 @@ Shape choose(const gemm_shard_plan* P, int64_t N, int64_t kblocks, int shards, c
     return s;
   }
   s.form = gsr::kFp8Wide;
-  s.m_tiles = best_box(wide, shards, rows, &s.box_rows);
+  s.m_tiles = best_box(s.form, shards, rows, &s.box_rows);
   s.boxes = wide / s.box_rows;
   // One row shard in one tile is split evenly here too, in whole warps' rows. (Boxes that hold
   // a few rows of 128 and end inside a shard's k-blocks are slow to copy: 136 rows, 8 K-shards
@@ -112,14 +120,14 @@ Shape choose(const gemm_shard_plan* P, int64_t N, int64_t kblocks, int shards, c
   // narrower ones the copies), a tile's start and store some 2500. Measured with all tiles
   // of 256 / 192 / 128 / 64 (us, N = K = 7168): M = 256 28 / 26 / 20 / 26, 512 29 / 27 / 31 /
   // 37, 1000 51 / 47 / 49 / 68, 4096 148 / 168 / 173 / 253.
-  constexpr int kCycles[4] = {320, 450, 680, 800};
+  constexpr struct { int n, cycles; } kWidths[] = {{256, 800}, {192, 680}, {128, 450}, {64, 320}};
   int64_t best = INT64_MAX;
-  for (int n = 256; n >= 64; n -= 64) {
-    const int64_t cost = cdiv(s.m_tiles * cdiv(N, n), pairs) * (kblocks * kCycles[n / 64 - 1] + 2500);
+  for (const auto& w : kWidths) {
+    const int64_t cost = cdiv(s.m_tiles * cdiv(N, w.n), pairs) * (kblocks * w.cycles + 2500);
     if (cost < best) {
       best = cost;
-      s.tile_n = n;
-      s.n_tiles = cdiv(N, n);
+      s.tile_n = w.n;
+      s.n_tiles = cdiv(N, w.n);
     }
   }
   return s;
@@ -130,15 +138,16 @@ gsr_status run_fp8(const gemm_shard_plan* P, bool ag, int64_t N, int R, const in
                    const void* const* X, const float* const* SX, const void* const* W, const float* const* SW,
                    void* Y, void* ws, gsr_stream_t stream) {
   const int m_shards = ag ? R : 1, k_shards = ag ? 1 : R;
-  int64_t kblocks = 0;
-  for (int r = 0; r < k_shards; ++r) kblocks += cdiv(K_r[r], kScaleBlock);
-  const Shape s = choose(P, N, kblocks, m_shards, M_r);
-  const int kz = gsr::fp8_kblocks(s.form, s.tile_n);
-  int64_t stages = 0, k_total = 0;
+  int64_t kblocks = 0, k_total = 0;
   for (int r = 0; r < k_shards; ++r) {
-    stages += cdiv(cdiv(K_r[r], kScaleBlock), kz);
+    kblocks += cdiv(K_r[r], kScaleBlock);
     k_total += K_r[r];
   }
+  if (N > kMostRows || k_total > kMostRows) return fail(GSR_ERR_INVALID_VALUE, "N or K is too large");
+  const Shape s = choose(P, N, kblocks, m_shards, M_r);
+  const int kz = gsr::fp8_kblocks(s.form, s.tile_n);
+  int64_t stages = 0;
+  for (int r = 0; r < k_shards; ++r) stages += cdiv(cdiv(K_r[r], kScaleBlock), kz);
   if (s.m_tiles * s.n_tiles > INT32_MAX / 2 || stages > INT32_MAX / 2)
     return fail(GSR_ERR_INVALID_VALUE, "M, N and K give too many tiles");
   const int64_t tiles = s.m_tiles * s.n_tiles;
@@ -223,8 +232,6 @@ gsr_status check_status_ws(const void* ws, size_t ws_bytes) {
     return fail(GSR_ERR_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", ws_bytes, gsr::kWsHeader);
   return ok();
 }
-
-constexpr int64_t kMostRows = (int64_t(1) << 30) - 256;   // a coordinate past every shard's rows
 
 }  // namespace
 

@@ -188,7 +188,10 @@ def test_ar(setup, M, N, K_r):
 
 
 @pytest.mark.parametrize("M,N,K_r", [(1, 7168, [896] * 8), (128, 7168, [896] * 8), (100, 20000, [512]), (1367, 6288, [1008] * 3),
-                                     (4096, 3648, [7168]), (600, 31992, [144] * 16), (64, 264, [32768])])
+                                     (4096, 3648, [7168]), (600, 31992, [144] * 16), (64, 264, [32768]),
+                                     # weight tiles of 128, 192 and 256 rows, one or many a pair
+                                     (200, 9000, [896] * 2), (300, 4000, [400, 640]), (256, 7168, [1792] * 4), (129, 5000, [1040]),
+                                     (512, 7168, [896] * 3), (1000, 7168, [1008]), (2000, 4864, [272]), (2500, 9728, [640, 128])])
 def test_ar_larger(setup, M, N, K_r):
     plan, ws = setup
     X, SX, W, SW = ar_inputs(F.gen(M), M, N, K_r)
@@ -239,6 +242,13 @@ def test_ag(setup, M_r, N, K):
     ref, bound = F.product_ref([x], [F.weights_of(W, SW)])
     F.close(Y, ref, bound)
     assert F.untouched(full, M, torch.ones(M, dtype=torch.bool, device=F.DEV))
+
+
+@pytest.mark.parametrize("M_r,N,K", [([42] * 8, 3648, 1792), ([100] * 16, 6288, 1024), ([33] * 16, 6288, 1024),
+                                     ([1024] * 8, 6288, 640), ([40, 0, 1, 300] * 4, 5000, 1552), ([8] * 16, 7168, 896)],
+                         ids=lambda v: "-".join(map(str, v)) if isinstance(v, list) else str(v))
+def test_ag_larger(setup, M_r, N, K):
+    test_ag(setup, M_r, N, K)
 
 
 def test_products_of_no_rows(setup):
