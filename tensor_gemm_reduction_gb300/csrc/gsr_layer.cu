@@ -69,8 +69,10 @@ __device__ int sort_entries(const LayerParams& p, Sorted& s) {
   int mine = kNone;
   float weight = 0.f;
   if (i < n) {
-    const long long v = p.wide ? reinterpret_cast<const long long*>(p.ids)[i] : reinterpret_cast<const int*>(p.ids)[i];
-    weight = p.weights[i];
+    // Past L1: the second kernel reads them before it has waited for anything itself.
+    const long long v = p.wide ? __ldcg(reinterpret_cast<const long long*>(p.ids) + i)
+                               : __ldcg(reinterpret_cast<const int*>(p.ids) + i);
+    weight = __ldcg(p.weights + i);
     if (v >= 0 && v < p.E) mine = static_cast<int>(v);
   }
   if (i < kLayerEntries) s.id[i] = mine;
