@@ -290,6 +290,33 @@ def test_zero_scales_give_zeros(setup):
     assert not Y.any()
 
 
+@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("K_r", [[1008, 1024], [48, 1040, 2000], [16] * 16], ids=lambda k: "-".join(map(str, k)))
+def test_shards_whose_rows_start_inside_a_sector(setup, M, K_r):
+    """Shards of K = 16 mod 32 beside aligned ones, in one call."""
+    plan, ws = setup
+    X, SX, W, SW = ar_inputs(F.gen(M + len(K_r)), M, 328, K_r)
+    full, Y = F.guarded(M, 328)
+    B.gemm_ar_fp8(plan, X, SX, W, SW, Y, ws)
+    B.gemm_shard_check_status(plan, ws)
+    F.close(Y, *ar_ref(X, SX, W, SW))
+    assert F.untouched(full, M, torch.ones(M, dtype=torch.bool, device=F.DEV))
+
+
+def test_a_row_per_shard(setup):
+    """16 row shards of no or one row: boxes of eight rows, and the empty shards among them."""
+    plan, ws = setup
+    g = F.gen(31)
+    M_r = [1, 0, 1, 1] * 4
+    A, SA = [F.bits8(g, m, 272) for m in M_r], [F.scales(g, 3, m) for m in M_r]
+    W, SW = F.bits8(g, 136, 272), F.scales(g, 2, 3)
+    Y = torch.empty(12, 136, dtype=torch.bfloat16, device=F.DEV)
+    B.gemm_ag_fp8(plan, A, SA, W, SW, Y, ws)
+    B.gemm_shard_check_status(plan, ws)
+    x = torch.cat([F.rows_of(*a) for a in zip(A, SA)])
+    F.close(Y, *F.product_ref([x], [F.weights_of(W, SW)]))
+
+
 @pytest.mark.parametrize("M", [3, 500])
 def test_waits_of_a_nanosecond(M):
     """The shortest limit that a wait can have: the call gives its result or a status, never

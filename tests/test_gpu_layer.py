@@ -153,6 +153,74 @@ def test_values_that_are_not_finite_stay_with_their_tokens(setup):
     assert torch.equal(Y[~odd], want[~odd]) and not Y[odd].isfinite().any()
 
 
+# Entries and experts on either side of the limits up to which the two kernels run.
+BOTH = pytest.mark.parametrize("T,topk,E", [(16, 4, 10), (17, 4, 10)], ids=["in two", "routed"])
+
+
+@BOTH
+def test_y_over_base_or_over_x_in_both_forms(setup, T, topk, E):
+    plan, ws = setup
+    s = inputs(14, T, topk, E, 136, 1096)
+    want = check(setup, s).clone()
+    for name in ("base", "X"):
+        c = dict(s, **{name: s[name].clone()})
+        B.gemm_expert_layer(plan, c["X"], c["ids"], c["weights"], c["W_up"], c["W_down"], c[name], ws, base=c["base"])
+        assert torch.equal(c[name], want)
+
+
+@BOTH
+def test_values_that_are_not_finite_in_both_forms(setup, T, topk, E):
+    """NaN in a token and in dropped entries' weights, infinity in an expert's weights and in
+    an entry's weight: the tokens and columns that use them, and no other."""
+    plan, ws = setup
+    s = inputs(15, T, topk, E, 56, 200, low=0)
+    s["ids"][:, 0] = torch.arange(T, device=U.DEV) % 4
+    s["ids"][:, 1] = 4 + torch.arange(T, device=U.DEV) % 5   # nobody names expert 9
+    s["ids"][:, 2:] = -1
+    s["weights"][:, 2:] = float("nan")
+    want = check(setup, dict(s, weights=s["weights"].nan_to_num())).clone()
+    s["X"][3, 5] = float("nan")
+    s["W_down"][7, 11, 2] = float("inf")
+    s["W_up"][9] = s["W_down"][9] = float("nan")
+    s["weights"][12, 0] = float("inf")
+    Y = torch.empty_like(want)
+    B.gemm_expert_layer(plan, s["X"], s["ids"], s["weights"], s["W_up"], s["W_down"], Y, ws, base=s["base"])
+    odd = torch.zeros(T, 200, dtype=torch.bool, device=U.DEV)
+    odd[3] = odd[12] = True
+    odd[(s["ids"][:, 1] == 7).nonzero()[:, 0], 11] = True
+    assert torch.equal(Y[~odd], want[~odd]) and not Y[odd].isfinite().any()
+
+
+@BOTH
+def test_every_entry_dropped_in_both_forms(setup, T, topk, E):
+    s = inputs(16, T, topk, E, 64, 72)
+    s["ids"].fill_(E)
+    s["weights"].fill_(float("inf"))
+    assert torch.equal(check(setup, s), s["base"])
+
+
+@BOTH
+def test_ids_written_by_the_launch_before(setup, T, topk, E):
+    """Ids, weights and tokens that the kernel right before the call writes, call after call
+    on the same buffers: every call uses its own."""
+    plan, ws = setup
+    s = [inputs(seed, T, topk, E, 64, 264) for seed in range(17, 21)]
+    for c in s:
+        c.update(W_up=s[0]["W_up"], W_down=s[0]["W_down"])
+    want = [check(setup, c).clone() for c in s]
+    buf = {k: torch.empty_like(s[0][k]) for k in ("ids", "weights", "X", "base")}
+    out = [torch.empty_like(s[0]["X"]) for _ in range(40)]
+    call = [B.prepare_expert_layer(plan, buf["X"], buf["ids"], buf["weights"], s[0]["W_up"], s[0]["W_down"], y, ws,
+                                   base=buf["base"]) for y in out]
+    for i, y in enumerate(out):
+        for k in ("base", "X", "weights", "ids"):
+            buf[k].copy_(s[i % 4][k])
+        call[i]()
+    torch.cuda.synchronize()
+    for i, y in enumerate(out):
+        assert torch.equal(y, want[i % 4]), i
+
+
 def test_equals_the_four_routed_calls(setup):
     """The layer and route, gated, grouped, combine on the same inputs: both near the
     64-bit values, with the same experts read."""
