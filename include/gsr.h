@@ -498,7 +498,7 @@ gsr_status gemm_group_combine(const gemm_shard_plan *plan, int64_t T, int topk, 
  *   T, topk   tokens and entries of each: T <= GSR_MAX_LAYER_TOKENS, T * topk <=
  *             GSR_MAX_LAYER_ENTRIES and max_M; T == 0 returns GSR_OK with no launch
  *   E, N, K   experts, their inner and the outer width: multiples of 8, at most max_N and
- *             max_K
+ *             max_K and 2^20, 2 N K below 2^38
  *   ids       device, T x topk integers of id_bytes (4 or 8) bytes; a value outside
  *             0..E-1 drops the entry, whatever its weight holds. A token may name an
  *             expert twice.

@@ -141,6 +141,15 @@ void fill_routed(gsr::RoutedParams& p, const gemm_shard_plan* P, int64_t M, int6
   p.partials = reinterpret_cast<float*>(w + kPartialsAt);
 }
 
+// A grouped product's tiles along N, and the limits of its tiles and of a group's matrix.
+int64_t grouped_n_tiles(int kind, int64_t N) { return cdiv(N, kind == gsr::kGated ? 128 : 256); }
+gsr_status check_grouped_size(int kind, int E, int64_t M, int64_t N, int64_t K) {
+  const int64_t wide = kind == gsr::kGated ? 2 * N : N;
+  if (wide * K >= (int64_t(1) << 38) || (cdiv(M, 64) + E) * grouped_n_tiles(kind, N) > INT32_MAX / 2)
+    return fail(GSR_ERR_INVALID_VALUE, "M, N, K and E give too many tiles or too large a matrix");
+  return ok();
+}
+
 gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int64_t N, int64_t K,
                        const int32_t* offsets, int64_t T, const void* X, const int32_t* rows,
                        const void* W, void* Y, void* ws, size_t ws_bytes, gsr_stream_t stream) {
@@ -165,10 +174,9 @@ gsr_status run_grouped(const gemm_shard_plan* P, int kind, int E, int64_t M, int
   if (!W || !aligned16(W)) return fail(GSR_ERR_INVALID_VALUE, "W must be non-NULL and 16-byte aligned");
   if ((M > 0 && (!X || !Y)) || !aligned16(X) || !aligned16(Y))
     return fail(GSR_ERR_INVALID_VALUE, "X and Y must be non-NULL and 16-byte aligned");
-  const int64_t wide = kind == gsr::kGated ? 2 * N : N;
-  const int64_t n_tiles = cdiv(N, kind == gsr::kGated ? 128 : 256);
-  if (wide * K >= (int64_t(1) << 38) || (cdiv(M, 64) + E) * n_tiles > INT32_MAX / 2)
-    return fail(GSR_ERR_INVALID_VALUE, "M, N, K and E give too many tiles or too large a matrix");
+  s = check_grouped_size(kind, E, M, N, K);
+  if (s) return s;
+  const int64_t wide = kind == gsr::kGated ? 2 * N : N, n_tiles = grouped_n_tiles(kind, N);
   s = check_routed_ws(P, ws, ws_bytes);
   if (s) return s;
   if (M == 0) return ok();
@@ -379,6 +387,10 @@ gsr_status gemm_expert_layer(const gemm_shard_plan* P, int64_t T, int topk, int 
     return fail(GSR_ERR_INVALID_VALUE, "W_up and W_down must be non-NULL and 16-byte aligned");
   if (!aligned16(X) || !aligned16(base) || !aligned16(Y))
     return fail(GSR_ERR_INVALID_VALUE, "X, base and Y must be 16-byte aligned");
+  // Both products' limits, before the first launch, and for either form alike.
+  s = check_grouped_size(gsr::kGated, E, T * topk, N, K);
+  if (!s) s = check_grouped_size(gsr::kGrouped, E, T * topk, K, N);
+  if (s) return s;
   s = check_routed_ws(P, ws, ws_bytes);
   if (s) return s;
   if (T == 0) return ok();

@@ -70,3 +70,26 @@ def test_binding_refuses_wrong_tensors(host):
     with pytest.raises(ValueError, match="X must be"):
         B.gemm_expert_layer(plan, t(2, 64), t(2, 3, dtype=torch.int32), t(2, 3, dtype=torch.float32), t(4, 16, 64),
                             t(4, 64, 8), t(2, 64), t(1))
+
+
+@pytest.mark.parametrize("T", [8, 64], ids=["in two", "routed"])
+def test_widths_too_large_for_the_products_are_refused_before_a_launch(host, T):
+    """A matrix that the layer's own products refuse is refused by the layer, by its two
+    kernels as by the routed ones, which would have written the workspace by then."""
+    lib, _ = host
+    side = 1 << 19
+    plan = B.gemm_shard_plan_create_host(152, 4096, 2 * side, 2 * side, 1)
+    size = B.gemm_routed_workspace_size(plan)
+
+    def call(N, K):
+        return lib.gemm_expert_layer(plan.handle, T, 8, 8, N, K, vp(0x1000), 4, vp(0x2000), vp(0x3000), vp(0x4000),
+                                     vp(0x5000), None, vp(0x6000), vp(WS), size, None)
+    for N, K in [(side, side), (2 * side, side // 8), (8, 2 * side), (2 * side, 8)]:
+        grouped = [fn(plan.handle, 8, 8 * T, n, k, vp(0x1000), 8 * T, vp(0x10000), None, vp(0x20000), vp(0x30000), vp(WS),
+                      size, None) for fn, n, k in ((lib.gemm_grouped_gated, N, K), (lib.gemm_grouped, K, N))]
+        if N * K * 2 < 1 << 38:
+            assert grouped == [B.GSR_ERR_UNSUPPORTED] * 2
+            refused(call(N, K), B.GSR_ERR_UNSUPPORTED, "arguments are valid")
+        else:
+            assert B.GSR_ERR_INVALID_VALUE in grouped
+            refused(call(N, K), B.GSR_ERR_INVALID_VALUE, "too large a matrix")
