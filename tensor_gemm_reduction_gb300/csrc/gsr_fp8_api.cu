@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 
@@ -253,7 +254,7 @@ gsr_status gemm_shard_rms_norm(const gemm_shard_plan* P, int64_t M, int64_t H, c
     return fail(GSR_ERR_INVALID_VALUE, "H=%lld must be a positive multiple of 8, at most %lld", (long long)H,
                 (long long)most);
   if (Q && H % 16) return fail(GSR_ERR_INVALID_VALUE, "H=%lld must be a multiple of 16 for Q", (long long)H);
-  if (!(eps >= 0.f) || eps > 3.0e38f) return fail(GSR_ERR_INVALID_VALUE, "eps must be finite and >= 0");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GSR_ERR_INVALID_VALUE, "eps must be finite and >= 0");
   if (M > 0 && !X) return fail(GSR_ERR_INVALID_VALUE, "X must not be NULL");
   if (M > 0 && !sum && !Y && !Q) return fail(GSR_ERR_INVALID_VALUE, "no output: sum, Y and Q are NULL");
   if (M > 0 && (Q != nullptr) != (scale != nullptr))

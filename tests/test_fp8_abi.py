@@ -157,3 +157,10 @@ for M in (1, 128, 129):
     lines = r.stderr.splitlines()
     assert len(lines) == 3 and all("ar_fp8 N=7168 K=7168 R=1 kernel=fp8" in x for x in lines)
     assert "form=narrow tile_n=96 boxes=1x8" in lines[0] and "boxes=1x64" in lines[1] and "form=wide" in lines[2]
+
+
+def test_norm_takes_every_finite_eps(host):
+    lib, plan = host
+    for eps in (0.0, 2.0 ** -149, 1.0, 3.2e38, 2.0 ** 128 - 2.0 ** 104):   # the last: the largest fp32
+        refused(lib.gemm_shard_rms_norm(plan.handle, 1, 64, vp(0x1000), None, None, eps, None, vp(0x2000), None, None,
+                                        None), B.GSR_ERR_UNSUPPORTED, "arguments are valid")
