@@ -554,8 +554,11 @@ gsr_status gemm_ar_lora(const gemm_shard_plan *plan, int64_t M, int64_t N, int R
  *     blocks of 128 x 128; a last group may be short. A K-shard starts its own.
  *   - Scales of rows are stored by column block: element (b, m) of a dense
  *     ceil(K / 128) x M array belongs to columns 128 b .. of row m. Scales of blocks
- *     are row-major, ceil(N / 128) x ceil(K / 128). Pointers 4-byte aligned. Any
- *     fp32 values are allowed.
+ *     are row-major, ceil(N / 128) x ceil(K / 128). Pointers 4-byte aligned. A product
+ *     takes a row's scale times a block's in fp32 before it meets the block's sum, so the
+ *     two may be any fp32 values whose product is a normal number or 0. Past the largest
+ *     number the product is an infinity (and NaN with a sum of 0), below 2^-126 it has
+ *     the bits that fp32 has left there.
  *   - K, K_r (and H with Q) are multiples of 16.
  *   - Quantising a group of values v: scale = max(max|v| / 448, 2^-126), q = v * (1 /
  *     scale) to the nearest e4m3, ties to even, at most 448 in magnitude. A group

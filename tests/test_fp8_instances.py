@@ -1,5 +1,5 @@
-"""Every kernel instance of the 8-bit products by name of its tile, and results whose
-bits do not depend on the tiles or on the CTAs.
+"""Every kernel instance of the 8-bit products by name of its tile, results whose bits do
+not depend on the tiles or on the CTAs, and scales at the ends of fp32's range.
 
 The bound of fp8_util on a sum (2^-17 of sum |x w|) at the K here and at K = 32768: a sum is
 made of at most 128 additions within a block and one per block of 128 columns, so 128 + 256
@@ -8,6 +8,7 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
@@ -163,3 +164,69 @@ def test_ar_has_the_same_bits_on_one_pair(setup, one_pair, M, N, K_r):
 def test_ag_has_the_same_bits_on_one_pair(setup, one_pair, M_r, N, K):
     s = ag_inputs(N, M_r, N, K)
     assert torch.equal(ag(setup, *s), ag(one_pair, *s))
+
+
+# ---------------------------------------------------------------- scales far from 1
+
+# An instance of each kind of sums: narrow, wide in pairs, wide with 128 sums a thread.
+FAR = pytest.mark.parametrize("M,N,K_r", [(40, 520, [272, 256]), (300, 4000, [400, 640]), (600, 5000, [1040])], ids=str)
+
+
+@gpu
+@FAR
+def test_large_scales_beside_small_ones(setup, M, N, K_r):
+    """Factors of 2^100 of one operand's scales and 2^-100 of the other's: the scales'
+    products are the same numbers, so the result has the same bits."""
+    X, SX, W, SW = ar_inputs(N, M, N, K_r)
+    want = ar(setup, X, SX, W, SW)
+    for r in range(len(K_r)):
+        for b in range(SX[r].shape[0]):
+            power = 100 if (r + b) % 2 else -100
+            SX[r][b] *= 2.0 ** power
+            SW[r][:, b] *= 2.0 ** -power
+    assert torch.equal(ar(setup, X, SX, W, SW), want)
+
+
+@gpu
+@FAR
+def test_scales_whose_product_passes_the_largest_number(setup, M, N, K_r):
+    """The product of the two is an infinity, so the elements that use it are not finite,
+    NaN where the block's sum is 0; the elements beside them are what they were."""
+    X, SX, W, SW = ar_inputs(N, M, N, K_r)
+    X[0].view(torch.uint8)[11, 128:256] = 0   # a row with a sum of 0
+    SW[0][2, 1] = 2.0
+    want = ar(setup, X, SX, W, SW)
+    SW[0][2, 1] *= 2.0 ** 99                  # of columns 256 .. 383 of the result
+    SX[0][1] *= 2.0 ** -99
+    SX[0][1, 11] = SX[0][1, 13] = 2.0 ** 30
+    Y = ar(setup, X, SX, W, SW)
+    rows = torch.zeros(M, dtype=torch.bool, device=F.DEV)
+    rows[11] = rows[13] = True
+    assert Y[11, 256:384].isnan().all() and not Y[13, 256:384].isfinite().any()
+    assert torch.equal(Y[~rows, 256:384], want[~rows, 256:384])
+    assert Y[rows, :256].isfinite().all() and Y[rows, 384:].isfinite().all()
+
+
+@gpu
+@FAR
+def test_scales_whose_product_has_few_bits_left(setup, M, N, K_r):
+    """Products of scales below 2^-126 are fp32's subnormal numbers, below 2^-150 0: the
+    result is that of these numbers. Every addition may be off by half the smallest number
+    (2^-150) besides its relative error, the output by half of bf16's (2^-134)."""
+    X, SX, W, SW = ar_inputs(N, M, N, K_r)
+    ref, mag, blocks = 0.0, 0.0, 0
+    for r, k in enumerate(K_r):
+        SX[r] *= 2.0 ** -66
+        SW[r] *= 2.0 ** -66
+        for b in range(F.blocks(k)):
+            sx, sw = SX[r][b].cpu().numpy(), SW[r][:, b].cpu().numpy()
+            p = np.float32(sx)[:, None] * np.float32(sw)[None, :]
+            assert p.dtype == np.float32 and (p < 2.0 ** -126).any()
+            p = torch.from_numpy(p.astype(np.float64)).to(F.DEV).repeat_interleave(128, 1)[:, :N]
+            x, w = X[r][:, 128 * b:128 * b + 128].double(), W[r][:, 128 * b:128 * b + 128].double()
+            ref = ref + p * (x @ w.t())
+            mag = mag + p * (x.abs() @ w.abs().t())
+            blocks += 1
+    Y = ar(setup, X, SX, W, SW)
+    assert bool((ref.abs() > 2.0 ** -126).any())
+    F.close(Y, ref, F.ROUND * ref.abs() + F.SUM * mag + (blocks + 1) * 2.0 ** -150 + 2.0 ** -134)
