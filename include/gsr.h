@@ -583,7 +583,9 @@ gsr_status gemm_ar_lora(const gemm_shard_plan *plan, int64_t M, int64_t N, int R
  *   sum       M x H bf16 out: h, or NULL
  *   Y         M x H bf16 out: y, or NULL
  *   Q, scale  M x H e4m3 and ceil(H / 128) x M fp32 out: y in 8 bits, or both NULL
- * One output at least. Everything is fp32 in between; sum, Y and Q are each rounded
+ * One output at least. Everything is fp32 in between, the squares' sum too: a row of
+ * finite h where it passes the largest number has y = 0, and where it vanishes, with eps
+ * 0, y is infinite (NaN for h = 0). sum, Y and Q are each rounded
  * once from the unrounded values. sum and Y may each be X or residual itself (not one
  * another's buffer); otherwise the outputs overlap nothing.
  */

@@ -474,3 +474,29 @@ def test_tensors_past_2_to_the_31(setup):
     B.gemm_ar_fp8(plan, [Q], [T], [W], [SW], Y, ws)
     B.gemm_shard_check_status(plan, ws)
     F.close(Y[at], *F.product_ref([F.rows_of(Q[at], T[:, at])], [F.weights_of(W, SW)]))
+
+
+@pytest.mark.parametrize("M,H", [(20, 1040), (200, 1040), (12, 8208)])
+def test_norm_of_rows_whose_squares_leave_fp32(setup, M, H):
+    """Finite rows whose squares sum up past the largest number or vanish, as documented;
+    the sum is theirs, and every other row keeps its bits."""
+    plan, _ = setup
+    X = F.normal(F.gen(41), M, H)
+    clean = X.clone()
+    X[7], X[8], X[9] = (X[7].float() * 2.0 ** 83).bfloat16(), (X[8].float() * 2.0 ** -85).bfloat16(), 0
+    X[8][X[8] == 0] = 2.0 ** -85
+    out = []
+    for x in (X, clean):
+        S, Y = torch.empty_like(x), torch.empty_like(x)
+        Q, T = torch.empty(M, H, dtype=F.E4M3, device=F.DEV), torch.empty(F.blocks(H), M, device=F.DEV)
+        B.gemm_shard_rms_norm(plan, x, None, 0.0, sum=S, Y=Y, Q=Q, scale=T)
+        assert torch.equal(S, x)
+        out.append((Y, Q.view(torch.uint8), T.t()))
+    rows = torch.ones(M, dtype=torch.bool, device=F.DEV)
+    rows[7:10] = False
+    for a, b in zip(*out):
+        assert torch.equal(a[rows], b[rows])
+    Y, Q, T = out[0]
+    assert not Y[7].any() and not (Q[7] & 0x7F).any() and (T[7] == F.TINY).all()
+    assert Y[8].isinf().all() and (T[8] == float("inf")).all()
+    assert Y[9].isnan().all() and T[9].isnan().all()
