@@ -414,7 +414,10 @@ gsr_status gemm_shard_pack_gather(const gemm_shard_plan *plan, int R, const int6
 #define GSR_MAX_LAYER_TOKENS 64    /* T of gemm_expert_layer                   */
 #define GSR_MAX_LAYER_ENTRIES 1024 /* its T * topk                             */
 
-/* Bytes of workspace for every routed call under the plan; 0 for a NULL plan. */
+/* Bytes of workspace for every routed call under the plan; 0 for a NULL plan. One size
+ * serves them all: it holds gemm_expert_layer's rows too, 4 * min(max_M,
+ * GSR_MAX_LAYER_ENTRIES) * max_N bytes, so a plan for routed calls takes the max_N that
+ * these need and a plan of its own serves a wider projection. */
 size_t gemm_routed_workspace_size(const gemm_shard_plan *plan);
 
 /* Zero its status word and counters (stream-ordered), once after allocating it

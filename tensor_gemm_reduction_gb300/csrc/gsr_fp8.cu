@@ -6,15 +6,16 @@
 // over the blocks b of 128 columns of every K-shard, x and w in e4m3. The inner sums
 // run on the tensor cores (tcgen05.mma kind::f8f6f4, fp32), a block in a fresh
 // accumulator; the epilogue warps multiply each block's sums by its scales and add
-// them up in fp32 registers: the scales are any fp32 numbers, so they cannot go into
+// them up in fp32 registers: the scales are fp32 numbers, so they cannot go into
 // the tensor cores' own block scales (powers of two).
 //
 // So that a scale is one number per thread, the tokens are the MMA's M: a TMEM lane is
 // a token row, and a warp's columns lie in two blocks of weight rows at most. A CTA
 // pair owns a tile of tokens x tile_n weight rows over the whole of K:
-// - kFp8Wide: 256 tokens (128 per CTA) x up to 256, a k-block per ring stage. A CTA's
-//   128 x 256 sums are 128 registers of each of its 256 epilogue threads, and two
-//   accumulators fill the TMEM: while the tensor cores fill one, the other is read.
+// - kFp8Wide: 256 tokens (128 per CTA) x up to 256. A CTA's 128 x 256 sums are 128
+//   registers of each of its 256 epilogue threads. A ring stage is a k-block for tiles of
+//   192 and 256 weight rows, two for those of up to 128, and the TMEM holds two stages'
+//   accumulators: while the tensor cores fill one stage's, the other's are read.
 // - kFp8Narrow: up to 128 tokens x up to 128, a stream of weights. The pair MMA of 128
 //   rows keeps a CTA's 64 rows twice over in TMEM: lanes 64..127 hold the second half
 //   of the columns. A stage is four k-blocks, each with an accumulator of its own, so
@@ -26,7 +27,8 @@
 // What bounds it. Wide: a k-block's MMAs take 512 cycles (256 x 256), but the epilogue's chain
 // of a k-block, two waits, four reads of TMEM at about 100 cycles each and the sums, some
 // 800; without it the copies would take 700 (L2). M = 4096, N = K = 7168 150 us, 2.8 PFLOP/s
-// (two thirds of the time the tensor cores are busy, as ncu counts them); M = 16384 584 us.
+// (61 % of the time the tensor cores are busy, as ncu counts them at M = 2048); M = 16384 586
+// us. (Of the instances this one alone spills: 12 bytes stored and 48 loaded a thread.)
 // Narrow: W from memory, 51 MB at N = K = 7168 in 7.6 us, and the launch, the first data and
 // the way out, about 5.5: M = 1 13.3 us, M = 128 14.5.
 // Measured and dropped: the next k-block's wait and first read before the last sums of this

@@ -25,8 +25,8 @@
 //
 // One token, 8 of 64 experts, N = 896, K = 7168: 308 MB of weights, 45 us at the copy
 // bandwidth; 51 back to back (by themselves and cold, the kernels read 5.3 and 4.2 TB/s:
-// a launch, the sort and the first data before each stream). Streams of 1.4 GB (16 tokens)
-// ran at 0.96.
+// a launch, the sort and the first data before each stream). 4 tokens (24 experts, 925 MB)
+// 146 us and 8 (42, 1618 MB) 255, 0.93 and 0.94 of it.
 //
 // The second kernel starts while the first one ends (programmatic dependent launch),
 // sorts its entries and prefetches its first weights into L2 before it waits for h.
@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(kThreadsL, kResident) gsr_layer_down_kernel(co
       }
     if (ctas > 1) cluster_sync();   // read by the first CTA before the next tile
   }
-  // Not earlier: with the next call's first kernel resident and waiting beside this one, 16
-  // tokens took 395 us, and 324 without.
+  // Not earlier: the next call's first kernel would be resident and wait beside this one,
+  // which gains nothing (4 tokens of 8 entries 146 us, released early 147; 8 255 / 254).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
