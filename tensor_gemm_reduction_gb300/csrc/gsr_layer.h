@@ -19,7 +19,7 @@ constexpr int kLayerMost = 1024;        // T * topk, at most
 // (Sizes alone do not tell the sides apart everywhere: 64 of 8 at the smaller widths lose 3 us.)
 // The routed form's down products leave their kernel as rows of bf16, as every product's
 // rows do, before the combine weights them in fp32: one rounding more. Relative error
-// against 64 bits 0.0017 in two kernels, 0.0018 to 0.0019 in the routed ones.
+// against 64 bits 0.0017 to 0.0018 in two kernels, 0.0018 to 0.0019 in the routed ones.
 constexpr int kLayerEntries = 64, kLayerPerExpert = 8;
 inline bool layer_in_two(int64_t entries, int E) {
   return entries <= kLayerEntries && entries <= static_cast<int64_t>(kLayerPerExpert) * E;
